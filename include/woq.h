@@ -408,6 +408,103 @@ int64_t woq_qgemm_int4o_splitk_workspace(int64_t N, int64_t b, int32_t splits);
 int woq_qgemm_int4o_splitk_noalloc(const woq_int4o_w* w, const uint16_t* xp, int64_t b, uint16_t* y, int64_t ldy,
                                    int32_t splits, void* stream);
 
+/* ------------------------------------------------- device ops: 8-bit rows */
+
+/*
+ * The residual's addition, the RMS norm and the 8-bit rows that stand between
+ * two products, in one pass.  For every row r < b, in fp32:
+ *   s[k] = x[r, k] + res[r, k]                     (res null: s = x)
+ *   v[k] = s[k] * (weight[k] + offset) / sqrt(mean_k s[k]^2 + eps)
+ *                                                  (weight null: v = s)
+ * and, where the pointer is not null (at least one must be given),
+ *   sum_out[r, k] = fp16(s[k])      the residual stream for the next layer,
+ *   y[r, k]       = fp16(v[k])      the fp16 input of a product,
+ *   q[r, k], q_scale[r]             the 8-bit input of woq_qgemm_int8_a8: the
+ *                                   INT8 scheme of woq_quantize_int8 over the
+ *                                   row, q_scale = fp32(max_k |v| / 127),
+ *                                   q = clamp(rne(fp32(v / q_scale)), +-127).
+ * s and v are never rounded to fp16 on the way.  A row of zeros gives q_scale
+ * 0 and codes 0; a row that holds a NaN or an infinity gives q_scale NaN and
+ * codes 0 (so a product of it is NaN).  weight is fp16 [K]; offset is added
+ * to it in fp32 (1 for models that store the gain minus one, else 0); eps > 0.
+ * Without a weight nothing is normalised: the addition and the 8-bit rows
+ * alone, for inputs that no norm precedes (eps and offset are then ignored;
+ * codes and scale are those of woq_quantize_int8 on the row, bit for bit).
+ * fp16 rows are 16-byte aligned with leading dimensions that are multiples of
+ * 8 and >= K; values past K are neither read nor written.  q is 16-byte
+ * aligned, ldq a multiple of 16 and >= K; each row's codes are followed by
+ * zeros up to a multiple of 16, so every row (the last too) must hold
+ * round_up(K, 16) bytes.  sum_out may be res or x, and y may be x, with the
+ * same leading dimension; other overlaps are not allowed.  K <= WOQ_NORM_MAX_K.
+ * b = 0 is a no-op.
+ */
+#define WOQ_NORM_MAX_K 65536
+int woq_add_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* res, int64_t ldres, const uint16_t* weight,
+                    float offset, float eps, int64_t b, int64_t K, uint16_t* sum_out, int64_t ldsum, uint16_t* y,
+                    int64_t ldy, int8_t* q, int64_t ldq, float* q_scale, void* stream);
+
+/*
+ * y[r, n] = fp16(scale(n) * xs[r] * sum_k code[n, k] * xq[r, k]) for r < b,
+ * n < N: an INT8 weight with INT8 activation rows (woq_add_rmsnorm), on the
+ * int8 matrix cores.  The integer sum is exact in int32 (so the result does
+ * not depend on the tiling); the scales multiply it in fp32.  Any number of
+ * rows, a decode batch or a packed prompt (woq_qgemv_int8 stops at 8).
+ * xq int8 [b, ldq], 16-byte aligned, ldq a multiple of 16 and >= K; every row
+ * must hold round_up(K, 16) bytes (bytes past K are read but meet code 0);
+ * codes of -128 are allowed.  xs fp32 [b]; y fp16 [b, ldy], ldy >= N, not
+ * overlapping the inputs.  K <= WOQ_A8_MAX_K, so that no sum leaves int32.
+ * b = 0 is a no-op.
+ */
+#define WOQ_A8_MAX_K 131072
+int woq_qgemm_int8_a8(const woq_int8_w* w, const int8_t* xq, int64_t ldq, const float* xs, int64_t b, uint16_t* y,
+                      int64_t ldy, void* stream);
+
+/* ---------------------------------------------- device ops: adapters */
+
+/*
+ * A pool of `count` low-rank adapters of one (possibly N-stacked) linear, in
+ * device memory: adapter a adds scale[a] * B[a] (A[a] x) to the linear's
+ * output.  A fp16 [count][nseg * R][lda] (lda a multiple of 8 and >= K) holds
+ * the rows that meet x, R for each segment of N (linears stacked along N, as
+ * q|k|v, have an A each); B fp16 [count][N][R].  Output rows of N in segment i,
+ * [seg_end[i-1], seg_end[i]), use rows i * R .. i * R + R - 1 of A.  scale is
+ * fp32 [count].  rank (int32 [count] in device memory, or null: all R) gives
+ * each adapter's own rank: inner products j >= rank[a] count as absent
+ * whatever A and B hold there; values outside [0, R] are clamped.  A and B are
+ * 16-byte aligned.  R is a multiple of 8, at most WOQ_LORA_MAX_R.
+ */
+#define WOQ_LORA_MAX_R 256
+typedef struct {
+    const uint16_t* A;
+    const uint16_t* B;
+    const float* scale;
+    const int32_t* rank;
+    int64_t N, K, lda;
+    int32_t R, count, nseg;
+    int64_t seg_end[WOQ_MAX_SEGMENTS];
+} woq_lora_w;
+
+/*
+ * The adapters of many requests beside one shared projection: for r < b, n < N
+ *   y[r, n] = fp16(base[r, n] + scale[a] * sum_{j < rank[a]} B[a][n, j] h[r, j])
+ *   h[r, j] = sum_k A[a][seg(n) * R + j, k] * x[r, k],        a = ids[r],
+ * accumulated in fp32; base is the projection's output (null: zeros).  ids
+ * int32 [b] in device memory names each row's adapter; a row whose id lies
+ * outside [0, count) has none: y = base.  Rows of one adapter may stand
+ * anywhere, so a decode batch of mixed requests and a packed prompt are the
+ * same call.  x fp16 [b, ldx], 16-byte aligned, ldx a multiple of 8 and >= K
+ * (values past K are not used); base fp16 [b, ldbase] and y fp16 [b, ldy] with leading
+ * dimensions >= N; y may be base (same leading dimension).  workspace: at
+ * least woq_lora_workspace(w, b) bytes of device memory, 16-byte aligned,
+ * owned by the caller, its contents on return unspecified; calls that share
+ * it must not overlap.  Deterministic.  b = 0 is a no-op.
+ * woq_lora_workspace returns a negative status for a bad descriptor or batch.
+ */
+int woq_lora_add(const woq_lora_w* w, const uint16_t* x, int64_t ldx, const int32_t* ids, int64_t b,
+                 const uint16_t* base, int64_t ldbase, uint16_t* y, int64_t ldy, void* workspace,
+                 int64_t workspace_bytes, void* stream);
+int64_t woq_lora_workspace(const woq_lora_w* w, int64_t b);
+
 /* --------------------------------------------------------- layer stack */
 
 #define WOQ_FMT_INT8  1

@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(_PKG, "libwoq.so")
 WOQ_OK, WOQ_EINVAL, WOQ_EALIGN, WOQ_ENOMEM, WOQ_EHIP, WOQ_EUNSUPPORTED, WOQ_ERANGE = 0, -1, -2, -3, -4, -5, -6
 WOQ_EIO, WOQ_EFORMAT = -8, -9
 MAX_SEGMENTS = 8
+NORM_MAX_K, A8_MAX_K, LORA_MAX_R = 65536, 131072, 256
 
 
 class WoqError(RuntimeError):
@@ -57,6 +58,12 @@ class StackStep(ctypes.Structure):
 
 class PagerStep(ctypes.Structure):
     _fields_ = [("code_offset", c_int64), ("w", Int8W)]
+
+
+class LoraW(ctypes.Structure):
+    _fields_ = [("A", c_void_p), ("B", c_void_p), ("scale", c_void_p), ("rank", c_void_p), ("N", c_int64),
+                ("K", c_int64), ("lda", c_int64), ("R", c_int32), ("count", c_int32), ("nseg", c_int32),
+                ("seg_end", c_int64 * MAX_SEGMENTS)]
 
 
 FMT_INT8, FMT_INT4O = 1, 2
@@ -97,6 +104,12 @@ _SIGS = {
     "woq_qgemm_int4o_x": (c_int, [POINTER(Int4oW), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
                                   c_void_p]),
     "woq_qgemm_int4o_x_supported": (c_int, [POINTER(Int4oGeom), c_int64, c_int64]),
+    "woq_add_rmsnorm": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_float, c_float, c_int64, c_int64,
+                                c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p]),
+    "woq_qgemm_int8_a8": (c_int, [POINTER(Int8W), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p]),
+    "woq_lora_add": (c_int, [POINTER(LoraW), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                             c_int64, c_void_p, c_int64, c_void_p]),
+    "woq_lora_workspace": (c_int64, [POINTER(LoraW), c_int64]),
     "woq_stack_create": (c_int, [POINTER(StackStep), c_int32, c_int64, POINTER(c_void_p)]),
     "woq_stack_run": (c_int, [c_void_p, POINTER(c_void_p), POINTER(c_void_p), c_int64, c_void_p]),
     "woq_stack_launches": (c_int, [c_void_p, c_int64, POINTER(c_int32)]),
@@ -465,6 +478,105 @@ def woq_qgemm_int4o(w: Int4oW, xp, y, stream=None, b: int | None = None):
     return y
 
 
+# ------------------------------------- device ops: 8-bit rows and adapters
+
+def _rows(t, what: str, dtype: str, b: int, width: int):
+    """(address, leading dimension) of a row-major device buffer that must
+    hold b rows of ``width`` values; rows may be apart (t.stride(0))."""
+    if str(t.dtype) != dtype or t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{what}: expected a 2-D {dtype} tensor on the GPU")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if rows < b or cols < width or (step != 1 and cols > 1):
+        raise ValueError(f"{what}: needs {b} rows of {width} adjacent values, got {tuple(t.shape)} with strides "
+                         f"{(ld, step)}")
+    if rows <= 1:
+        ld = max(ld, -(-cols // 16) * 16)     # of a single row the stride says nothing
+    return t.data_ptr(), ld
+
+
+def _vector(t, what: str, dtype: str, n: int):
+    """Address of a contiguous device vector of at least n values."""
+    if str(t.dtype) != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of {n} values on the GPU")
+    return t.data_ptr()
+
+
+def _call(name: str, stream, first, others, *args):
+    """Call the C entry point on ``stream``, or on the current stream of the
+    device that holds the tensors, with that device current."""
+    import torch
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
+    fn = getattr(_lib(), name)
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)), name)
+
+
+def woq_add_rmsnorm(x, weight, eps: float, res=None, sum_out=None, y=None, q=None, q_scale=None,
+                    offset: float = 0.0, K: int | None = None, stream=None, b: int | None = None):
+    """Add ``res`` to ``x`` (fp16 [b, >= K]), normalise by the root mean square
+    and the gain ``weight`` (fp16 [K]; None: no norm, then K defaults to x's
+    width) and write any of: the sum (fp16), y (fp16), the 8-bit rows q (int8
+    [b, >= round_up(K, 16)]) with their scales q_scale (fp32 [b])."""
+    b = x.shape[0] if b is None else b
+    if K is None:
+        K = x.shape[1] if weight is None else weight.shape[0]
+    if (q is None) != (q_scale is None):
+        raise ValueError("q and q_scale go together")
+    half, nothing = "torch.float16", (None, 0)
+    xp = _rows(x, "x", half, b, K)
+    rp = nothing if res is None else _rows(res, "res", half, b, K)
+    sp = nothing if sum_out is None else _rows(sum_out, "sum_out", half, b, K)
+    yp = nothing if y is None else _rows(y, "y", half, b, K)
+    qp = nothing if q is None else _rows(q, "q", "torch.int8", b, -(-K // 16) * 16)
+    _call("woq_add_rmsnorm", stream, x, (weight, res, sum_out, y, q, q_scale), *xp, *rp,
+          None if weight is None else _vector(weight, "weight", half, K), offset, eps, b, K, *sp, *yp, *qp,
+          None if q is None else _vector(q_scale, "q_scale", "torch.float32", b))
+
+
+def woq_qgemm_int8_a8(w: Int8W, xq, xs, y, stream=None, b: int | None = None):
+    """y (fp16 [b, >= N]) = an INT8 weight times the 8-bit rows xq (int8 [b, >=
+    round_up(K, 16)]) with their scales xs (fp32 [b]), as woq_add_rmsnorm
+    writes them."""
+    b = xq.shape[0] if b is None else b
+    xp, ldq = _rows(xq, "xq", "torch.int8", b, -(-w.K // 16) * 16)
+    yp, ldy = _rows(y, "y", "torch.float16", b, w.N)
+    _call("woq_qgemm_int8_a8", stream, xq, (xs, y), ctypes.byref(w), xp, ldq,
+          _vector(xs, "xs", "torch.float32", b), b, yp, ldy)
+    return y
+
+
+def woq_lora_workspace(w: LoraW, b: int) -> int:
+    """Bytes of the workspace of woq_lora_add for batches of b rows."""
+    n = _lib().woq_lora_workspace(ctypes.byref(w), b)
+    if n < 0:
+        _check(n, "woq_lora_workspace")
+    return n
+
+
+def woq_lora_add(w: LoraW, x, ids, base, y, workspace, stream=None, b: int | None = None):
+    """y (fp16 [b, >= N]) = base (fp16, or None for zeros; may be y) + each
+    row's own adapter ids[r] (int32) of the pool ``w`` (DeviceLora.desc)
+    applied to x (fp16 [b, >= K]); rows with an id outside the pool keep base."""
+    b = x.shape[0] if b is None else b
+    half = "torch.float16"
+    xp = _rows(x, "x", half, b, w.K)
+    bp = (None, 0) if base is None else _rows(base, "base", half, b, w.N)
+    yp = _rows(y, "y", half, b, w.N)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    _call("woq_lora_add", stream, x, (ids, base, y, workspace), ctypes.byref(w), *xp,
+          _vector(ids, "ids", "torch.int32", b), b, *bp, *yp, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    return y
+
+
 # ------------------------------------------------- device-resident weights
 
 class DeviceInt8:
@@ -522,6 +634,39 @@ class DeviceInt4o:
         for p in parts:
             self.segments.append((end, end + p[0].shape[0]))
             end += p[0].shape[0]
+
+
+class DeviceLora:
+    """A pool of low-rank adapters of one linear (woq_lora_w) over device
+    tensors, which it keeps: A fp16 [count, S * R, >= K], B fp16 [count, N, R],
+    scale fp32 [count] and, optionally, rank int32 [count].  ``segments`` are
+    the ends of the S linears stacked along N (as q|k|v), default one.
+    Adapters may be written into the tensors at any time; calls see what the
+    stream holds by then."""
+
+    def __init__(self, A, B, scale, rank=None, K: int | None = None, segments=None):
+        half = "torch.float16"
+        if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0]:
+            raise ValueError("A is [count, S * R, >= K], B is [count, N, R]")
+        count, N, R = B.shape
+        segments = [N] if segments is None else [int(e) for e in segments]
+        if not 1 <= len(segments) <= MAX_SEGMENTS or segments[-1] != N or A.shape[1] != len(segments) * R:
+            raise ValueError(f"{len(segments)} segments of N = {N} with rank {R} need A [{count}, "
+                             f"{len(segments) * R}, >= K], got {tuple(A.shape)}")
+        K = A.shape[2] if K is None else K
+        if not 1 <= K <= A.shape[2]:
+            raise ValueError(f"K = {K}, but A's rows hold {A.shape[2]} values")
+        self.A, self.B, self.scale, self.rank = A, B, scale, rank
+        self.count, self.N, self.R, self.K = count, N, R, K
+        d = self.desc = LoraW()
+        d.A, d.B = _vector(A, "A", half, 0), _vector(B, "B", half, 0)
+        d.scale = _vector(scale, "scale", "torch.float32", count)
+        d.rank = None if rank is None else _vector(rank, "rank", "torch.int32", count)
+        if any(t is not None and t.device != A.device for t in (B, scale, rank)):
+            raise ValueError("the pool's tensors are on different devices")
+        d.N, d.K, d.lda, d.R, d.count, d.nseg = N, K, A.shape[2], R, count, len(segments)
+        for i, e in enumerate(segments):
+            d.seg_end[i] = e
 
 
 # ------------------------------------------------------------- stack runner
