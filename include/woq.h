@@ -474,6 +474,7 @@ int woq_qgemm_int8_a8(const woq_int8_w* w, const int8_t* xq, int64_t ldq, const 
  * 16-byte aligned.  R is a multiple of 8, at most WOQ_LORA_MAX_R.
  */
 #define WOQ_LORA_MAX_R 256
+#define WOQ_LORA_MAX_ROWS 1000000
 typedef struct {
     const uint16_t* A;
     const uint16_t* B;
@@ -497,7 +498,8 @@ typedef struct {
  * dimensions >= N; y may be base (same leading dimension).  workspace: at
  * least woq_lora_workspace(w, b) bytes of device memory, 16-byte aligned,
  * owned by the caller, its contents on return unspecified; calls that share
- * it must not overlap.  Deterministic.  b = 0 is a no-op.
+ * it must not overlap.  Deterministic.  b <= WOQ_LORA_MAX_ROWS; b = 0 is a
+ * no-op.
  * woq_lora_workspace returns a negative status for a bad descriptor or batch.
  */
 int woq_lora_add(const woq_lora_w* w, const uint16_t* x, int64_t ldx, const int32_t* ids, int64_t b,
