@@ -4,18 +4,19 @@
 //   h[r, i] = sum_k A[a][i, k] x[r, k],   a = ids[r],
 //
 // with y = base on rows without an adapter.  Two launches: the inner products
-// h into the workspace (fp32, one partial sum per K range), and the outer
-// ones added to the base.
+// h into the workspace, and the outer ones added to the base.
 //
 // Both run on the fp16 matrix cores with 16 ranks (or 16 outputs) of ONE
 // adapter against 16 rows: rows that share an adapter share its bytes, and a
 // result column belongs to one row, so rows never mix.  h is not rounded to
-// fp16 on the way: a row of h is scaled by a power of two to below 2^14 and
-// split into two fp16 halves, hi + lo, at least 22 bits; one 16x16x32 step
-// multiplies 16 ranks of B with both.
+// fp16 on the way: the ranks of a row are scaled by a power of two to below
+// 2^14 and split into two fp16 halves, hi + lo, at least 22 bits; one 16x16x32
+// step multiplies 16 ranks of B with both.
 //
-// A decode batch is bound by the bytes of the adapters that its rows name (or,
-// at a few rows, by the two launches); a prompt by the base and the output.
+// A decode batch is bound by the bytes of the adapters that its rows name, or,
+// at a few rows, by two launches of a few memory round trips each: the kernels
+// keep every load of a round in flight together and have no barrier before the
+// sums meet.  A prompt is bound by the base and the output.
 #include <hip/hip_runtime.h>
 
 #include "woq_gemv.h"
@@ -36,9 +37,10 @@ struct LoraArgs {
     const int32_t* ids;
     const uint16_t* base;     // null: zeros
     uint16_t* y;
-    float* h;                 // [splits][b][nseg R]
+    float* h;                 // few rows: sums [splits][b][nseg R]; else halves [b][nseg][groups][hi, lo][16 RT]
+    int32_t* exps;            // else: the halves' exponents [b][nseg][groups]
     int64_t ldx, ldbase, ldy, lda;
-    int b, N, K, R, count, nseg, splits;
+    int b, N, K, R, count, nseg, splits, groups, per;
     int vec;                  // rows of base and y may be read and written in 16-byte pieces
     int seg_end[WOQ_MAX_SEGMENTS];
     int tile0[WOQ_MAX_SEGMENTS + 1];   // output tiles before each segment
@@ -49,10 +51,11 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int id) {
 }
 
 __device__ __forceinline__ h8 as_h8(uint4 v) { return __builtin_bit_cast(h8, v); }
+__device__ __forceinline__ uint4 load16(const uint16_t* p) { return gload_u4(reinterpret_cast<const uint4*>(p)); }
 
-// Values k .. k + 7 of a row, zero from `end` on (which nothing past is read).
+// Values k .. k + 7 of a row, zero from `end` on (where nothing is read).
 __device__ __forceinline__ uint4 load8_until(const uint16_t* row, int k, int end) {
-    if (k + 8 <= end) return gload_u4(reinterpret_cast<const uint4*>(row + k));
+    if (k + 8 <= end) return load16(row + k);
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -60,111 +63,228 @@ __device__ __forceinline__ uint4 load8_until(const uint16_t* row, int k, int end
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The inner products.  blockIdx.y names RT rank tiles of 16 in one segment,
-// blockIdx.z one of the K ranges; the W waves split the range and add their
-// sums in LDS in a fixed order.
-//   LEADER (few rows): one workgroup per row; it works if its row is the first
-//     of its adapter, for all rows of that adapter (so distinct adapters run
-//     side by side, and a shared one is read once).
-//   otherwise: one workgroup per window of 32 rows, one adapter of the window
-//     after another (a packed prompt has one or two in a window).
-template <int W, int RT, bool LEADER>
+// The power of two that brings a row's largest |h| (as bits) to [2^13, 2^14).  A row that
+// is not finite is left as it is: every output of it is lost.
+__device__ __forceinline__ int scale_exponent(uint32_t big) {
+    return big == 0 || big >= 0x7F800000u ? 0 : 14 - __builtin_amdgcn_frexp_expf(__uint_as_float(big));
+}
+// hi | lo << 16 of v 2^ex
+__device__ __forceinline__ uint32_t split_halves(float v, int ex) {
+    const float s = ldexpf(v, ex);
+    const uint16_t hi = f_to_h(s);
+    return (uint32_t)hi | (uint32_t)((hi & 0x7C00u) == 0x7C00u ? 0 : f_to_h(s - h_to_f(hi))) << 16;
+}
+// v_perm selectors: the hi, or the lo, halves of two such words
+constexpr uint32_t HI = 0x05040100u, LO = 0x07060302u;
+
+// The adapters of a window of up to 64 NW rows, found by each wave for itself:
+// a lane holds the ids of rows lane, 64 + lane, ...
+template <int NW>
+struct Window {
+    int ids[NW];
+    __device__ __forceinline__ void read(const LoraArgs& a, int first, int rows, int lane) {
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            ids[w] = 64 * w + lane < rows ? *gptr(a.ids + first + 64 * w + lane) : -1;
+            if ((unsigned)ids[w] >= (unsigned)a.count) ids[w] = -1;
+        }
+    }
+};
+
+// The inner products of RT rank tiles of 16 in one segment (blockIdx.y).  The
+// W waves split the K range and add their sums in LDS in a fixed order.
+//   LEADER (few rows): one workgroup per row (blockIdx.x) and K range
+//     (blockIdx.z); it works if its row is the first of its adapter, for all
+//     rows of that adapter, so distinct adapters run side by side and a shared
+//     one is read once.  The ranges' sums go to the workspace as they are.
+//   otherwise: one workgroup per window of 32 rows; the workgroups of a window
+//     (blockIdx.z) take its adapters in turn (a packed prompt has one or two in a
+//     window).  h is written scaled and split, ready to be multiplied.
+// A wave reads 64 channels of its rows of A and x at a time, eight adjacent lanes
+// a row, D such pieces ahead, and turns them into operand order in a part of
+// LDS of its own (no barrier): read a lane per row straight into the operands,
+// the address unit bound this kernel (25 us, 3001 rows of 3584, two segments of rank 64).
+template <int W, int RT, int D, bool LEADER>
 __global__ __launch_bounds__(64 * W) void lora_down_kernel(LoraArgs a) {
-    constexpr int WIN = LEADER ? 256 : 32;
-    constexpr int UNR = 4;
-    static_assert(!LEADER || 64 * W >= WIN, "a thread per row of the window");
-    __shared__ int sid[WIN], list[WIN], cnt[W];
-    __shared__ __align__(16) f4 red[W][RT * 2][64];
+    constexpr int NW = LEADER ? 4 : 1, WIN = LEADER ? 256 : 32, KC = 64;
+    constexpr int CT = LEADER ? 1 : 2;                 // column tiles of 16 rows of x at a time
+    constexpr int AP = 2 * RT, XP = 2 * CT;            // pieces of a lane: eight rows each
+    constexpr int AREA = 16 * (RT + CT) * 2 * KC;      // bytes of a wave: the operands, then its sums
+    static_assert(AREA >= RT * CT * 1024, "the sums fit where the operands were");
+    __shared__ uint8_t list[W][WIN];
+    __shared__ __align__(16) uint8_t lds[W][AREA];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m = lane & 15, c = lane >> 4;
-    const int groups = (a.R + 16 * RT - 1) / (16 * RT);
-    const int seg = blockIdx.y / groups, j0 = (blockIdx.y % groups) * 16 * RT;
+    const int seg = blockIdx.y / a.groups, group = blockIdx.y % a.groups, j0 = group * 16 * RT;
     const int w0 = LEADER ? 0 : blockIdx.x * WIN;
     const int nwin = min(a.b - w0, WIN);
-    if (tid < nwin) sid[tid] = *gptr(a.ids + w0 + tid);
-    __syncthreads();
+    Window<NW> win;
+    win.read(a, w0, nwin, lane);
+    uint8_t* mem = lds[wave];
+    auto place = [](int row, int ch) { return row * 2 * KC + 16 * (ch ^ (row & 7)); };
+    const int pr = lane >> 3, pc = lane & 7;           // row and chunk of this lane in a piece
 
-    // this wave's 32-channel steps
-    const int steps = (a.K + 31) / 32, full = a.K / 32;
-    const int units = a.splits * W, unit = blockIdx.z * W + wave;
-    const int lo = (int)((int64_t)steps * unit / units), hi = (int)((int64_t)steps * (unit + 1) / units);
-    const int hi_full = min(hi, full);
+    // this wave's pieces of K
+    const int chunks = (a.K + KC - 1) / KC;
+    const int units = LEADER ? a.splits * W : W, unit = LEADER ? blockIdx.z * W + wave : wave;
+    const int lo = (int)((int64_t)chunks * unit / units), hi = (int)((int64_t)chunks * (unit + 1) / units);
 
-    for (int p = LEADER ? (int)blockIdx.x : 0; p < (LEADER ? (int)blockIdx.x + 1 : nwin); ++p) {
-        const int id = __builtin_amdgcn_readfirstlane(sid[p]);
-        if ((unsigned)id >= (unsigned)a.count || j0 >= rank_of(a, id)) continue;
-        const bool match = tid < nwin && sid[tid] == id;
-        const u64 mask = __ballot(match);
-        if (lane == 0) cnt[wave] = __popcll(mask);
-        if (__syncthreads_or(match && tid < p)) continue;   // not the first of its adapter
-        int before = 0, total = 0;
+    u64 left = LEADER ? 1ull : __ballot(win.ids[0] >= 0);
+    for (int turn = 0; left; ++turn) {
+        int id;
+        u64 of[NW];
+        if constexpr (LEADER) {
+            left = 0;
+            const int r = blockIdx.x;
+            id = -1;
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-            if (w < wave) before += cnt[w];
-            total += cnt[w];
+            for (int w = 0; w < NW; ++w)
+                if (r >> 6 == w) id = __builtin_amdgcn_readlane(win.ids[w], r & 63);
+            if (id < 0) return;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                of[w] = __ballot(win.ids[w] == id);
+                const u64 earlier = r >> 6 > w ? ~0ull : r >> 6 == w ? (1ull << (r & 63)) - 1 : 0;
+                if (of[w] & earlier) return;          // not the first of its adapter
+            }
+        } else {
+            id = __builtin_amdgcn_readlane(win.ids[0], __ffsll(left) - 1);
+            of[0] = __ballot(win.ids[0] == id);
+            left &= ~of[0];
+            if (turn % (int)gridDim.z != (int)blockIdx.z) continue;
         }
-        if (match) list[before + __popcll(mask & ((1ull << lane) - 1))] = tid;
-        __syncthreads();
+        const int rank = rank_of(a, id);
+        if (j0 >= rank) continue;
+        int total = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            if (of[w] >> lane & 1) list[wave][total + __popcll(of[w] & ((1ull << lane) - 1))] = (uint8_t)(64 * w + lane);
+            total += __popcll(of[w]);
+        }
+        __builtin_amdgcn_wave_barrier();
 
-        const uint16_t* ap[RT];
+        const uint16_t* ap[AP];
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
-            ap[t] = a.A + (((int64_t)id * a.nseg + seg) * a.R + min(j0 + 16 * t + m, a.R - 1)) * a.lda;
-        for (int c0 = 0; c0 < total; c0 += 32) {
-            // columns past the list repeat its first row; their results are dropped
-            const bool two = total - c0 > 16;
-            const uint16_t* xp[2];
+        for (int i = 0; i < AP; ++i)
+            ap[i] = a.A + (((int64_t)id * a.nseg + seg) * a.R + min(j0 + 8 * i + pr, a.R - 1)) * a.lda + 8 * pc;
+        for (int c0 = 0; c0 < total; c0 += 16 * CT) {
+            // columns past the list repeat its first row, or hold anything; their
+            // results are dropped
+            const bool two = CT == 2 && total - c0 > 16;
+            const uint16_t* xp[XP];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                xp[i] = a.x + (int64_t)(w0 + list[c0 + 16 * i + m < total ? c0 + 16 * i + m : c0]) * a.ldx;
-            f4 acc[RT][2];
+            for (int i = 0; i < XP; ++i) {
+                const int col = c0 + 8 * i + pr;
+                xp[i] = a.x + (int64_t)(w0 + list[wave][col < total ? col : c0]) * a.ldx + 8 * pc;
+            }
+            uint4 av[D][AP], xv[D][XP];
+            auto load = [&](int d, int chunk) {
+                if (chunk >= hi) return;
+                const int k = chunk * KC;
+                if (k + KC <= a.K) {
 #pragma unroll
-            for (int t = 0; t < RT; ++t) acc[t][0] = acc[t][1] = f4{0.f, 0.f, 0.f, 0.f};
-            int s = lo;
-            for (; s + UNR <= hi_full; s += UNR) {
-                uint4 av[UNR][RT], xv[UNR][2];
+                    for (int i = 0; i < AP; ++i) av[d][i] = load16(ap[i] + k);
 #pragma unroll
-                for (int u = 0; u < UNR; ++u) {
+                    for (int i = 0; i < XP; ++i)
+                        if (c0 + 8 * i < total) xv[d][i] = load16(xp[i] + k);
+                } else {                               // the row's last piece, zero past its end
+                    const int end = a.K - 8 * pc;
 #pragma unroll
-                    for (int t = 0; t < RT; ++t) av[u][t] = gload_u4(reinterpret_cast<const uint4*>(ap[t] + (s + u) * 32 + 8 * c));
-                    xv[u][0] = gload_u4(reinterpret_cast<const uint4*>(xp[0] + (s + u) * 32 + 8 * c));
-                    if (two) xv[u][1] = gload_u4(reinterpret_cast<const uint4*>(xp[1] + (s + u) * 32 + 8 * c));
+                    for (int i = 0; i < AP; ++i) av[d][i] = load8_until(ap[i], k, end);
+#pragma unroll
+                    for (int i = 0; i < XP; ++i) xv[d][i] = load8_until(xp[i], k, end);
                 }
+            };
+            f4 acc[RT][CT];
 #pragma unroll
-                for (int u = 0; u < UNR; ++u) {
+            for (int t = 0; t < RT; ++t) acc[t][0] = acc[t][CT - 1] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int t = 0; t < RT; ++t)
-                        acc[t][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_h8(av[u][t]), as_h8(xv[u][0]), acc[t][0], 0, 0, 0);
-                    if (two) {
+            for (int d = 0; d < D; ++d) load(d, lo + d);
+            for (int s = lo; s < hi; s += D) {
 #pragma unroll
-                        for (int t = 0; t < RT; ++t)
-                            acc[t][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_h8(av[u][t]), as_h8(xv[u][1]), acc[t][1], 0, 0, 0);
+                for (int d = 0; d < D; ++d) {
+                    if (s + d >= hi) break;
+                    auto put = [&](int row, uint4 v) {
+                        *(__attribute__((address_space(3))) u32x4*)(mem + place(row, pc)) = u32x4{v.x, v.y, v.z, v.w};
+                    };
+#pragma unroll
+                    for (int i = 0; i < AP; ++i) put(8 * i + pr, av[d][i]);
+#pragma unroll
+                    for (int i = 0; i < XP; ++i)
+                        if (c0 + 8 * i < total) put(16 * RT + 8 * i + pr, xv[d][i]);
+                    load(d, s + d + D);
+                    auto get = [&](int row, int step) {
+                        return __builtin_bit_cast(h8, *(const __attribute__((address_space(3))) u32x4*)(mem + place(row, 4 * step + c)));
+                    };
+#pragma unroll
+                    for (int step = 0; step < KC / 32; ++step) {
+                        h8 af[RT];
+#pragma unroll
+                        for (int t = 0; t < RT; ++t) af[t] = get(16 * t + m, step);
+                        const h8 x0 = get(16 * RT + m, step);
+#pragma unroll
+                        for (int t = 0; t < RT; ++t) acc[t][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(af[t], x0, acc[t][0], 0, 0, 0);
+                        if (two) {
+                            const h8 x1 = get(16 * RT + 16 + m, step);
+#pragma unroll
+                            for (int t = 0; t < RT; ++t) acc[t][CT - 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(af[t], x1, acc[t][CT - 1], 0, 0, 0);
+                        }
                     }
                 }
             }
-            for (; s < hi; ++s) {                      // what is left, the row's last piece among it
-                const int k = s * 32 + 8 * c;
-                const h8 x0 = as_h8(load8_until(xp[0], k, a.K)), x1 = as_h8(load8_until(xp[1], k, a.K));
-#pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    const h8 av = as_h8(load8_until(ap[t], k, a.K));
-                    acc[t][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, x0, acc[t][0], 0, 0, 0);
-                    acc[t][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, x1, acc[t][1], 0, 0, 0);
-                }
-            }
+            auto red = [&](int w, int i) { return (__attribute__((address_space(3))) f4*)lds[w] + i * 64 + lane; };
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                red[wave][2 * t][lane] = acc[t][0];
-                red[wave][2 * t + 1][lane] = acc[t][1];
+                *red(wave, CT * t) = acc[t][0];
+                if (CT == 2) *red(wave, CT * t + 1) = acc[t][CT - 1];
             }
             __syncthreads();
-            for (int i = tid; i < RT * 2 * 64; i += 64 * W) {
-                const int l = i & 63, t = i >> 7, col = c0 + 16 * (i >> 6 & 1) + (l & 15), j = j0 + 16 * t + 4 * (l >> 4);
-                if (col < total && j < a.R) {
-                    f4 v = red[0][i >> 6][l];
+            // a wave finishes a column tile: a lane has ranks 4c .. 4c + 3
+            // of every rank tile of one row
+            const int col = c0 + 16 * wave + m;
+            if (wave == 0 || (wave == 1 && two)) {
+                f4 v[RT];
 #pragma unroll
-                    for (int w = 1; w < W; ++w) v += red[w][i >> 6][l];
-                    *(__attribute__((address_space(1))) f4*)(a.h + (((int64_t)blockIdx.z * a.b + w0 + list[col]) * a.nseg + seg) * a.R + j) = v;
+                for (int t = 0; t < RT; ++t) {
+                    v[t] = *red(0, CT * t + wave);
+#pragma unroll
+                    for (int w = 1; w < W; ++w) v[t] += *red(w, CT * t + wave);
+                }
+                const int64_t row = (w0 + list[wave][col < total ? col : c0]);
+                if constexpr (LEADER) {
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) {
+                        const int j = j0 + 16 * t + 4 * c;
+                        if (col < total && j < a.R)
+                            *(__attribute__((address_space(1))) f4*)(a.h + (((int64_t)blockIdx.z * a.b + row) * a.nseg + seg) * a.R + j) = v[t];
+                    }
+                } else {
+                    uint32_t big = 0;
+#pragma unroll
+                    for (int t = 0; t < RT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (j0 + 16 * t + 4 * c + e >= rank) v[t][e] = 0.f;
+                            big = max(big, __float_as_uint(v[t][e]) & 0x7FFFFFFFu);
+                        }
+                    big = max(big, (uint32_t)__shfl_xor((int)big, 16));
+                    big = max(big, (uint32_t)__shfl_xor((int)big, 32));
+                    const int ex = scale_exponent(big);
+                    if (col < total) {
+                        const int64_t at = (row * a.nseg + seg) * a.groups + group;
+                        uint16_t* out = reinterpret_cast<uint16_t*>(a.h) + at * 32 * RT;
+#pragma unroll
+                        for (int t = 0; t < RT; ++t) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) w[e] = split_halves(v[t][e], ex);
+                            *(__attribute__((address_space(1))) u32x2*)(out + 16 * t + 4 * c) =
+                                u32x2{__builtin_amdgcn_perm(w[1], w[0], HI), __builtin_amdgcn_perm(w[3], w[2], HI)};
+                            *(__attribute__((address_space(1))) u32x2*)(out + 16 * RT + 16 * t + 4 * c) =
+                                u32x2{__builtin_amdgcn_perm(w[1], w[0], LO), __builtin_amdgcn_perm(w[3], w[2], LO)};
+                        }
+                        if (c == 0) *gptr(a.exps + at) = -ex;
+                    }
                 }
             }
             __syncthreads();
@@ -172,232 +292,450 @@ __global__ __launch_bounds__(64 * W) void lora_down_kernel(LoraArgs a) {
     }
 }
 
-// The outer products: 16 MU rows x 64 J outputs of one segment per workgroup
-// of four waves, J output tiles a wave; ID adapters at a time, so that a decode
-// batch of many adapters has the loads of several in flight.
-template <int MU, int J, int ID>
-__global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
-    constexpr int TM = 16 * MU, TPR = 256 / TM;        // rows, threads per row
-    extern __shared__ __align__(16) uint32_t hp[];     // [TM][Rp + 4]: hi | lo << 16
-    __shared__ int sid[TM], sexp[TM];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int m = lane & 15, c = lane >> 4;
-    const int Rp = (a.R + 15) & ~15, ldh = Rp + 4;
+// The columns of a wave's J output tiles, 16 J adjacent ones of one segment.
+// The four results that a lane has of a tile are adjacent columns; two tiles
+// side by side give a lane eight, and the four lanes of a row 64 adjacent bytes.
+template <int J>
+struct Cols {
+    // first column of the results of lane group c in tile j
+    static __device__ __forceinline__ constexpr int at(int c, int j) {
+        return j < (J & ~1) ? 32 * (j >> 1) + 8 * c + 4 * (j & 1) : 16 * j + 4 * c;
+    }
+    // column of row mm of tile j's matrix operand
+    static __device__ __forceinline__ int row(int mm, int j) { return at(mm >> 2, j) + (mm & 3); }
+    // whole: 16-byte aligned, all columns inside the segment (else the first `left`)
+    static __device__ __forceinline__ void load(uint32_t (&v)[2 * J], const uint16_t* p, int c, int left, bool whole) {
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j + 1 < J; j += 2) {
+                const uint4 q = load16(p + at(c, j));
+                v[2 * j] = q.x, v[2 * j + 1] = q.y, v[2 * j + 2] = q.z, v[2 * j + 3] = q.w;
+            }
+            if constexpr (J % 2) {
+                const uint2 q = gload_u2(reinterpret_cast<const uint2*>(p + at(c, J - 1)));
+                v[2 * J - 2] = q.x, v[2 * J - 1] = q.y;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4 * J; ++e) {
+                const int n = at(c, e >> 2) + (e & 3);
+                const uint32_t t = n < left ? (uint32_t)*gptr(p + n) << (16 * (e & 1)) : 0;
+                v[e >> 1] = e & 1 ? v[e >> 1] | t : t;
+            }
+        }
+    }
+    static __device__ __forceinline__ void store(const uint32_t (&v)[2 * J], uint16_t* p, int c, int left, bool whole) {
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j + 1 < J; j += 2)
+                gstore_u4(reinterpret_cast<uint4*>(p + at(c, j)), make_uint4(v[2 * j], v[2 * j + 1], v[2 * j + 2], v[2 * j + 3]));
+            if constexpr (J % 2)
+                *(__attribute__((address_space(1))) u32x2*)(p + at(c, J - 1)) = u32x2{v[2 * J - 2], v[2 * J - 1]};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4 * J; ++e) {
+                const int n = at(c, e >> 2) + (e & 3);
+                if (n < left) *gptr(p + n) = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+            }
+        }
+    }
+    // fp16(base + s d) of a row's results
+    static __device__ __forceinline__ void add(uint32_t (&v)[2 * J], const f4 (&d)[J], float s) {
+#pragma unroll
+        for (int e = 0; e < 2 * J; ++e) {
+            const h2 b = as_h2(v[e]);
+            v[e] = (uint32_t)f_to_h(fmaf(d[e >> 1][2 * (e & 1)], s, (float)b[0])) |
+                   (uint32_t)f_to_h(fmaf(d[e >> 1][2 * (e & 1) + 1], s, (float)b[1])) << 16;
+        }
+    }
+};
+
+// Segment and first output column of this workgroup's tile (blockIdx.x).
+__device__ __forceinline__ int tile_segment(const LoraArgs& a, int width, int& n0) {
     int seg = 0;
 #pragma unroll
     for (int i = 1; i < WOQ_MAX_SEGMENTS; ++i)
         if (i < a.nseg && (int)blockIdx.x >= a.tile0[i]) seg = i;
-    const int seg_lo = seg ? a.seg_end[seg - 1] : 0, seg_hi = a.seg_end[seg];
-    const int n0 = seg_lo + ((int)blockIdx.x - a.tile0[seg]) * 64 * J;
-    const int r0 = blockIdx.y * TM, rows = min(a.b - r0, TM);
-    // a lane's 4 J outputs of a row are adjacent
-    const int nw = n0 + wave * 16 * J, nl = nw + c * 4 * J;
-    const bool whole = a.vec && (n0 & 7) == 0 && nl + 4 * J <= seg_hi;
+    n0 = (seg ? a.seg_end[seg - 1] : 0) + ((int)blockIdx.x - a.tile0[seg]) * width;
+    return seg;
+}
 
-    // the base, on its way while h is made ready
-    uint32_t base[MU][2 * J];
+// The outer products of a decode batch: 16 rows x 64 outputs of one segment per
+// workgroup of four waves, one output tile a wave.  Each adapter of the 16 rows
+// gives a tile of results, of which its rows keep theirs.  A step is 16 ranks of
+// one adapter; the operands of the next U steps are always on their way.
+__global__ __launch_bounds__(256, 4) void lora_up_rows_kernel(LoraArgs a) {
+    constexpr int TM = 16, U = 16;
+    using C = Cols<1>;
+    extern __shared__ __align__(16) uint32_t hp[];     // [TM][Rp + 4]: hi | lo << 16
+    __shared__ int sexp[TM];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int m = lane & 15, c = lane >> 4;
+    const int Rp = (a.R + 15) & ~15, ldh = Rp + 4;
+    int n0;
+    const int seg = tile_segment(a, 64, n0), r0 = blockIdx.y * TM, rows = min(a.b - r0, TM);
+    const int nw = n0 + 16 * wave, left = a.seg_end[seg] - nw;      // this wave's columns
+    const bool whole = a.vec && (n0 & 7) == 0 && left >= 16;
+    Window<1> win;
+    win.read(a, r0, rows, lane);
+    uint32_t v[2] = {0, 0};
+    if (a.base && m < rows) C::load(v, a.base + (int64_t)(r0 + m) * a.ldbase + nw, c, left, whole);
+
+    // h, 16 threads a row: the K ranges' sums of four ranks, added in order.
+    // They are read before it is known what the row's adapter has of them (a
+    // row without one has none in the workspace): what it has not is dropped.
+    const int r = tid >> 4, q = tid & 15;
+    uint32_t* row = hp + r * ldh;
+    const float* hr = a.h + ((int64_t)(r0 + min(r, rows - 1)) * a.nseg + seg) * a.R;
+    const int64_t range = (int64_t)a.b * a.nseg * a.R;
+    for (int j = 4 * q; j < a.R; j += 64) {
+        f4 s = {0.f, 0.f, 0.f, 0.f};
+        for (int z = 0; z < a.splits; z += 8) {        // eight loads in flight
+            f4 p[8];
 #pragma unroll
-    for (int i = 0; i < MU; ++i) {
-        const int r = 16 * i + m;
+            for (int u = 0; u < 8; ++u)
+                p[u] = *(__attribute__((address_space(1))) const f4*)(hr + min(z + u, a.splits - 1) * range + j);
 #pragma unroll
-        for (int e = 0; e < 2 * J; ++e) base[i][e] = 0;
-        if (!a.base || r >= rows || nl >= seg_hi) continue;
-        const uint16_t* br = a.base + (int64_t)(r0 + r) * a.ldbase + nl;
-        if (whole) {
-            if constexpr (J % 2 == 0) {
-#pragma unroll
-                for (int e = 0; e < J / 2; ++e) {
-                    const uint4 v = gload_nt(reinterpret_cast<const uint4*>(br) + e);
-                    base[i][4 * e] = v.x, base[i][4 * e + 1] = v.y, base[i][4 * e + 2] = v.z, base[i][4 * e + 3] = v.w;
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < J; ++e) {
-                    const uint2 v = gload_u2(reinterpret_cast<const uint2*>(br) + e);
-                    base[i][2 * e] = v.x, base[i][2 * e + 1] = v.y;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4 * J; ++e)
-                if (nl + e < seg_hi) base[i][e >> 1] |= (uint32_t)*gptr(br + e) << (16 * (e & 1));
+            for (int u = 0; u < 8; ++u)
+                if (z + u < a.splits) s += p[u];
         }
+        *(f4*)(row + j) = s;
     }
 
-    // h: the ranges' sums added in order, scaled by a power of two, in two halves
-    {
-        const int r = tid / TPR, q = tid % TPR;
-        const int id = r < rows ? *gptr(a.ids + r0 + r) : -1;
-        const bool on = (unsigned)id < (unsigned)a.count;
-        const int rank = on ? rank_of(a, id) : 0;
-        const float* hr = a.h + ((int64_t)(r0 + r) * a.nseg + seg) * a.R;
-        const int64_t range = (int64_t)a.b * a.nseg * a.R;
-        uint32_t* row = hp + r * ldh;
+    // the distinct adapters of the rows, the k-th in lane k
+    int list = 0, count = 0, most = 0;
+    for (u64 rest = __ballot(win.ids[0] >= 0); rest; ++count) {
+        const int id = __builtin_amdgcn_readlane(win.ids[0], __ffsll(rest) - 1);
+        rest &= ~__ballot(win.ids[0] == id);
+        if (lane == count) list = id;
+        most = max(most, rank_of(a, id));
+    }
+    const int groups = (most + 15) >> 4, steps = left > 0 ? count * groups : 0;
+    const int lane_b = C::row(m, 0) * a.R + 8 * (c & 1);
+    int lk = 0, lt = 0;                                // the next step to load
+    auto load_b = [&](uint4& to) {
+        const int id = __builtin_amdgcn_readlane(list, lk), rank = rank_of(a, id);
+        const uint16_t* p = a.B + ((int64_t)id * a.N + nw) * a.R + 16 * lt;
+        if (left >= 16 && rank >= 16 * (lt + 1)) to = load16(p + lane_b);
+        else to = load8_until(p + (int64_t)(min(C::row(m, 0), left - 1)) * a.R, 8 * (c & 1), rank - 16 * lt);
+        if (++lt == groups) lt = 0, ++lk;
+    };
+    uint4 bv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (u < steps) load_b(bv[u]);
+    const int mine = __shfl(win.ids[0], m);
+    const float scale = mine >= 0 ? *gptr(a.scale + mine) : 0.f;
+
+    {   // what the row has of h, scaled by a power of two, in two halves
+        const int own = __shfl(win.ids[0], r);
+        const int rk = own >= 0 ? rank_of(a, own) : 0;
         uint32_t big = 0;
-        for (int j = 4 * q; j < Rp; j += 4 * TPR) {
-            f4 v = {0.f, 0.f, 0.f, 0.f};
-            if (j < rank) {
-                for (int s = 0; s < a.splits; ++s) v += *(__attribute__((address_space(1))) const f4*)(hr + s * range + j);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (j + e >= rank) v[e] = 0.f;
-                    big = max(big, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-                }
-            }
-            *(f4*)(row + j) = v;
-        }
-#pragma unroll
-        for (int d = 1; d < TPR; d <<= 1) big = max(big, (uint32_t)__shfl_xor((int)big, d));
-        // a row that is not finite is left as it is: every output of it is lost
-        const int ex = big == 0 || big >= 0x7F800000u ? 0 : 14 - __builtin_amdgcn_frexp_expf(__uint_as_float(big));
-        for (int j = 4 * q; j < Rp; j += 4 * TPR) {
-            const f4 v = *(const f4*)(row + j);
-            uint32_t w[4];
+        for (int j = 4 * q; j < Rp; j += 64) {
+            f4 s = *(const f4*)(row + j);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float t = ldexpf(v[e], ex);
-                const uint16_t hi = f_to_h(t);
-                const float rest = t - h_to_f(hi);
-                w[e] = (uint32_t)hi | (uint32_t)((hi & 0x7C00u) == 0x7C00u ? 0 : f_to_h(rest)) << 16;
+                if (j + e >= rk) s[e] = 0.f;
+                big = max(big, __float_as_uint(s[e]) & 0x7FFFFFFFu);
             }
-            *(u32x4*)(row + j) = u32x4{w[0], w[1], w[2], w[3]};
+            *(f4*)(row + j) = s;
         }
-        if (q == 0) {
-            sid[r] = on ? id : -1;
-            sexp[r] = -ex;
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) big = max(big, (uint32_t)__shfl_xor((int)big, d));
+        const int ex = scale_exponent(big);
+        for (int j = 4 * q; j < Rp; j += 64) {
+            const f4 s = *(const f4*)(row + j);
+            *(u32x4*)(row + j) = u32x4{split_halves(s[0], ex), split_halves(s[1], ex), split_halves(s[2], ex), split_halves(s[3], ex)};
         }
+        if (q == 0) sexp[r] = -ex;
     }
     __syncthreads();
 
-    const int mine = lane < TM ? sid[lane] : -1;
-    u64 left = __ballot(mine >= 0);
-    const uint32_t sel = c < 2 ? 0x05040100u : 0x07060302u;   // the hi or the lo halves of two values
-    auto put = [&](int i, const f4 (&d)[J], bool plain, float s, int ex) {
-        const int r = 16 * i + m;
-        uint16_t* yr = a.y + (int64_t)(r0 + r) * a.ldy + nl;
-        uint32_t o[2 * J];
+    f4 acc = {0.f, 0.f, 0.f, 0.f}, d[1] = {acc};
+    int k = 0, t = 0;
+    const uint32_t sel = c < 2 ? HI : LO;
+    for (int s = 0; s < steps; s += U) {
 #pragma unroll
-        for (int e = 0; e < 2 * J; ++e) {
-            const h2 bv = as_h2(base[i][e]);
-            const float v0 = fmaf(ldexpf(d[e >> 1][2 * (e & 1)], ex), s, (float)bv[0]);
-            const float v1 = fmaf(ldexpf(d[e >> 1][2 * (e & 1) + 1], ex), s, (float)bv[1]);
-            o[e] = plain ? base[i][e] : (uint32_t)f_to_h(v0) | (uint32_t)f_to_h(v1) << 16;
-        }
-        if (whole) {
-            if constexpr (J % 2 == 0) {
-#pragma unroll
-                for (int e = 0; e < J / 2; ++e)
-                    gstore_u4(reinterpret_cast<uint4*>(yr) + e, make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
-            } else {
-#pragma unroll
-                for (int e = 0; e < J; ++e) *(__attribute__((address_space(1))) u32x2*)(yr + 4 * e) = u32x2{o[2 * e], o[2 * e + 1]};
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4 * J; ++e)
-                if (nl + e < seg_hi) *gptr(yr + e) = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
-        }
-    };
-    while (left) {
-        int id[ID], rank[ID], most = 0;
-        u64 of[ID];
-#pragma unroll
-        for (int k = 0; k < ID; ++k) {
-            // past the last adapter the first is repeated, for no rows
-            id[k] = k && !left ? id[0] : __builtin_amdgcn_readlane(mine, __ffsll(left) - 1);
-            of[k] = k && !left ? 0 : __ballot(mine == id[k]);
-            left &= ~of[k];
-            rank[k] = rank_of(a, id[k]);
-            most = max(most, rank[k]);
-        }
-        f4 acc[ID][MU][J];
-#pragma unroll
-        for (int k = 0; k < ID; ++k)
-#pragma unroll
-            for (int i = 0; i < MU; ++i)
-#pragma unroll
-                for (int j = 0; j < J; ++j) acc[k][i][j] = f4{0.f, 0.f, 0.f, 0.f};
-        for (int t = 0; t < most; t += 16) {
-            uint4 bv[ID][J];
-#pragma unroll
-            for (int k = 0; k < ID; ++k)
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    const int n = min(nw + (m >> 2) * 4 * J + 4 * j + (m & 3), seg_hi - 1), f = t + 8 * (c & 1);
-                    const uint16_t* br = a.B + ((int64_t)id[k] * a.N + n) * a.R;
-                    bv[k][j] = f < rank[k] ? load8_until(br, f, rank[k]) : make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-            for (int i = 0; i < MU; ++i) {
-                const uint32_t* row = hp + (16 * i + m) * ldh + t + 8 * (c & 1);
-                const u32x4 p0 = *(const u32x4*)row, p1 = *(const u32x4*)(row + 4);
+        for (int u = 0; u < U; ++u) {
+            if (s + u < steps) {
+                const uint32_t* hw = hp + m * ldh + 16 * t + 8 * (c & 1);
+                const u32x4 p0 = *(const u32x4*)hw, p1 = *(const u32x4*)(hw + 4);
                 const h8 hv = as_h8(make_uint4(__builtin_amdgcn_perm(p0[1], p0[0], sel), __builtin_amdgcn_perm(p0[3], p0[2], sel),
                                                __builtin_amdgcn_perm(p1[1], p1[0], sel), __builtin_amdgcn_perm(p1[3], p1[2], sel)));
-#pragma unroll
-                for (int k = 0; k < ID; ++k)
-#pragma unroll
-                    for (int j = 0; j < J; ++j)
-                        acc[k][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_h8(bv[k][j]), hv, acc[k][i][j], 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_h8(bv[u]), hv, acc, 0, 0, 0);
+                if (s + u + U < steps) load_b(bv[u]);
+                if (++t == groups) {
+                    if (mine == __builtin_amdgcn_readlane(list, k)) d[0] = acc;
+                    acc = f4{0.f, 0.f, 0.f, 0.f};
+                    t = 0, ++k;
+                }
             }
         }
-        if (nl < seg_hi) {
+    }
+    if (left <= 0 || m >= rows || (mine < 0 && a.base == a.y && a.ldbase == a.ldy)) return;
+    if (mine >= 0) {
+        const int ex = sexp[m];
 #pragma unroll
-            for (int k = 0; k < ID; ++k) {
-                const float s = *gptr(a.scale + id[k]);
+        for (int e = 0; e < 4; ++e) d[0][e] = ldexpf(d[0][e], ex);
+        C::add(v, d, scale);
+    }
+    C::store(v, a.y + (int64_t)(r0 + m) * a.ldy + nw, c, left, whole);
+}
+
+// The outer products of a prompt: 64 rows, 16 to each of four waves, x 64
+// outputs at a time, over a.per such tiles; h comes scaled and split and stays in
+// registers.  One adapter of the rows after another, each writing its own rows.
+//
+// h is the first matrix operand and B the second, with column m of its tile j
+// the output 4 m + j: a lane then has four adjacent outputs of four rows, and
+// the 16 lanes of a row 128 adjacent bytes.  B is read in the order it lies in
+// memory, once for the four waves, and passes through LDS into operand order.
+// (A lane-per-row access costs the address unit a lookup per lane: with it for
+// B, base and y this kernel took 125 us, 3001 rows, 28672 outputs, rank 64; with
+// 32 rows and a B of its own to each wave, and so only two waves on a SIMD, 110;
+// now 93, where copying base to y takes 65.  Two adapters of a window in one pass
+// measured 114: the registers cost more than the second pass.)
+template <int RT, bool MULTI>
+__global__ __launch_bounds__(256, 4) void lora_up_wide_kernel(LoraArgs a) {
+    constexpr int J = 4, TM = 64, TN = 16 * J;
+    constexpr int NB = RT == 1 ? 1 : RT / 2;           // steps of 32 ranks (of 16: one, both halves at once)
+    constexpr int CH = 2 * RT, NP = (TN * CH + 255) / 256;   // 16-byte pieces of a row of B, of a thread
+    __shared__ __align__(16) uint8_t lds[2][TN * 32 * RT];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int m = lane & 15, c = lane >> 4;
+    int n_first;
+    const int seg = tile_segment(a, TN * a.per, n_first), hi = a.seg_end[seg];
+    const int r0 = blockIdx.y * TM, rows = min(a.b - r0, TM);
+    const int tiles = min(a.per, (hi - n_first + TN - 1) / TN), groups = MULTI ? a.groups : 1;
+    const bool vec = a.vec && (n_first & 3) == 0;
+    Window<1> win;
+    win.read(a, r0, rows, lane);
+
+    // a lane's rows 16 wave + 4 c + e, its columns 4 m .. 4 m + 3 of the tile
+    const int row0 = 16 * wave + 4 * c;
+    const uint16_t* bp = a.base ? a.base + (int64_t)(r0 + row0) * a.ldbase + n_first + 4 * m : nullptr;
+    uint16_t* yp = a.y + (int64_t)(r0 + row0) * a.ldy + n_first + 4 * m;
+    uint2 v[4];
+    auto load_base = [&](int i, uint32_t of) {         // bit e of `of`: row row0 + e
+        const int left = hi - n_first - i * TN - 4 * m;
 #pragma unroll
-                for (int i = 0; i < MU; ++i)
-                    if (of[k] >> (16 * i + m) & 1) put(i, acc[k][i], false, s, sexp[16 * i + m]);
+        for (int e = 0; e < 4; ++e) {
+            v[e] = make_uint2(0, 0);
+            if (!a.base || !(of >> e & 1)) continue;
+            const uint16_t* p = bp + e * a.ldbase + i * TN;
+            if (vec && left >= 4) {
+                v[e] = gload_u2(reinterpret_cast<const uint2*>(p));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < left) (j < 2 ? v[e].x : v[e].y) |= (uint32_t)*gptr(p + j) << (16 * (j & 1));
+            }
+        }
+    };
+    auto store = [&](int i, uint32_t of) {
+        const int left = hi - n_first - i * TN - 4 * m;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (!(of >> e & 1)) continue;
+            uint16_t* p = yp + e * a.ldy + i * TN;
+            if (vec && left >= 4) {
+                *(__attribute__((address_space(1))) u32x2*)p = u32x2{v[e].x, v[e].y};
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < left) *gptr(p + j) = (uint16_t)((j < 2 ? v[e].x : v[e].y) >> (16 * (j & 1)));
+            }
+        }
+    };
+    // position of piece ch of row `row` of B in LDS: eight lanes that read together
+    // (rows 4 m + j, one piece) fall on different banks
+    auto place = [](int row, int ch) {
+        return row * 32 * RT + 16 * (ch ^ (RT == 4 ? row >> 2 & 7 : RT == 2 ? row >> 2 & 3 : row >> 2 & 1));
+    };
+    const int ch = tid % CH, brow = tid / CH;          // this thread's piece of B, and those 256 / CH rows apart
+
+    // what the workspace holds of a row's h: rows of other adapters, or without
+    // one, may hold anything (their results are dropped)
+    h8 hv[RT];
+    int ex[4];
+    auto load_h = [&](int g) {
+        const int64_t at = ((int64_t)min(r0 + 16 * wave + m, a.b - 1) * a.nseg + seg) * groups + g;
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(a.h) + at * 32 * RT + 8 * c;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) hv[t] = as_h8(load16(p + 32 * t));
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            ex[e] = *gptr(a.exps + ((int64_t)min(r0 + row0 + e, a.b - 1) * a.nseg + seg) * groups + g);
+    };
+    // none of these waits for the adapters to be known
+    load_h(0);
+    load_base(0, (uint32_t)(~0ull >> (64 - rows) >> row0) & 15u);
+    bool once = true;
+    u64 rest = __ballot(win.ids[0] >= 0);
+    const u64 plain = __ballot(lane < rows) & ~rest;
+    int turn = 0;
+    while (rest) {
+        const int id = __builtin_amdgcn_readlane(win.ids[0], __ffsll(rest) - 1);
+        const u64 all = __ballot(win.ids[0] == id);
+        rest &= ~all;
+        const bool mine = all >> (16 * wave) & 0xFFFF;  // this wave has rows of it
+        const uint32_t of = (uint32_t)(all >> row0) & 15u;
+        const int rank = rank_of(a, id), used = MULTI ? max(1, (rank + 16 * RT - 1) / (16 * RT)) : 1;
+        const float scale = *gptr(a.scale + id);
+
+        uint4 bq[NP];
+        auto load_b = [&](int i, int g) {
+            // whole pieces of the rows that there are; ranks that the adapter has not
+            // are cut off when the pieces are staged
+            const int k = 16 * g * RT;
+            const bool some = k + 8 * ch < rank && brow < TN;
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                const int n = min(n_first + i * TN + brow + 256 / CH * q, hi - 1);
+                bq[q] = load16(some ? a.B + ((int64_t)id * a.N + n) * a.R + k + 8 * ch : a.B);
+            }
+        };
+        auto stage_b = [&](uint8_t* mem, int g) {
+            const int left = rank - 16 * g * RT - 8 * ch;
+            if (left < 8) {
+#pragma unroll
+                for (int q = 0; q < NP; ++q) {
+                    uint32_t w[4] = {bq[q].x, bq[q].y, bq[q].z, bq[q].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] &= (left > 2 * e ? 0xFFFFu : 0u) | (left > 2 * e + 1 ? 0xFFFF0000u : 0u);
+                    bq[q] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            if (brow < TN) {
+#pragma unroll
+                for (int q = 0; q < NP; ++q)
+                    *(__attribute__((address_space(3))) u32x4*)(mem + place(brow + 256 / CH * q, ch)) =
+                        u32x4{bq[q].x, bq[q].y, bq[q].z, bq[q].w};
+            }
+        };
+        load_b(0, 0);
+        if (MULTI || !once) load_h(0);
+        if (!once) load_base(0, of);
+        once = false;
+        float s[4];                                    // scale and the power of two of a lane's rows
+        auto scales = [&]() {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[e] = ldexpf(scale, rank ? ex[e] : 0);
+                // a finite scale stays finite: sums of zero have to stay zero
+                if (__builtin_isinf(s[e]) && !__builtin_isinf(scale)) s[e] = copysignf(3.4028235e38f, scale);
+            }
+            // an adapter of rank 0 left nothing there
+            if (rank == 0) {
+#pragma unroll
+                for (int t = 0; t < RT; ++t) hv[t] = h8{};
+            }
+        };
+        scales();
+        for (int i = 0; i < tiles; ++i) {
+            f4 sum[J];
+            for (int g = 0; g < used; ++g, turn ^= 1) {
+                uint8_t* mem = lds[turn];
+                stage_b(mem, g);
+                const bool last = g + 1 == used;
+                load_b(last ? min(i + 1, tiles - 1) : i, last ? 0 : g + 1);
+                __syncthreads();
+                if (mine) {
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        f4 acc = {0.f, 0.f, 0.f, 0.f};
+                        h8 bv[NB];
+#pragma unroll
+                        for (int t = 0; t < NB; ++t)
+                            bv[t] = __builtin_bit_cast(h8, *(const __attribute__((address_space(3))) u32x4*)(mem + place(4 * m + j, RT == 1 ? c & 1 : 4 * t + c)));
+#pragma unroll
+                        for (int t = 0; t < RT; ++t)   // the hi halves of all ranks, then the lo
+                            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(hv[t], bv[t % NB], acc, 0, 0, 0);
+                        if constexpr (MULTI) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) sum[j][e] = g ? fmaf(acc[e], s[e], sum[j][e]) : acc[e] * s[e];
+                        } else {
+                            sum[j] = acc;
+                        }
+                    }
+                }
+                if constexpr (MULTI) {
+                    load_h(last ? 0 : g + 1);
+                    scales();
+                }
+            }
+            if (mine) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const h2 b0 = as_h2(v[e].x), b1 = as_h2(v[e].y);
+                    const float f = MULTI ? 1.f : s[e];
+                    v[e].x = (uint32_t)f_to_h(fmaf(sum[0][e], f, (float)b0[0])) | (uint32_t)f_to_h(fmaf(sum[1][e], f, (float)b0[1])) << 16;
+                    v[e].y = (uint32_t)f_to_h(fmaf(sum[2][e], f, (float)b1[0])) | (uint32_t)f_to_h(fmaf(sum[3][e], f, (float)b1[1])) << 16;
+                }
+                store(i, of);
+                if (i + 1 < tiles) load_base(i + 1, of);
             }
         }
     }
     // rows without an adapter
-    if (nl < seg_hi && (a.base != a.y || a.ldbase != a.ldy)) {
-        const f4 none[J] = {};
-#pragma unroll
-        for (int i = 0; i < MU; ++i)
-            if (16 * i + m < rows && sid[16 * i + m] < 0) put(i, none, true, 0.f, 0);
+    const uint32_t bare = (uint32_t)(plain >> row0) & 15u;
+    if (!(plain >> (16 * wave) & 0xFFFF) || (a.base == a.y && a.ldbase == a.ldy)) return;
+    for (int i = 0; i < tiles; ++i) {
+        load_base(i, bare);
+        store(i, bare);
     }
 }
 
 // Rows up to which a workgroup per row looks for its adapter's other rows.
 constexpr int LEADER_ROWS = 256;
-// Partial sums of a row: at most so many K ranges, in each of the two forms.
-constexpr int LEADER_SPLITS = 16, WINDOW_SPLITS = 4;
+// K ranges of a row's inner products, at most, in that form.
+constexpr int LEADER_SPLITS = 16;
 
-int rank_tiles(int b, int R) { return b <= LEADER_ROWS ? 1 : R <= 16 ? 1 : R <= 32 ? 2 : 4; }
+// 16-rank tiles that a window's workgroup takes together.
+int rank_tiles(int64_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }
 
-int k_ranges(int b, int K, int R, int nseg) {
-    const bool leader = b <= LEADER_ROWS;
-    const int rt = rank_tiles(b, R), waves = leader ? 4 : 8;
-    const int64_t units = woq::ceil_div(b, leader ? 1 : 32) * nseg * woq::ceil_div(R, 16 * rt);
-    const int64_t want = woq::ceil_div(1024, units), most = std::max<int64_t>(1, K / (waves * 64));
-    return (int)std::min<int64_t>(std::min(want, most), leader ? LEADER_SPLITS : WINDOW_SPLITS);
+// K ranges that leave every wave of a few rows' workgroups one round of loads,
+// four pieces of 64 channels.
+int k_ranges(int K) { return (int)std::min<int64_t>(woq::ceil_div(K, 4 * 4 * 64), LEADER_SPLITS); }
+
+hipError_t launch(const void* kernel, dim3 grid, int threads, size_t lds, hipStream_t s, LoraArgs a) {
+    void* argv[] = {&a};
+    return hipLaunchKernel(kernel, grid, dim3((unsigned)threads), argv, lds, s);
 }
 
-template <int W, int RT, bool LEADER>
-hipError_t launch_down(const LoraArgs& a, hipStream_t s) {
-    LoraArgs args = a;
-    void* argv[] = {&args};
-    const int groups = (int)woq::ceil_div(a.R, 16 * RT);
-    return hipLaunchKernel(reinterpret_cast<const void*>(&lora_down_kernel<W, RT, LEADER>),
-                           dim3((unsigned)(LEADER ? a.b : woq::ceil_div(a.b, 32)), (unsigned)(a.nseg * groups), (unsigned)a.splits),
-                           dim3(64 * W), argv, 0, s);
-}
-
-template <int MU, int J, int ID>
-hipError_t launch_up(LoraArgs a, hipStream_t s) {
+// Output tiles of `width` columns, counted segment by segment.
+unsigned count_tiles(LoraArgs& a, int width) {
     a.tile0[0] = 0;
     for (int i = 0; i < a.nseg; ++i)
-        a.tile0[i + 1] = a.tile0[i] + (int)woq::ceil_div(a.seg_end[i] - (i ? a.seg_end[i - 1] : 0), 64 * J);
-    void* argv[] = {&a};
-    const size_t lds = (size_t)16 * MU * (woq::round_up(a.R, 16) + 4) * 4;
-    if (lds > 60 * 1024) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&lora_up_kernel<MU, J, ID>),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-        if (e != hipSuccess) return e;
-    }
-    return hipLaunchKernel(reinterpret_cast<const void*>(&lora_up_kernel<MU, J, ID>),
-                           dim3((unsigned)a.tile0[a.nseg], (unsigned)woq::ceil_div(a.b, 16 * MU)), dim3(256), argv, lds, s);
+        a.tile0[i + 1] = a.tile0[i] + (int)woq::ceil_div(a.seg_end[i] - (i ? a.seg_end[i - 1] : 0), width);
+    return (unsigned)a.tile0[a.nseg];
+}
+
+hipError_t launch_few(LoraArgs a, hipStream_t s) {
+    a.splits = k_ranges(a.K);
+    a.groups = (int)woq::ceil_div(a.R, 16);
+    hipError_t e = launch(reinterpret_cast<const void*>(&lora_down_kernel<4, 1, 4, true>),
+                          dim3((unsigned)a.b, (unsigned)(a.nseg * a.groups), (unsigned)a.splits), 256, 0, s, a);
+    if (e != hipSuccess) return e;
+    const unsigned tiles = count_tiles(a, 64);
+    return launch(reinterpret_cast<const void*>(&lora_up_rows_kernel), dim3(tiles, (unsigned)woq::ceil_div(a.b, 16)), 256,
+                  (size_t)16 * (woq::round_up(a.R, 16) + 4) * 4, s, a);
+}
+
+template <int RT, int D>
+hipError_t launch_many(LoraArgs a, hipStream_t s) {
+    constexpr int SLOTS = 2;
+    a.groups = (int)woq::ceil_div(a.R, 16 * RT);
+    a.exps = reinterpret_cast<int32_t*>(a.h) + (int64_t)a.b * a.nseg * a.groups * 16 * RT;
+    hipError_t e = launch(reinterpret_cast<const void*>(&lora_down_kernel<8, RT, D, false>),
+                          dim3((unsigned)woq::ceil_div(a.b, 32), (unsigned)(a.nseg * a.groups), SLOTS), 512, 0, s, a);
+    if (e != hipSuccess) return e;
+    // tiles a workgroup goes through: more where there is work enough for the device
+    const int64_t rows = woq::ceil_div(a.b, 64);
+    a.per = (int)std::max<int64_t>(1, std::min<int64_t>(4, rows * woq::ceil_div(a.N, 64) / 1024));
+    return launch(a.groups > 1 ? reinterpret_cast<const void*>(&lora_up_wide_kernel<RT, RT == 4>)
+                               : reinterpret_cast<const void*>(&lora_up_wide_kernel<RT, false>),
+                  dim3(count_tiles(a, 64 * a.per), (unsigned)rows), 256, 0, s, a);
 }
 
 int check_lora_w(const woq_lora_w* w) {
@@ -415,9 +753,11 @@ extern "C" {
 int64_t woq_lora_workspace(const woq_lora_w* w, int64_t b) {
     if (check_lora_w(w) != WOQ_OK || b < 0) return WOQ_EINVAL;
     if ((w->R & 7) || w->R > WOQ_LORA_MAX_R || b > WOQ_LORA_MAX_ROWS) return WOQ_EUNSUPPORTED;
-    // no less for more rows, so that one workspace serves every smaller batch
-    const int64_t rows = std::min<int64_t>(LEADER_SPLITS * b, std::max<int64_t>(LEADER_SPLITS * LEADER_ROWS, WINDOW_SPLITS * b));
-    return std::max<int64_t>(16, rows * w->nseg * w->R * 4);
+    // few rows: the ranges' sums; many: halves and an exponent for each group
+    // of ranks.  No less for more rows, so one workspace serves smaller batches.
+    const int64_t few = std::min<int64_t>(b, LEADER_ROWS) * LEADER_SPLITS * w->nseg * w->R * 4;
+    const int64_t width = 16 * rank_tiles(w->R), many = b * w->nseg * woq::ceil_div(w->R, width) * (width * 4 + 4);
+    return std::max<int64_t>(16, b <= LEADER_ROWS ? few : std::max(few, many));
 }
 
 int woq_lora_add(const woq_lora_w* w, const uint16_t* x, int64_t ldx, const int32_t* ids, int64_t b,
@@ -456,16 +796,16 @@ int woq_lora_add(const woq_lora_w* w, const uint16_t* x, int64_t ldx, const int3
     a.R = w->R;
     a.count = w->count;
     a.nseg = w->nseg;
-    a.splits = k_ranges(a.b, a.K, a.R, a.nseg);
+    a.splits = a.groups = a.per = 1;
+    a.exps = nullptr;
     a.vec = woq::aligned16(y) && (ldy & 7) == 0 && (!base || (woq::aligned16(base) && (ldbase & 7) == 0));
     for (int i = 0; i < WOQ_MAX_SEGMENTS; ++i) a.seg_end[i] = i < w->nseg ? (int)w->seg_end[i] : (int)w->N;
     hipStream_t s = (hipStream_t)stream;
     hipError_t e;
-    if (b <= LEADER_ROWS) e = launch_down<4, 1, true>(a, s);
-    else if (rank_tiles(a.b, a.R) == 1) e = launch_down<8, 1, false>(a, s);
-    else if (rank_tiles(a.b, a.R) == 2) e = launch_down<8, 2, false>(a, s);
-    else e = launch_down<8, 4, false>(a, s);
-    if (e == hipSuccess) e = b <= 64 ? launch_up<1, 1, 8>(a, s) : launch_up<4, 4, 1>(a, s);
+    if (b <= LEADER_ROWS) e = launch_few(a, s);
+    else if (rank_tiles(a.R) == 1) e = launch_many<1, 4>(a, s);
+    else if (rank_tiles(a.R) == 2) e = launch_many<2, 2>(a, s);
+    else e = launch_many<4, 2>(a, s);
     if (e != hipSuccess) {
         woq::set_hip_error((int)e);
         return WOQ_EHIP;

@@ -69,6 +69,7 @@ class LoraW(ctypes.Structure):
 FMT_INT8, FMT_INT4O = 1, 2
 
 _LIB = None
+_torch = None       # torch, imported with the library
 
 _SIGS = {
     "woq_strerror": (ctypes.c_char_p, [c_int]),
@@ -145,7 +146,7 @@ EXPORTS = tuple(_SIGS)
 
 
 def _lib():
-    global _LIB
+    global _LIB, _torch
     if _LIB is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"libwoq.so is not built ({LIB_PATH}); run "
@@ -154,7 +155,8 @@ def _lib():
         # the library binds to that runtime instead of loading a second one
         # (with two in one process the GPU was reported missing on MI355X)
         try:
-            import torch  # noqa: F401
+            import torch
+            _torch = torch
         except ImportError:
             pass
         lib = ctypes.CDLL(LIB_PATH)
@@ -480,11 +482,11 @@ def woq_qgemm_int4o(w: Int4oW, xp, y, stream=None, b: int | None = None):
 
 # ------------------------------------- device ops: 8-bit rows and adapters
 
-def _rows(t, what: str, dtype: str, b: int, width: int):
+def _rows(t, what: str, dtype, b: int, width: int):
     """(address, leading dimension) of a row-major device buffer that must
     hold b rows of ``width`` values; rows may be apart (t.stride(0))."""
-    if str(t.dtype) != dtype or t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{what}: expected a 2-D {dtype} tensor on the GPU")
+    if t.dtype is not dtype or t.dim() != 2:
+        raise ValueError(f"{what}: expected a 2-D {dtype} tensor, got {t.dim()}-D {t.dtype}")
     rows, cols = t.shape
     ld, step = t.stride()
     if rows < b or cols < width or (step != 1 and cols > 1):
@@ -495,27 +497,33 @@ def _rows(t, what: str, dtype: str, b: int, width: int):
     return t.data_ptr(), ld
 
 
-def _vector(t, what: str, dtype: str, n: int):
+def _vector(t, what: str, dtype, n: int):
     """Address of a contiguous device vector of at least n values."""
-    if str(t.dtype) != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of {n} values on the GPU")
+    if t.dtype is not dtype or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of {n} values, got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _call(name: str, stream, first, others, *args):
-    """Call the C entry point on ``stream``, or on the current stream of the
-    device that holds the tensors, with that device current."""
-    import torch
-    dev = first.device
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
-    fn = getattr(_lib(), name)
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)), name)
+def _call(name: str, stream, tensors, *args):
+    """Call the C entry point ``name`` on ``stream``, or on the current stream
+    of the device that holds the tensors (None entries aside), with that device
+    current."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name}: tensors on {tensors[0].device} and {t.device}")
+    if dev < 0:
+        raise ValueError(f"{name}: the tensors are not on the GPU")
+    # torch.cuda.current_stream() builds a Stream object, 2.7 us a call; this
+    # reads the same handle
+    raw = _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if dev == _torch._C._cuda_getDevice():
+        status = getattr(_LIB, name)(*args, raw)
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)), name)
+        with _torch.cuda.device(dev):
+            status = getattr(_LIB, name)(*args, raw)
+    if status != WOQ_OK:
+        raise WoqError(status, name)
 
 
 def woq_add_rmsnorm(x, weight, eps: float, res=None, sum_out=None, y=None, q=None, q_scale=None,
@@ -524,36 +532,42 @@ def woq_add_rmsnorm(x, weight, eps: float, res=None, sum_out=None, y=None, q=Non
     and the gain ``weight`` (fp16 [K]; None: no norm, then K defaults to x's
     width) and write any of: the sum (fp16), y (fp16), the 8-bit rows q (int8
     [b, >= round_up(K, 16)]) with their scales q_scale (fp32 [b])."""
-    b = x.shape[0] if b is None else b
+    _lib()
+    half = _torch.float16
+    if b is None:
+        b = x.shape[0]
     if K is None:
         K = x.shape[1] if weight is None else weight.shape[0]
     if (q is None) != (q_scale is None):
         raise ValueError("q and q_scale go together")
-    half, nothing = "torch.float16", (None, 0)
-    xp = _rows(x, "x", half, b, K)
-    rp = nothing if res is None else _rows(res, "res", half, b, K)
-    sp = nothing if sum_out is None else _rows(sum_out, "sum_out", half, b, K)
-    yp = nothing if y is None else _rows(y, "y", half, b, K)
-    qp = nothing if q is None else _rows(q, "q", "torch.int8", b, -(-K // 16) * 16)
-    _call("woq_add_rmsnorm", stream, x, (weight, res, sum_out, y, q, q_scale), *xp, *rp,
-          None if weight is None else _vector(weight, "weight", half, K), offset, eps, b, K, *sp, *yp, *qp,
-          None if q is None else _vector(q_scale, "q_scale", "torch.float32", b))
+    xp, ldx = _rows(x, "x", half, b, K)
+    wp = None if weight is None else _vector(weight, "weight", half, K)
+    rp, ldr = (None, 0) if res is None else _rows(res, "res", half, b, K)
+    sp, lds = (None, 0) if sum_out is None else _rows(sum_out, "sum_out", half, b, K)
+    yp, ldy = (None, 0) if y is None else _rows(y, "y", half, b, K)
+    qp, ldq, qs = None, 0, None
+    if q is not None:
+        qp, ldq = _rows(q, "q", _torch.int8, b, -(-K // 16) * 16)
+        qs = _vector(q_scale, "q_scale", _torch.float32, b)
+    _call("woq_add_rmsnorm", stream, (x, weight, res, sum_out, y, q, q_scale), xp, ldx, rp, ldr, wp, offset, eps, b, K,
+          sp, lds, yp, ldy, qp, ldq, qs)
 
 
 def woq_qgemm_int8_a8(w: Int8W, xq, xs, y, stream=None, b: int | None = None):
     """y (fp16 [b, >= N]) = an INT8 weight times the 8-bit rows xq (int8 [b, >=
     round_up(K, 16)]) with their scales xs (fp32 [b]), as woq_add_rmsnorm
     writes them."""
-    b = xq.shape[0] if b is None else b
-    xp, ldq = _rows(xq, "xq", "torch.int8", b, -(-w.K // 16) * 16)
-    yp, ldy = _rows(y, "y", "torch.float16", b, w.N)
-    _call("woq_qgemm_int8_a8", stream, xq, (xs, y), ctypes.byref(w), xp, ldq,
-          _vector(xs, "xs", "torch.float32", b), b, yp, ldy)
+    _lib()
+    if b is None:
+        b = xq.shape[0]
+    xp, ldq = _rows(xq, "xq", _torch.int8, b, -(-w.K // 16) * 16)
+    yp, ldy = _rows(y, "y", _torch.float16, b, w.N)
+    _call("woq_qgemm_int8_a8", stream, (xq, xs, y), w, xp, ldq, _vector(xs, "xs", _torch.float32, b), b, yp, ldy)
     return y
 
 
 def woq_lora_workspace(w: LoraW, b: int) -> int:
-    """Bytes of the workspace of woq_lora_add for batches of b rows."""
+    """Bytes of the workspace of woq_lora_add for batches of up to b rows."""
     n = _lib().woq_lora_workspace(ctypes.byref(w), b)
     if n < 0:
         _check(n, "woq_lora_workspace")
@@ -564,16 +578,17 @@ def woq_lora_add(w: LoraW, x, ids, base, y, workspace, stream=None, b: int | Non
     """y (fp16 [b, >= N]) = base (fp16, or None for zeros; may be y) + each
     row's own adapter ids[r] (int32) of the pool ``w`` (DeviceLora.desc)
     applied to x (fp16 [b, >= K]); rows with an id outside the pool keep base."""
-    b = x.shape[0] if b is None else b
-    half = "torch.float16"
-    xp = _rows(x, "x", half, b, w.K)
-    bp = (None, 0) if base is None else _rows(base, "base", half, b, w.N)
-    yp = _rows(y, "y", half, b, w.N)
+    _lib()
+    half = _torch.float16
+    if b is None:
+        b = x.shape[0]
+    xp, ldx = _rows(x, "x", half, b, w.K)
+    bp, ldb = (None, 0) if base is None else _rows(base, "base", half, b, w.N)
+    yp, ldy = _rows(y, "y", half, b, w.N)
     if not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous")
-    _call("woq_lora_add", stream, x, (ids, base, y, workspace), ctypes.byref(w), *xp,
-          _vector(ids, "ids", "torch.int32", b), b, *bp, *yp, workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+    _call("woq_lora_add", stream, (x, ids, base, y, workspace), w, xp, ldx, _vector(ids, "ids", _torch.int32, b), b,
+          bp, ldb, yp, ldy, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return y
 
 
@@ -645,7 +660,8 @@ class DeviceLora:
     stream holds by then."""
 
     def __init__(self, A, B, scale, rank=None, K: int | None = None, segments=None):
-        half = "torch.float16"
+        _lib()
+        half = _torch.float16
         if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0]:
             raise ValueError("A is [count, S * R, >= K], B is [count, N, R]")
         count, N, R = B.shape
@@ -658,12 +674,12 @@ class DeviceLora:
             raise ValueError(f"K = {K}, but A's rows hold {A.shape[2]} values")
         self.A, self.B, self.scale, self.rank = A, B, scale, rank
         self.count, self.N, self.R, self.K = count, N, R, K
+        if any(t is not None and (t.device != A.device or not t.is_cuda) for t in (A, B, scale, rank)):
+            raise ValueError("the pool's tensors have to be on one GPU")
         d = self.desc = LoraW()
         d.A, d.B = _vector(A, "A", half, 0), _vector(B, "B", half, 0)
-        d.scale = _vector(scale, "scale", "torch.float32", count)
-        d.rank = None if rank is None else _vector(rank, "rank", "torch.int32", count)
-        if any(t is not None and t.device != A.device for t in (B, scale, rank)):
-            raise ValueError("the pool's tensors are on different devices")
+        d.scale = _vector(scale, "scale", _torch.float32, count)
+        d.rank = None if rank is None else _vector(rank, "rank", _torch.int32, count)
         d.N, d.K, d.lda, d.R, d.count, d.nseg = N, K, A.shape[2], R, count, len(segments)
         for i, e in enumerate(segments):
             d.seg_end[i] = e
