@@ -25,7 +25,7 @@ struct A8Args {
     int64_t ldq, ldy, b;
     int N, K, Kd, nseg;
     int tiles_m, tiles_n, GM; // tiles of activation and weight rows; token tiles side by side
-    int vec;                  // y may be written in 16-byte pieces
+    int vec;                  // y may be written in 8-byte pieces
     int seg_end[WOQ_MAX_SEGMENTS];
     float seg_scale[WOQ_MAX_SEGMENTS];
 };
@@ -39,7 +39,7 @@ __device__ __forceinline__ float row_scale(const A8Args& a, int n) {
 }
 
 // One workgroup: BM activation rows x BN weight rows, WM x WN x WK waves.
-template <int BM, int BN, int WM, int WN, int WK, int KS, int PF>
+template <int BM, int BN, int WM, int WN, int WK, int KS, int PF, bool EARLY>
 __global__ __launch_bounds__(64 * WM * WN * WK) void qgemm_int8_a8_lds(A8Args a) {
     constexpr int T = 64 * WM * WN * WK;
     constexpr int CPS = KS / 16;                       // 16-byte chunks of a row per stage
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void qgemm_int8_a8_lds(A8Args a)
     // chunk p of a stage: row p / CPS, chunk p % CPS; it lies in LDS at chunk
     // position (p % CPS) ^ swizzle(row), so that the eight lanes of a fragment
     // read that go together fall on different banks
-    auto swz_w = [](int row) { return (row & 3) | ((row >> 2) / NT & 1) << 2; };
+    auto swz_w = [](int row) { return row / NT & 7; };
     auto swz_x = [](int row) { return row & 7; };
     uint4 sw[PF][LW], sx[PF][LX];
     auto load = [&](uint4 (&lw)[LW], uint4 (&lx)[LX], int s) {
@@ -118,55 +118,72 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void qgemm_int8_a8_lds(A8Args a)
     for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
-    // weight row of fragment j, lane row m: the 4 NT rows of a lane's results
-    // are adjacent, so its part of an output row is one piece
-    const int wrow = wn * 16 * NT + (m >> 2) * 4 * NT + (m & 3), xrow = wm * 16 * MT + m;
-    auto compute = [&](const uint8_t* buf) {
+    // the activations are the first operand and the weights the second, with
+    // column m of tile j the weight row NT m + j: a lane then has NT adjacent
+    // outputs of four rows, and the 16 lanes of a row 16 NT adjacent ones
+    const int wrow = wn * 16 * NT + NT * m, xrow = wm * 16 * MT + m;
+    i32x4 wf[NT], xf[MT];
+    auto fragments = [&](const uint8_t* buf, int t) {
+        const int ch = (wk * STEPS + t) * 4 + c;
 #pragma unroll
-        for (int t = 0; t < STEPS; ++t) {
-            const int ch = (wk * STEPS + t) * 4 + c;
-            i32x4 wf[NT], xf[MT];
+        for (int j = 0; j < NT; ++j)
+            wf[j] = *(const __attribute__((address_space(3))) i32x4*)(buf + (wrow + j) * KS + 16 * (ch ^ swz_w(wrow + j)));
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int row = wrow + 4 * j;
-                wf[j] = *(const __attribute__((address_space(3))) i32x4*)(buf + row * KS + 16 * (ch ^ swz_w(row)));
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const int row = xrow + 16 * i;
-                xf[i] = *(const __attribute__((address_space(3))) i32x4*)(buf + (BN + row) * KS + 16 * (ch ^ swz_x(row)));
-            }
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    acc[j][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[j], xf[i], acc[j][i], 0, 0, 0);
+        for (int i = 0; i < MT; ++i) {
+            const int row = xrow + 16 * i;
+            xf[i] = *(const __attribute__((address_space(3))) i32x4*)(buf + (BN + row) * KS + 16 * (ch ^ swz_x(row)));
         }
     };
+    auto multiply = [&]() {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) acc[j][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xf[i], wf[j], acc[j][i], 0, 0, 0);
+    };
 
+    // Register set u holds the stages that are u modulo PF, read PF turns ahead
+    // (stages past the end read the first chunk over and over: loads that always
+    // happen let every wait count exactly).  In turn s, stage s is multiplied
+    // out of its buffer and stage s + 1 goes into the other one, which was last
+    // read before the previous barrier:
+    //   EARLY: between the first operand reads and the products, which then hide
+    //   the writes (where the products of a turn take longer than the loads);
+    //   else after the products, so that the loads have that much longer.
     const int S = (a.Kd + KS - 1) / KS;
-    uint8_t *b0 = lds, *b1 = lds + STAGE;
-    static_assert(PF == 1 || PF % 2 == 0, "the buffers alternate within one turn of the register sets");
+    auto buf = [&](int s) { return lds + (s & 1) * STAGE; };
+    static_assert(PF == 1 || PF % 2 == 0, "the buffers alternate within one round of the register sets");
 #pragma unroll
     for (int u = 0; u < PF; ++u) load(sw[u], sx[u], u);
-    store(sw[0], sx[0], 0, b0);
+    store(sw[0], sx[0], 0, buf(0));
+    if constexpr (EARLY) load(sw[0], sx[0], PF);
     __syncthreads();
-    if constexpr (PF == 1) {
-        for (int s = 0; s < S; ++s) {
-            if (s + 1 < S) load(sw[0], sx[0], s + 1);
-            compute(s & 1 ? b1 : b0);
-            if (s + 1 < S) store(sw[0], sx[0], s + 1, s & 1 ? b0 : b1);
-            __syncthreads();
+    // set: of stage s + 1; own: of stage s
+    auto turn = [&](int s, int set, int own, const uint8_t* from, uint8_t* to) {
+        if constexpr (!EARLY) load(sw[own], sx[own], s + PF);
+        // only the products of turns past the end are left out, not their loads
+        if (PF == 1 || s < S) fragments(from, 0);
+        if constexpr (EARLY) {
+            store(sw[set], sx[set], s + 1, to);
+            load(sw[set], sx[set], s + 1 + PF);
         }
+        if (PF == 1 || s < S) {
+            multiply();
+#pragma unroll
+            for (int t = 1; t < STEPS; ++t) {
+                fragments(from, t);
+                multiply();
+            }
+        }
+        if constexpr (!EARLY) store(sw[set], sx[set], s + 1, to);
+        __syncthreads();
+    };
+    if constexpr (PF == 1) {
+        for (int s = 0; s < S; ++s) turn(s, 0, 0, buf(s), buf(s + 1));
     } else {
         for (int s = 0; s < S; s += PF) {
 #pragma unroll
-            for (int u = 0; u < PF; ++u) {
-                load(sw[u], sx[u], s + u + PF);
-                if (s + u < S) compute(u & 1 ? b1 : b0);
-                store(sw[(u + 1) % PF], sx[(u + 1) % PF], s + u + 1, u & 1 ? b0 : b1);
-                __syncthreads();
-            }
+            for (int u = 0; u < PF; ++u)
+                turn(s + u, (u + 1) % PF, u, buf(u), buf(u + 1));
         }
     }
 
@@ -191,64 +208,83 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void qgemm_int8_a8_lds(A8Args a)
                     acc[j][i] += *(const __attribute__((address_space(3))) i32x4*)&red[((g * WM * WN + wave) * NT * MT + j * MT + i) * 64 + lane];
     }
 
-    const int nl = n0 + wn * 16 * NT + c * 4 * NT;     // this lane's 4 NT outputs
+    const int nl = n0 + wn * 16 * NT + NT * m;         // this lane's NT outputs
     if (nl >= a.N) return;
-    float scale[4 * NT];
+    float scale[NT];
 #pragma unroll
-    for (int j = 0; j < 4 * NT; ++j) scale[j] = row_scale(a, nl + j);
+    for (int j = 0; j < NT; ++j) scale[j] = row_scale(a, nl + j);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int row = xrow + 16 * i;
-        if (row >= rows_x) continue;
-        const float sx1 = *gptr(a.qs + r0 + row);
-        uint16_t* yr = a.y + (r0 + row) * a.ldy + nl;
-        uint32_t h[2 * NT];
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int e = 0; e < 4; ++e) {
+            const int row = wm * 16 * MT + 16 * i + 4 * c + e;
+            if (row >= rows_x) continue;
+            const float sx1 = *gptr(a.qs + r0 + row);
+            uint16_t* yr = a.y + (r0 + row) * a.ldy + nl;
+            uint16_t h[NT];
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                h[2 * j + e] = (uint32_t)f_to_h((float)acc[j][i][2 * e] * (sx1 * scale[4 * j + 2 * e])) |
-                               (uint32_t)f_to_h((float)acc[j][i][2 * e + 1] * (sx1 * scale[4 * j + 2 * e + 1])) << 16;
-        if (a.vec && nl + 4 * NT <= a.N) {
-            if constexpr (NT % 2 == 0) {
-#pragma unroll
-                for (int j = 0; j < NT; j += 2)
-                    gstore_u4(reinterpret_cast<uint4*>(yr + 4 * j), make_uint4(h[2 * j], h[2 * j + 1], h[2 * j + 2], h[2 * j + 3]));
+            for (int j = 0; j < NT; ++j) h[j] = f_to_h((float)acc[j][i][e] * (sx1 * scale[j]));
+            if (NT == 4 && a.vec && nl + 4 <= a.N) {
+                *(__attribute__((address_space(1))) u32x2*)yr = u32x2{h[0] | (uint32_t)h[1 % NT] << 16, h[2 % NT] | (uint32_t)h[3 % NT] << 16};
+            } else if (NT == 2 && a.vec && nl + 2 <= a.N) {
+                *gptr(reinterpret_cast<uint32_t*>(yr)) = h[0] | (uint32_t)h[1 % NT] << 16;
             } else {
 #pragma unroll
-                for (int j = 0; j < NT; ++j) *(__attribute__((address_space(1))) u32x2*)(yr + 4 * j) = u32x2{h[2 * j], h[2 * j + 1]};
+                for (int j = 0; j < NT; ++j)
+                    if (nl + j < a.N) *gptr(yr + j) = h[j];
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4 * NT; ++j)
-                if (nl + j < a.N) *gptr(yr + j) = (uint16_t)(h[j >> 1] >> (16 * (j & 1)));
         }
-    }
 }
 
-template <int BM, int BN, int WM, int WN, int WK, int KS, int PF>
+template <int BM, int BN, int WM, int WN, int WK, int KS, int PF, bool EARLY>
 hipError_t launch_lds(A8Args a, hipStream_t s) {
     a.tiles_m = (int)woq::ceil_div(a.b, BM);
     a.tiles_n = (int)woq::ceil_div(a.N, BN);
     a.GM = 8;
     void* argv[] = {&a};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&qgemm_int8_a8_lds<BM, BN, WM, WN, WK, KS, PF>),
+    return hipLaunchKernel(reinterpret_cast<const void*>(&qgemm_int8_a8_lds<BM, BN, WM, WN, WK, KS, PF, EARLY>),
                            dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n)), dim3(64 * WM * WN * WK), argv, 0, s);
 }
 
-hipError_t launch_a8(const A8Args& a, hipStream_t s) {
-    if (a.b <= 16) {
-        if (a.N > 16384) return launch_lds<16, 64, 1, 2, 4, 512, 1>(a, s);
-        return launch_lds<16, 16, 1, 1, 8, 512, 2>(a, s);
+// Tiles from small to large, each with the fastest division into waves, stage
+// length and prefetch depth of a sweep on MI355X (rows 1 to 2048, weights
+// 8192 x 3584, 28672 x 3584, 3584 x 14336, 3584 x 4096 and 1024 x 1024).
+struct A8Plan {
+    int bm, bn;
+    hipError_t (*launch)(A8Args, hipStream_t);
+};
+const A8Plan PLANS[] = {
+    {16, 16, &launch_lds<16, 16, 1, 1, 8, 512, 2, true>},
+    {16, 32, &launch_lds<16, 32, 1, 2, 4, 512, 2, false>},
+    {16, 64, &launch_lds<16, 64, 1, 4, 2, 256, 2, true>},
+    {32, 32, &launch_lds<32, 32, 1, 2, 4, 512, 2, false>},
+    {16, 128, &launch_lds<16, 128, 1, 4, 2, 256, 2, false>},
+    {32, 64, &launch_lds<32, 64, 1, 2, 4, 256, 2, false>},
+    {64, 64, &launch_lds<64, 64, 2, 2, 4, 256, 2, true>},
+    {64, 128, &launch_lds<64, 128, 1, 4, 2, 128, 4, false>},
+    {128, 128, &launch_lds<128, 128, 2, 4, 1, 128, 2, false>},
+    {128, 256, &launch_lds<128, 256, 2, 4, 1, 128, 2, true>},
+    {256, 256, &launch_lds<256, 256, 2, 4, 1, 128, 1, true>},
+};
+
+// The smallest tile that still gives at most one workgroup to a compute unit,
+// else the largest: a second round of workgroups cost more than the reuse
+// that a larger tile adds (256 rows of 8192 x 3584: 64 x 128 tiles 16.5 us,
+// 64 x 64 17.3; 1021 rows: 128 x 256 36.8, 128 x 128 38.9; 509 rows of
+// 28672 x 3584: 256 x 256 60.9, 128 x 256 75.5), and idle compute units cost
+// more than that reuse gains (256 rows of 3584 x 14336: 64 x 64 33.4 us,
+// 64 x 128, half the workgroups, 46).  Of two tiles of one size, the one with more
+// workgroups.
+const A8Plan& choose_plan(const A8Args& a) {
+    const int64_t cus = woq::compute_units();
+    const A8Plan* best = nullptr;
+    int64_t best_tiles = 0;
+    for (const A8Plan& p : PLANS) {
+        const int64_t tiles = woq::ceil_div(a.b, p.bm) * woq::ceil_div(a.N, p.bn);
+        if (best && p.bm * p.bn > best->bm * best->bn) break;
+        if (tiles <= cus && (!best || tiles > best_tiles)) best = &p, best_tiles = tiles;
     }
-    if (a.b <= 64) {
-        if (a.N > 16384) return launch_lds<64, 128, 2, 4, 1, 128, 4>(a, s);
-        return launch_lds<64, 16, 1, 1, 8, 512, 2>(a, s);
-    }
-    if (a.b <= 256) return launch_lds<64, 64, 2, 2, 2, 128, 4>(a, s);
-    if (a.b <= 512) return launch_lds<64, 128, 1, 4, 2, 128, 2>(a, s);
-    if (a.b <= 1024) return launch_lds<128, 256, 2, 4, 1, 128, 2>(a, s);
-    return launch_lds<256, 256, 4, 4, 1, 128, 1>(a, s);
+    return best ? *best : PLANS[sizeof(PLANS) / sizeof(PLANS[0]) - 1];
 }
 
 }  // namespace
@@ -265,7 +301,9 @@ extern "C" int woq_qgemm_int8_a8(const woq_int8_w* w, const int8_t* xq, int64_t 
     if (!w->codes || !xq || !xs || !y) return WOQ_EINVAL;
     if (!woq::aligned16(w->codes) || !woq::aligned16(xq) || (ldq & 15) || ((uintptr_t)xs & 3u) || ((uintptr_t)y & 1u))
         return WOQ_EALIGN;
-    if (w->K > WOQ_A8_MAX_K || w->N > (int64_t)INT32_MAX - 64 || b > 16 * 65535) return WOQ_EUNSUPPORTED;
+    if (w->K > WOQ_A8_MAX_K || w->N > (int64_t)INT32_MAX - 512 || b > (int64_t)INT32_MAX - 512 ||
+        woq::ceil_div(b, 256) * woq::ceil_div(w->N, 256) > INT32_MAX)
+        return WOQ_EUNSUPPORTED;
     A8Args a;
     a.codes = static_cast<const uint8_t*>(w->codes);
     a.q = xq;
@@ -282,8 +320,8 @@ extern "C" int woq_qgemm_int8_a8(const woq_int8_w* w, const int8_t* xq, int64_t 
         a.seg_end[i] = i < w->nseg ? (int)w->seg_end[i] : (int)w->N;
         a.seg_scale[i] = i < w->nseg ? w->seg_scale[i] : 0.0f;
     }
-    a.vec = woq::aligned16(y) && (ldy & 7) == 0;
-    const hipError_t e = launch_a8(a, (hipStream_t)stream);
+    a.vec = ((uintptr_t)y & 7u) == 0 && (ldy & 3) == 0;
+    const hipError_t e = choose_plan(a).launch(a, (hipStream_t)stream);
     if (e != hipSuccess) {
         woq::set_hip_error((int)e);
         return WOQ_EHIP;

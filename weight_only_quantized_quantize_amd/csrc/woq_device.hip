@@ -51,9 +51,24 @@ void set_launch_events(void* start, void* stop) {
 
 extern "C" int woq_last_hip_error(void) { return woq::g_last_hip_error; }
 
+namespace woq {
+int compute_units() {
+    static std::atomic<int> cached[64];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+    int n = cached[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1) n = 256;
+        cached[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+}  // namespace woq
+
 namespace {
 
 using namespace woqk;
+using woq::compute_units;
 
 // ------------------------------------------------------------ permute/split
 
@@ -1292,8 +1307,6 @@ int launch_status(hipError_t e) {
     return WOQ_OK;
 }
 
-int compute_units();
-
 // Tiles per workgroup and waves per tile of the vector kernel (measured on
 // MI355X over the 3B- and 70B-shaped products): narrow products split each
 // tile's groups over four waves so that enough loads are in flight on every
@@ -1355,19 +1368,6 @@ hipError_t launch_int4o_tile_b(const Int4oArgs& a, const GatherArgs& ga, int64_t
 template <int B>
 hipError_t launch_int8_valu(const Int8Args& a, int quads, hipStream_t s) {
     return launch_kernel(qgemv_int8_valu<B>, dim3(quads), dim3(64), 0, s, a);
-}
-
-// Compute units of the current device, read once per device.
-int compute_units() {
-    static std::atomic<int> cached[64];
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-    int n = cached[dev].load(std::memory_order_relaxed);
-    if (n == 0) {
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1) n = 256;
-        cached[dev].store(n, std::memory_order_relaxed);
-    }
-    return n;
 }
 
 // The widest matrix-core plans put eight tiles (each of rb tiles per wave) in

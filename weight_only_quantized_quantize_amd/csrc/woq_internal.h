@@ -21,6 +21,9 @@ void set_hip_error(int code);
 // reports); set by the runner's timing pass around one launch.
 void set_launch_events(void* start, void* stop);
 
+// Compute units of the current device (read once per device).
+int compute_units();
+
 // Launch step i of a stack with the given step contents (the entry itself or
 // a copy whose weight pointers were moved); argument checks as woq_stack_run.
 int stack_run_step(woq_stack* st, int64_t i, const woq_stack_step* s, const uint16_t* x, uint16_t* y, int64_t b,
