@@ -154,6 +154,11 @@ __global__ __launch_bounds__(T) void add_rmsnorm_kernel(NormArgs a) {
         const bool bad = !(vmax < __builtin_huge_valf());
         const float scale = bad ? __builtin_nanf("") : vmax / 127.0f;
         const bool zero = bad || scale == 0.0f;
+        // v / scale by a reciprocal is off by less than 127 * 2^-22; where that
+        // could decide the rounding, the division decides (and where the
+        // reciprocal overflows)
+        const float inv = zero ? 0.0f : 1.0f / scale;
+        const bool exact = !(inv < __builtin_huge_valf());
         int8_t* qr = a.q + r * a.ldq;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
@@ -161,7 +166,10 @@ __global__ __launch_bounds__(T) void add_rmsnorm_kernel(NormArgs a) {
             uint32_t w[2] = {0, 0};
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float d = zero ? 0.0f : fminf(fmaxf(rintf(v[p][j] / scale), -127.0f), 127.0f);
+                const float f = v[p][j] * inv;
+                float d = rintf(f);
+                if (exact || fabsf(f - d) > 0.4999f) d = rintf(v[p][j] / scale);
+                d = zero ? 0.0f : fminf(fmaxf(d, -127.0f), 127.0f);
                 w[j >> 2] |= ((uint32_t)(int)d & 0xFFu) << (8 * (j & 3));
             }
             // whole 16-byte pieces of the row are written, zeros past K
@@ -220,7 +228,14 @@ extern "C" int woq_add_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* r
     const int chunks = (int)woq::ceil_div(K, 16) * 2;    // whole 16-byte pieces of the codes
     hipStream_t s = (hipStream_t)stream;
     hipError_t e;
-    if (chunks <= 256) e = launch<256, 1>(a, b, s);
+    // one chunk to a thread as long as a row fits a workgroup: 4096 rows of 8192,
+    // all outputs, 57.9 us (5.2 TB/s, the rate of a large copy) with 1024 threads,
+    // 61.2 and 65.3 with two and four chunks to a thread; 1021 rows of 3584 9.1 us
+    // with 512, 11.7 with 1024; 2048 rows of 16384 51.5 us with 1024, 53.6 with 512
+    if (chunks <= 64) e = launch<64, 1>(a, b, s);
+    else if (chunks <= 128) e = launch<128, 1>(a, b, s);
+    else if (chunks <= 256) e = launch<256, 1>(a, b, s);
+    else if (chunks <= 512) e = launch<512, 1>(a, b, s);
     else if (chunks <= 1024) e = launch<1024, 1>(a, b, s);
     else if (chunks <= 2048) e = launch<1024, 2>(a, b, s);
     else if (chunks <= 4096) e = launch<1024, 4>(a, b, s);
