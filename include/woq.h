@@ -566,6 +566,25 @@ int woq_stack_run(woq_stack* st, const uint16_t* const* inputs, uint16_t* const*
                   void* stream);
 
 /*
+ * woq_stack_run with low-rank adapters beside its steps: after step i has
+ * written outputs[out_slot], woq_lora_add adds each row's own adapter of the
+ * pool adapters[i] (null: none beside this step), applied to the step's input,
+ * in place, before the next step runs - so a step that reads an earlier step's
+ * output sees it adapted.  adapters holds an entry for every step; a pool's N and
+ * K are those of its step (WOQ_EINVAL otherwise), its segments may differ from
+ * the weight's.  ids int32 [b] and the pools as for woq_lora_add, whose limits
+ * hold for every adapted step: K a multiple of 8, the input 16-byte aligned.
+ * workspace: woq_stack_lora_workspace bytes, owned by the caller; runs that
+ * share it, or the runner, must not overlap.  A step's input and output have to be
+ * different buffers where it has a pool.
+ */
+int woq_stack_run_lora(woq_stack* st, const uint16_t* const* inputs, uint16_t* const* outputs, int64_t b,
+                       const woq_lora_w* const* adapters, const int32_t* ids, void* workspace,
+                       int64_t workspace_bytes, void* stream);
+/* Bytes for batches of up to b rows, or a negative status. */
+int64_t woq_stack_lora_workspace(const woq_stack* st, const woq_lora_w* const* adapters, int64_t b);
+
+/*
  * Kernel launches of one woq_stack_run pass at batch b (a folded INT4O step
  * or an INT8 step is one launch, a permute-then-product INT4O step two, three
  * with the split-K reduction), assuming 16-byte aligned inputs.

@@ -530,6 +530,107 @@ def test_block_captured_and_replayed(gpu_lib, b):
         torch.cuda.synchronize()
 
 
+# ------------------------------------------------- adapters beside a stack's steps
+
+def small_stack(fmt, rng, dims):
+    """A chain of linears in one format; each step reads the one before it."""
+    steps, keep = [], []
+    for i, (N, K) in enumerate(dims):
+        W = (rng.standard_normal((N, K)) / np.sqrt(K)).astype(np.float32)
+        if fmt == "int8":
+            d = woq.DeviceInt8([woq.woq_quantize_int8(W)])
+            keep.append(d)
+            steps.append(woq.step_int8(d, i, i))
+        else:
+            g = woq.woq_int4o_geometry(K)
+            perm = O.global_perm(K, np.sort(rng.choice(K, g.n_out, replace=False)))
+            d, pd = woq.DeviceInt4o([woq.woq_quantize_int4o(W, perm, g.n_out)], g), dev(perm)
+            keep += [d, pd]
+            steps.append(woq.step_int4o(d, pd, i, i))
+    return steps, keep
+
+
+@pytest.mark.parametrize("fmt,b", [("int8", 1), ("int8", 7), ("int4o", 2), ("int4o", 40)])
+def test_stack_with_adapters_equals_its_steps(gpu_lib, fmt, b):
+    """A chain of three steps, adapters beside the first and the last: the bits of
+    running each step and woq_lora_add by hand, also on replays of a graph."""
+    import torch
+    case("stack adapters", fmt, b)
+    rng = np.random.default_rng(b)
+    dims = [(520, 256), (1000, 520), (264, 1000)]
+    steps, keep = small_stack(fmt, rng, dims)
+    pools = []
+    for i, (N, K) in enumerate(dims):
+        A, B, s, ends = lora_pool(4, N, K, 16, 2, rng)
+        pools.append(None if i == 1 else woq.DeviceLora(dev(A), dev(B), dev(s), K=K, segments=ends))
+    ids = dev(rng.integers(-1, 4, b).astype(np.int32))
+    x = dev(rng.standard_normal((b, 256)).astype(np.float16))
+    outs = [full(b, N, 7, "float16") for N, _ in dims]
+    st = woq.Stack(steps, b)
+    st.bind([x] + outs[:2], outs)
+    ws = torch.empty(st.lora_workspace(pools, b), dtype=torch.uint8, device="cuda")
+    st.run_lora(b, pools, ids, ws)
+    got = [host(o).copy() for o in outs]
+
+    hand = [full(b, N, 7, "float16") for N, _ in dims]
+    src = x
+    for step, pool, out in zip(steps, pools, hand):
+        step.in_slot = step.out_slot = 0
+        one = woq.Stack([step], b)
+        one.bind([src], [out])
+        one.run(b)
+        if pool is not None:
+            woq.woq_lora_add(pool.desc, src, ids, out, out, ws)
+        src = out
+    for g, h in zip(got, hand):
+        np.testing.assert_array_equal(g.view(np.uint16), host(h).view(np.uint16))
+
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        st.run_lora(b, pools, ids, ws)
+    for _ in range(3):
+        for o in outs:
+            o.fill_(3)
+        g.replay()
+        for o, h in zip(outs, got):
+            np.testing.assert_array_equal(host(o).view(np.uint16), h.view(np.uint16))
+    st.run(b)                                      # without adapters the rows without one agree
+    assert np.array_equal(host(outs[0])[host(ids) < 0], got[0][host(ids) < 0])
+    del keep
+
+
+def test_stack_with_adapters_refuses_before_the_first_launch(gpu_lib):
+    import torch
+    rng = np.random.default_rng(0)
+    dims = [(64, 128), (48, 64)]
+    steps, keep = small_stack("int8", rng, dims)
+    st = woq.Stack(steps, 4)
+    x, outs = full(4, 128, 1, "float16"), [full(4, N, 7, "float16") for N, _ in dims]
+    st.bind([x, outs[0]], outs)
+    ids = dev(np.zeros(4, np.int32))
+
+    def pool(N, K, R=16):
+        A, B, s, ends = lora_pool(2, N, K, R, 1, rng)
+        return woq.DeviceLora(dev(A), dev(B), dev(s), K=K, segments=ends)
+
+    good = pool(64, 128)
+    ws = torch.empty(st.lora_workspace([good, None], 4), dtype=torch.uint8, device="cuda")
+    for pools in ([None, pool(64, 64)], [None, pool(48, 128)]):           # N or K of another step
+        with pytest.raises(woq.WoqError) as e:
+            st.run_lora(4, pools, ids, ws)
+        assert e.value.status == woq.WOQ_EINVAL
+    with pytest.raises(woq.WoqError) as e:
+        st.run_lora(4, [None, pool(48, 64)], ids, ws[:16])
+    assert e.value.status == woq.WOQ_EINVAL
+    with pytest.raises(ValueError):
+        st.run_lora(4, [good], ids, ws)                                    # a pool per step
+    with pytest.raises(ValueError):
+        st.run_lora(4, [good, None], ids[:3], ws)
+    assert np.all(host(outs[0]) == 7) and np.all(host(outs[1]) == 7)       # nothing ran
+    del keep
+
+
 def test_empty_calls_are_no_ops(gpu_lib):
     blk = Block(2, 64, 48, 3)
     blk.y.fill_(5)

@@ -249,6 +249,10 @@ hipError_t launch_lds(A8Args a, hipStream_t s) {
 // Tiles from small to large, each with the fastest division into waves, stage
 // length and prefetch depth of a sweep on MI355X (rows 1 to 2048, weights
 // 8192 x 3584, 28672 x 3584, 3584 x 14336, 3584 x 4096 and 1024 x 1024).
+// The 64 x 128 tile has two: with one row of tiles the weights stream from HBM
+// and the loop with the fewest operand reads is ahead (61 rows of 28672 x 3584:
+// 23.5 us against 24.2), with several they come from L2 and two K halves side by
+// side are (256 rows of 8192 x 3584: 16.5 against 17.1).
 struct A8Plan {
     int bm, bn;
     hipError_t (*launch)(A8Args, hipStream_t);
@@ -261,7 +265,10 @@ const A8Plan PLANS[] = {
     {16, 128, &launch_lds<16, 128, 1, 4, 2, 256, 2, false>},
     {32, 64, &launch_lds<32, 64, 1, 2, 4, 256, 2, false>},
     {64, 64, &launch_lds<64, 64, 2, 2, 4, 256, 2, true>},
-    {64, 128, &launch_lds<64, 128, 1, 4, 2, 128, 4, false>},
+    {64, 128, [](A8Args a, hipStream_t s) {
+         return a.b <= 64 ? launch_lds<64, 128, 2, 4, 1, 128, 4, false>(a, s)
+                          : launch_lds<64, 128, 1, 4, 2, 128, 4, false>(a, s);
+     }},
     {128, 128, &launch_lds<128, 128, 2, 4, 1, 128, 2, false>},
     {128, 256, &launch_lds<128, 256, 2, 4, 1, 128, 2, true>},
     {256, 256, &launch_lds<256, 256, 2, 4, 1, 128, 1, true>},

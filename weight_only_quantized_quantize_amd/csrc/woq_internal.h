@@ -24,6 +24,11 @@ void set_launch_events(void* start, void* stop);
 // Compute units of the current device (read once per device).
 int compute_units();
 
+// The argument checks of woq_lora_add, in its order; nothing is launched.
+int lora_check(const woq_lora_w* w, const uint16_t* x, int64_t ldx, const int32_t* ids, int64_t b,
+               const uint16_t* base, int64_t ldbase, const uint16_t* y, int64_t ldy, const void* workspace,
+               int64_t workspace_bytes);
+
 // Launch step i of a stack with the given step contents (the entry itself or
 // a copy whose weight pointers were moved); argument checks as woq_stack_run.
 int stack_run_step(woq_stack* st, int64_t i, const woq_stack_step* s, const uint16_t* x, uint16_t* y, int64_t b,

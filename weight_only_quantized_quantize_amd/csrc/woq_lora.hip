@@ -748,6 +748,28 @@ int check_lora_w(const woq_lora_w* w) {
 
 }  // namespace
 
+namespace woq {
+
+int lora_check(const woq_lora_w* w, const uint16_t* x, int64_t ldx, const int32_t* ids, int64_t b,
+               const uint16_t* base, int64_t ldbase, const uint16_t* y, int64_t ldy, const void* workspace,
+               int64_t workspace_bytes) {
+    const int rc = check_lora_w(w);
+    if (rc != WOQ_OK) return rc;
+    if (b < 0 || ldx < w->K || ldy < w->N || (base && ldbase < w->N)) return WOQ_EINVAL;
+    if (b == 0 || w->N == 0) return WOQ_OK;
+    if (!x || !ids || !y || !workspace || (w->count > 0 && (!w->A || !w->B || !w->scale))) return WOQ_EINVAL;
+    if (!aligned16(x) || (ldx & 7) || ((uintptr_t)ids & 3u) || ((uintptr_t)y & 1u) || ((uintptr_t)base & 1u) ||
+        !aligned16(workspace) || !aligned16(w->A) || !aligned16(w->B) || (w->lda & 7) ||
+        ((uintptr_t)w->scale & 3u) || ((uintptr_t)w->rank & 3u))
+        return WOQ_EALIGN;
+    if ((w->R & 7) || w->R > WOQ_LORA_MAX_R || w->N > (int64_t)INT32_MAX - 512 || w->K > (int64_t)INT32_MAX - 512 ||
+        b > WOQ_LORA_MAX_ROWS)
+        return WOQ_EUNSUPPORTED;
+    return workspace_bytes < woq_lora_workspace(w, b) ? WOQ_EINVAL : WOQ_OK;
+}
+
+}  // namespace woq
+
 extern "C" {
 
 int64_t woq_lora_workspace(const woq_lora_w* w, int64_t b) {
@@ -763,19 +785,8 @@ int64_t woq_lora_workspace(const woq_lora_w* w, int64_t b) {
 int woq_lora_add(const woq_lora_w* w, const uint16_t* x, int64_t ldx, const int32_t* ids, int64_t b,
                  const uint16_t* base, int64_t ldbase, uint16_t* y, int64_t ldy, void* workspace,
                  int64_t workspace_bytes, void* stream) {
-    const int rc = check_lora_w(w);
-    if (rc != WOQ_OK) return rc;
-    if (b < 0 || ldx < w->K || ldy < w->N || (base && ldbase < w->N)) return WOQ_EINVAL;
-    if (b == 0 || w->N == 0) return WOQ_OK;
-    if (!x || !ids || !y || !workspace || (w->count > 0 && (!w->A || !w->B || !w->scale))) return WOQ_EINVAL;
-    if (!woq::aligned16(x) || (ldx & 7) || ((uintptr_t)ids & 3u) || ((uintptr_t)y & 1u) || ((uintptr_t)base & 1u) ||
-        !woq::aligned16(workspace) || !woq::aligned16(w->A) || !woq::aligned16(w->B) || (w->lda & 7) ||
-        ((uintptr_t)w->scale & 3u) || ((uintptr_t)w->rank & 3u))
-        return WOQ_EALIGN;
-    if ((w->R & 7) || w->R > WOQ_LORA_MAX_R || w->N > (int64_t)INT32_MAX - 512 || w->K > (int64_t)INT32_MAX - 512 ||
-        b > WOQ_LORA_MAX_ROWS)
-        return WOQ_EUNSUPPORTED;
-    if (workspace_bytes < woq_lora_workspace(w, b)) return WOQ_EINVAL;
+    const int rc = woq::lora_check(w, x, ldx, ids, b, base, ldbase, y, ldy, workspace, workspace_bytes);
+    if (rc != WOQ_OK || b == 0 || w->N == 0) return rc;
     LoraArgs a;
     a.A = w->A;
     a.B = w->B;

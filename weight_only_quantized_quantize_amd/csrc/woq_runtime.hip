@@ -228,6 +228,46 @@ int woq_stack_run(woq_stack* st, const uint16_t* const* inputs, uint16_t* const*
     return run_pass(st, inputs, outputs, b, stream, nullptr);
 }
 
+int64_t woq_stack_lora_workspace(const woq_stack* st, const woq_lora_w* const* adapters, int64_t b) {
+    if (!st || !adapters || b < 1 || b > st->max_b) return WOQ_EINVAL;
+    int64_t most = 16;
+    for (size_t i = 0; i < st->steps.size(); ++i) {
+        if (!adapters[i]) continue;
+        const int64_t n = woq_lora_workspace(adapters[i], b);
+        if (n < 0) return n;
+        most = std::max(most, n);
+    }
+    return most;
+}
+
+int woq_stack_run_lora(woq_stack* st, const uint16_t* const* inputs, uint16_t* const* outputs, int64_t b,
+                       const woq_lora_w* const* adapters, const int32_t* ids, void* workspace,
+                       int64_t workspace_bytes, void* stream) {
+    if (!st || !inputs || !outputs || !adapters || b < 1 || b > st->max_b) return WOQ_EINVAL;
+    auto width_in = [](const woq_stack_step& s) { return s.fmt == WOQ_FMT_INT4O ? s.w4.geom.K : s.w8.K; };
+    auto width_out = [](const woq_stack_step& s) { return s.fmt == WOQ_FMT_INT4O ? s.w4.N : s.w8.N; };
+    for (size_t i = 0; i < st->steps.size(); ++i) {        // every pool before the first launch
+        const woq_stack_step& s = st->steps[i];
+        const woq_lora_w* w = adapters[i];
+        if (!w) continue;
+        const uint16_t *x = inputs[s.in_slot], *y = outputs[s.out_slot];
+        if (w->K != width_in(s) || w->N != width_out(s) || x == y) return WOQ_EINVAL;
+        const int rc = woq::lora_check(w, x, w->K, ids, b, y, w->N, y, w->N, workspace, workspace_bytes);
+        if (rc) return rc;
+    }
+    for (size_t i = 0; i < st->steps.size(); ++i) {
+        const woq_stack_step& s = st->steps[i];
+        const uint16_t* x = inputs[s.in_slot];
+        uint16_t* y = outputs[s.out_slot];
+        int rc = run_step(st, i, s, x, y, b, stream, nullptr);
+        if (rc == WOQ_OK && adapters[i])
+            rc = woq_lora_add(adapters[i], x, adapters[i]->K, ids, b, y, adapters[i]->N, y, adapters[i]->N, workspace,
+                              workspace_bytes, stream);
+        if (rc) return rc;
+    }
+    return WOQ_OK;
+}
+
 int woq_stack_time(woq_stack* st, const uint16_t* const* inputs, uint16_t* const* outputs, int64_t b, void* stream,
                    int32_t iters, float* step_ms, float* pass_ms) {
     if (!st || !inputs || !outputs || b < 1 || b > st->max_b || iters < 1 || !pass_ms ||

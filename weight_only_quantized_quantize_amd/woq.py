@@ -113,6 +113,9 @@ _SIGS = {
     "woq_lora_workspace": (c_int64, [POINTER(LoraW), c_int64]),
     "woq_stack_create": (c_int, [POINTER(StackStep), c_int32, c_int64, POINTER(c_void_p)]),
     "woq_stack_run": (c_int, [c_void_p, POINTER(c_void_p), POINTER(c_void_p), c_int64, c_void_p]),
+    "woq_stack_run_lora": (c_int, [c_void_p, POINTER(c_void_p), POINTER(c_void_p), c_int64, POINTER(c_void_p),
+                                   c_void_p, c_void_p, c_int64, c_void_p]),
+    "woq_stack_lora_workspace": (c_int64, [c_void_p, POINTER(c_void_p), c_int64]),
     "woq_stack_launches": (c_int, [c_void_p, c_int64, POINTER(c_int32)]),
     "woq_stack_time": (c_int, [c_void_p, POINTER(c_void_p), POINTER(c_void_p), c_int64, c_void_p, c_int32,
                                POINTER(c_float), POINTER(c_float)]),
@@ -492,9 +495,8 @@ def _rows(t, what: str, dtype, b: int, width: int):
     if rows < b or cols < width or (step != 1 and cols > 1):
         raise ValueError(f"{what}: needs {b} rows of {width} adjacent values, got {tuple(t.shape)} with strides "
                          f"{(ld, step)}")
-    if rows <= 1:
-        ld = max(ld, -(-cols // 16) * 16)     # of a single row the stride says nothing
-    return t.data_ptr(), ld
+    # of a single row the stride says nothing
+    return t.data_ptr(), ld if rows > 1 else max(ld, -(-cols // 16) * 16)
 
 
 def _vector(t, what: str, dtype, n: int):
@@ -713,6 +715,29 @@ class Stack:
     def run(self, b: int, stream=None):
         need_rows(b, *self._in, *self._out)
         _check(_lib().woq_stack_run(self.handle, self._pin, self._pout, b, _stream(stream)), "woq_stack_run")
+
+    def _pools(self, adapters):
+        if len(adapters) != self.n:
+            raise ValueError(f"{len(adapters)} pools for {self.n} steps")
+        return (c_void_p * max(1, self.n))(*[None if p is None else ctypes.addressof(p.desc) for p in adapters])
+
+    def lora_workspace(self, adapters, b: int) -> int:
+        """Bytes of the workspace of run_lora for batches of up to b rows."""
+        n = _lib().woq_stack_lora_workspace(self.handle, self._pools(adapters), b)
+        if n < 0:
+            _check(n, "woq_stack_lora_workspace")
+        return n
+
+    def run_lora(self, b: int, adapters, ids, workspace, stream=None):
+        """run with each row's own low-rank adapter ids[r] (int32 [b]) added
+        beside the steps: ``adapters`` holds a DeviceLora, or None, for every
+        step; workspace as lora_workspace says."""
+        need_rows(b, *self._in, *self._out)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace: must be contiguous")
+        _call("woq_stack_run_lora", stream, (*self._in, *self._out, ids, workspace), self.handle, self._pin, self._pout,
+              b, self._pools(adapters), _vector(ids, "ids", _torch.int32, b), workspace.data_ptr(),
+              workspace.numel() * workspace.element_size())
 
     def launches(self, b: int) -> int:
         n = c_int32()
