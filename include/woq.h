@@ -435,10 +435,11 @@ int woq_qgemm_int4o_splitk_noalloc(const woq_int4o_w* w, const uint16_t* xp, int
  * aligned, ldq a multiple of 16 and >= K; each row's codes are followed by
  * zeros up to a multiple of 16, so every row (the last too) must hold
  * round_up(K, 16) bytes.  sum_out may be res or x, and y may be x, with the
- * same leading dimension; other overlaps are not allowed.  K <= WOQ_NORM_MAX_K.
- * b = 0 is a no-op.
+ * same leading dimension; other overlaps are not allowed.  K <= WOQ_NORM_MAX_K,
+ * b <= WOQ_NORM_MAX_ROWS; b = 0 is a no-op.
  */
 #define WOQ_NORM_MAX_K 65536
+#define WOQ_NORM_MAX_ROWS 4000000
 int woq_add_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* res, int64_t ldres, const uint16_t* weight,
                     float offset, float eps, int64_t b, int64_t K, uint16_t* sum_out, int64_t ldsum, uint16_t* y,
                     int64_t ldy, int8_t* q, int64_t ldq, float* q_scale, void* stream);
@@ -452,8 +453,8 @@ int woq_add_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* res, int64_t
  * xq int8 [b, ldq], 16-byte aligned, ldq a multiple of 16 and >= K; every row
  * must hold round_up(K, 16) bytes (bytes past K are read but meet code 0);
  * codes of -128 are allowed.  xs fp32 [b]; y fp16 [b, ldy], ldy >= N, not
- * overlapping the inputs.  K <= WOQ_A8_MAX_K, so that no sum leaves int32.
- * b = 0 is a no-op.
+ * overlapping the inputs.  K <= WOQ_A8_MAX_K, so that no sum leaves int32;
+ * ceil(b / 256) * ceil(N / 256) below 2^22.  b = 0 is a no-op.
  */
 #define WOQ_A8_MAX_K 131072
 int woq_qgemm_int8_a8(const woq_int8_w* w, const int8_t* xq, int64_t ldq, const float* xs, int64_t b, uint16_t* y,
@@ -475,6 +476,7 @@ int woq_qgemm_int8_a8(const woq_int8_w* w, const int8_t* xq, int64_t ldq, const 
  */
 #define WOQ_LORA_MAX_R 256
 #define WOQ_LORA_MAX_ROWS 1000000
+#define WOQ_LORA_MAX_N (1 << 28)
 typedef struct {
     const uint16_t* A;
     const uint16_t* B;
@@ -498,8 +500,8 @@ typedef struct {
  * dimensions >= N; y may be base (same leading dimension).  workspace: at
  * least woq_lora_workspace(w, b) bytes of device memory, 16-byte aligned,
  * owned by the caller, its contents on return unspecified; calls that share
- * it must not overlap.  Deterministic.  b <= WOQ_LORA_MAX_ROWS; b = 0 is a
- * no-op.
+ * it must not overlap.  Deterministic for a given b.  N <= WOQ_LORA_MAX_N and
+ * b <= WOQ_LORA_MAX_ROWS; b = 0 is a no-op.
  * woq_lora_workspace returns a negative status for a bad descriptor or batch.
  */
 int woq_lora_add(const woq_lora_w* w, const uint16_t* x, int64_t ldx, const int32_t* ids, int64_t b,

@@ -641,6 +641,146 @@ def test_empty_calls_are_no_ops(gpu_lib):
     assert np.all(host(blk.y) == 5) and np.all(host(blk.n) == 5)
 
 
+@pytest.mark.parametrize("b", [3, 65, 300])
+def test_rows_past_the_batch_are_left_as_they_were(gpu_lib, b):
+    """Buffers of more rows than the call names: those behind stay untouched."""
+    blk = Block(b + 5, 200, 130, b)
+    for t in (blk.sum, blk.n, blk.y):
+        t.fill_(9)
+    blk.q.fill_(9)
+    blk.qs.fill_(9)
+    d = blk.d
+    woq.woq_add_rmsnorm(d["x"], d["w"], 1e-6, res=d["res"], sum_out=blk.sum, y=blk.n, q=blk.q, q_scale=blk.qs, b=b)
+    woq.woq_qgemm_int8_a8(blk.w8.desc, blk.q, blk.qs, blk.y, b=b)
+    woq.woq_lora_add(blk.pool.desc, blk.n, d["ids"], blk.y, blk.y, blk.ws, b=b)
+    for t in (blk.sum, blk.n, blk.y, blk.q):
+        assert np.all(host(t)[b:] == 9)
+    assert np.all(host(blk.qs)[b:] == 9)
+    few, blk.y = host(blk.y)[:b].copy(), full(b, 130, 0, "float16")
+    small = Block(b + 5, 200, 130, b)
+    small.run()
+    # (the adapters' partial sums may be cut differently for another b)
+    np.testing.assert_allclose(few.astype(np.float64), host(small.y)[:b].astype(np.float64), rtol=2 * H, atol=0.02)
+
+
+def test_two_streams_at_once(gpu_lib):
+    """Runs on two streams with buffers of their own, interleaved, give the bits of
+    runs one after the other."""
+    import torch
+    blocks = [Block(40, 1000, 500, 1), Block(40, 1000, 500, 2), Block(300, 640, 300, 3), Block(1, 2048, 700, 4)]
+    want = []
+    for blk in blocks:
+        blk.run()
+        want.append(host(blk.y).copy())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for _ in range(20):
+        for blk, s in zip(blocks, streams):
+            blk.run(stream=s)
+    torch.cuda.synchronize()
+    for blk, w in zip(blocks, want):
+        np.testing.assert_array_equal(host(blk.y).view(np.uint16), w.view(np.uint16))
+
+
+def far_rows(rows, width, ld, dtype):
+    import torch
+    t = torch.empty((rows - 1) * ld + width, dtype=getattr(torch, dtype), device="cuda")
+    return t.as_strided((rows, width), (ld, 1))
+
+
+def test_offsets_past_32_bits_activations(gpu_lib):
+    """Rows of activations, codes and outputs that lie more than 2^31 values apart."""
+    import torch
+    rows, K, N, ld = 5, 100, 70, 2 ** 29 + 64
+    x, res, w = norm_case(rows, K, 1)
+    big = {k: far_rows(rows, up(K, 8), ld, "float16") for k in ("x", "sum")}
+    big["x"][:, :K] = torch.from_numpy(x).cuda()
+    q, qs = far_rows(rows, up(K, 16), ld, "int8"), torch.empty(rows, device="cuda")
+    case("norm far rows")
+    woq.woq_add_rmsnorm(big["x"], dev(w), 1e-6, sum_out=big["sum"], q=q, q_scale=qs, K=K)
+    s_ref, v_ref = O.add_rmsnorm(x, None, w)
+    within(host(big["sum"].contiguous())[:, :K], s_ref, np.abs(s_ref) * (H + 2 * U) + SUB)
+    qh = host(q.contiguous())
+    within(qh[:, :K], v_ref / O.rows_scale(v_ref)[:, None], 0.5 + 127 * 2.0 ** -16)
+    case("product far rows")
+    rng = np.random.default_rng(2)
+    codes, scales, w8 = a8_weight(N, K, rng)
+    y = far_rows(rows, N, ld, "float16")
+    woq.woq_qgemm_int8_a8(w8.desc, q, qs, y)
+    ref = O.linear_int8_a8(codes, [N], scales, qh[:, :K], host(qs))
+    within(host(y.contiguous()), ref, np.abs(ref) * (H + 4 * U) + SUB)
+    for b in (rows, 300):                        # both forms of the adapters' kernels
+        case("adapters far rows", b)
+        A, B, s, ends = lora_pool(2, N, K, 16, 1, rng)
+        pool = woq.DeviceLora(dev(A), dev(B), dev(s), K=K)
+        step = ld if b == rows else 2 ** 23 + 8  # the last row past 2^31 either way
+        xs, ys = far_rows(b, up(K, 8), step, "float16"), far_rows(b, N, step, "float16")
+        xv = rng.standard_normal((b, K)).astype(np.float16)
+        xs[:, :K] = torch.from_numpy(xv).cuda()
+        ys.fill_(0.5)
+        ids = rng.integers(-1, 2, b).astype(np.int32)
+        ws = torch.empty(woq.woq_lora_workspace(pool.desc, b), dtype=torch.uint8, device="cuda")
+        woq.woq_lora_add(pool.desc, xs, dev(ids), ys, ys, ws)
+        ref, spread = O.lora_add(np.full((b, N), 0.5), xv, ids, A, B, s, ends)
+        within(host(ys.contiguous()), ref, np.abs(ref) * (H + 2 * U) + SUB + spread * ((K / 16 + 48) * U + 2.0 ** -20))
+        del xs, ys
+
+
+def test_offsets_past_32_bits_weights(gpu_lib):
+    """Weights and pools of more than 2^31 bytes or values: their last rows."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(3)
+    N, K = 17000, woq.A8_MAX_K
+    case("product large weight")
+    codes = torch.randint(1, 256, (N, K), generator=g, device="cuda", dtype=torch.uint8)
+    w = woq.Int8W()
+    w.codes, w.N, w.K, w.nseg = codes.data_ptr(), N, K, 1
+    w.seg_end[0], w.seg_scale[0] = N, 2.0 ** -12
+    for b in (2, 70):
+        q = torch.randint(-127, 128, (b, K), generator=g, device="cuda", dtype=torch.int8)
+        qs, y = torch.full((b,), 2.0 ** -6, device="cuda"), full(b, N, 0, "float16")
+        woq.woq_qgemm_int8_a8(w, q, qs, y)
+        at = torch.cat([torch.arange(20), torch.arange(N - 200, N)]).cuda()
+        ref = ((q.double() @ (codes[at].double() - 128).t().contiguous()) * 2.0 ** -18).cpu().numpy()
+        within(host(y[:, at]), ref, np.abs(ref) * (H + 4 * U) + SUB)
+    del codes, q
+    torch.cuda.empty_cache()
+    count, N, K, R = 9, 2 ** 20 + 3, 64, 256
+    case("adapters large pool")
+    A = torch.randn(count, R, K, generator=g, device="cuda").half() * 0.125
+    B = torch.zeros(count, N, R, dtype=torch.float16, device="cuda")
+    at = torch.cat([torch.arange(40), torch.arange(N - 300, N)]).cuda()
+    part = torch.randn(len(at), R, generator=g, device="cuda").half() * 0.25
+    B[count - 1, at] = part
+    s = torch.ones(count, device="cuda")
+    pool = woq.DeviceLora(A, B, s)
+    for b in (2, 257):
+        x = torch.randn(b, K, generator=g, device="cuda").half()
+        ids = torch.full((b,), count - 1, dtype=torch.int32, device="cuda")
+        y = torch.empty(b, N, dtype=torch.float16, device="cuda")
+        ws = torch.empty(woq.woq_lora_workspace(pool.desc, b), dtype=torch.uint8, device="cuda")
+        woq.woq_lora_add(pool.desc, x, ids, None, y, ws)
+        xd, Ad, Bd = x.double().cpu().numpy(), A[-1].double().cpu().numpy(), part.double().cpu().numpy()
+        ref, spread = xd @ Ad.T @ Bd.T, np.abs(xd) @ np.abs(Ad).T @ np.abs(Bd).T
+        within(host(y[:, at]), ref, np.abs(ref) * (H + 2 * U) + SUB + spread * ((K / 16 + R + 32) * U + 2.0 ** -20))
+        assert not y[:, 1000:N - 1000].any()
+    case("adapters rows of A far apart")
+    count, R, K, lda = 3, 16, 40, 2 ** 26
+    A = torch.zeros(count, R, lda, dtype=torch.float16, device="cuda")
+    A[:, :, :K] = torch.randn(count, R, K, generator=g, device="cuda").half()
+    B = torch.randn(count, 50, R, generator=g, device="cuda").half()
+    pool = woq.DeviceLora(A, B, torch.ones(count, device="cuda"), K=K)
+    for b in (3, 260):
+        x = torch.randn(b, K, generator=g, device="cuda").half()
+        ids = (torch.arange(b, device="cuda") % count).int()
+        y = torch.empty(b, 50, dtype=torch.float16, device="cuda")
+        ws = torch.empty(woq.woq_lora_workspace(pool.desc, b), dtype=torch.uint8, device="cuda")
+        woq.woq_lora_add(pool.desc, x, ids, None, y, ws)
+        ref, spread = O.lora_add(np.zeros((b, 50)), x.cpu().numpy(), host(ids), A[:, :, :K].cpu().numpy(), B.cpu().numpy(),
+                                 np.ones(count), [50])
+        within(host(y), ref, np.abs(ref) * (H + 2 * U) + SUB + spread * ((K / 16 + 48) * U + 2.0 ** -20))
+
+
 def test_binding_checks_buffers_before_a_launch(gpu_lib):
     import torch
     blk = Block(4, 64, 48, 3)

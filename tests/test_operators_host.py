@@ -88,7 +88,8 @@ def norm_args(**kw):
     (dict(ldsum=68), woq.WOQ_EALIGN), (dict(y=P + 2), woq.WOQ_EALIGN), (dict(ldy=68), woq.WOQ_EALIGN),
     (dict(q=P + 8), woq.WOQ_EALIGN), (dict(ldq=72), woq.WOQ_EALIGN), (dict(q_scale=P + 2), woq.WOQ_EALIGN),
     (dict(K=65537, ldx=65544, ldres=65544, ldsum=65544, ldy=65544, ldq=65552), woq.WOQ_EUNSUPPORTED),
-    (dict(b=1 << 31), woq.WOQ_EUNSUPPORTED), (dict(b=0), woq.WOQ_OK), (dict(b=0, x=None), woq.WOQ_OK),
+    (dict(b=1 << 31), woq.WOQ_EUNSUPPORTED), (dict(b=4000001), woq.WOQ_EUNSUPPORTED),
+    (dict(b=0), woq.WOQ_OK), (dict(b=0, x=None), woq.WOQ_OK),
 ])
 def test_norm_refusals(change, status):
     assert call("woq_add_rmsnorm", *norm_args(**change)) == status
@@ -112,6 +113,7 @@ def weight8(N=40, K=100, ends=None, codes=P):
     (dict(xq=P + 8), woq.WOQ_EALIGN), (dict(ldq=120), woq.WOQ_EALIGN), (dict(xs=P + 2), woq.WOQ_EALIGN),
     (dict(y=P + 1), woq.WOQ_EALIGN), (dict(w=weight8(K=131073), ldq=131088), woq.WOQ_EUNSUPPORTED),
     (dict(w=weight8(N=1 << 31), ldy=1 << 31), woq.WOQ_EUNSUPPORTED), (dict(b=1 << 31), woq.WOQ_EUNSUPPORTED),
+    (dict(w=weight8(N=1 << 22), ldy=1 << 22, b=1 << 18), woq.WOQ_EUNSUPPORTED),
     (dict(b=0, xq=None), woq.WOQ_OK), (dict(w=weight8(N=0, codes=None)), woq.WOQ_OK),
 ])
 def test_product_refusals(change, status):
@@ -149,7 +151,9 @@ def pool(N=40, K=100, lda=104, R=16, count=3, ends=None, **ptrs):
     (dict(ids=P + 2), woq.WOQ_EALIGN), (dict(y=P + 1), woq.WOQ_EALIGN), (dict(base=P + 1), woq.WOQ_EALIGN),
     (dict(ws=P + 8), woq.WOQ_EALIGN), (dict(w=pool(R=12)), woq.WOQ_EUNSUPPORTED),
     (dict(w=pool(R=264)), woq.WOQ_EUNSUPPORTED), (dict(w=pool(N=1 << 31), ldy=1 << 31, ldbase=1 << 31), woq.WOQ_EUNSUPPORTED),
-    (dict(b=1 << 31), woq.WOQ_EUNSUPPORTED), (dict(b=0, x=None), woq.WOQ_OK), (dict(w=pool(N=0, A=None)), woq.WOQ_OK),
+    (dict(w=pool(N=(1 << 28) + 1), ldy=1 << 29, ldbase=1 << 29), woq.WOQ_EUNSUPPORTED),
+    (dict(b=1 << 31), woq.WOQ_EUNSUPPORTED), (dict(b=1000001), woq.WOQ_EUNSUPPORTED),
+    (dict(b=0, x=None), woq.WOQ_OK), (dict(w=pool(N=0, A=None)), woq.WOQ_OK),
 ])
 def test_adapter_refusals(change, status):
     a = dict(w=pool(), x=P, ldx=104, ids=P, b=3, base=P, ldbase=40, y=P, ldy=40, ws=P, ws_bytes=1 << 40, stream=None)
@@ -192,3 +196,10 @@ def test_binding_refuses_what_the_library_cannot_see():
         woq.DeviceLora(A, B, s, segments=[10, 40], K=65)
     with pytest.raises(ValueError):                       # well formed, but not on the GPU
         woq.DeviceLora(A, B, s, segments=[10, 40])
+
+
+def test_stack_with_adapters_refusals():
+    one = (ctypes.c_void_p * 1)(P)
+    for args in ((None, one, one, 1, one, P, P, 1 << 20, None),):
+        assert call("woq_stack_run_lora", *args) == woq.WOQ_EINVAL
+    assert call("woq_stack_lora_workspace", None, one, 1) == woq.WOQ_EINVAL

@@ -309,8 +309,8 @@ extern "C" int woq_qgemm_int8_a8(const woq_int8_w* w, const int8_t* xq, int64_t 
     if (!woq::aligned16(w->codes) || !woq::aligned16(xq) || (ldq & 15) || ((uintptr_t)xs & 3u) || ((uintptr_t)y & 1u))
         return WOQ_EALIGN;
     if (w->K > WOQ_A8_MAX_K || w->N > (int64_t)INT32_MAX - 512 || b > (int64_t)INT32_MAX - 512 ||
-        woq::ceil_div(b, 256) * woq::ceil_div(w->N, 256) > INT32_MAX)
-        return WOQ_EUNSUPPORTED;
+        woq::ceil_div(b, 256) * woq::ceil_div(w->N, 256) > (int64_t)UINT32_MAX / 1024)
+        return WOQ_EUNSUPPORTED;     // a launch has fewer than 2^32 threads
     A8Args a;
     a.codes = static_cast<const uint8_t*>(w->codes);
     a.q = xq;

@@ -762,7 +762,7 @@ int lora_check(const woq_lora_w* w, const uint16_t* x, int64_t ldx, const int32_
         !aligned16(workspace) || !aligned16(w->A) || !aligned16(w->B) || (w->lda & 7) ||
         ((uintptr_t)w->scale & 3u) || ((uintptr_t)w->rank & 3u))
         return WOQ_EALIGN;
-    if ((w->R & 7) || w->R > WOQ_LORA_MAX_R || w->N > (int64_t)INT32_MAX - 512 || w->K > (int64_t)INT32_MAX - 512 ||
+    if ((w->R & 7) || w->R > WOQ_LORA_MAX_R || w->N > WOQ_LORA_MAX_N || w->K > (int64_t)INT32_MAX - 512 ||
         b > WOQ_LORA_MAX_ROWS)
         return WOQ_EUNSUPPORTED;
     return workspace_bytes < woq_lora_workspace(w, b) ? WOQ_EINVAL : WOQ_OK;

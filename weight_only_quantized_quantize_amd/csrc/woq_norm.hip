@@ -207,7 +207,7 @@ extern "C" int woq_add_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* r
         (sum_out && !half_rows_ok(sum_out, ldsum)) || (y && !half_rows_ok(y, ldy)) ||
         (q && (!woq::aligned16(q) || (ldq & 15) || ((uintptr_t)q_scale & 3u))))
         return WOQ_EALIGN;
-    if (K > WOQ_NORM_MAX_K || b > INT32_MAX) return WOQ_EUNSUPPORTED;
+    if (K > WOQ_NORM_MAX_K || b > WOQ_NORM_MAX_ROWS) return WOQ_EUNSUPPORTED;
     NormArgs a;
     a.x = x;
     a.res = res;
