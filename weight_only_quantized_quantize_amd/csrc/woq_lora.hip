@@ -363,9 +363,12 @@ __device__ __forceinline__ int tile_segment(const LoraArgs& a, int width, int& n
 // The outer products of a decode batch: 16 rows x 64 outputs of one segment per
 // workgroup of four waves, one output tile a wave.  Each adapter of the 16 rows
 // gives a tile of results, of which its rows keep theirs.  A step is 16 ranks of
-// one adapter; the operands of the next U steps are always on their way.
+// one adapter; the operands of the next 2 U steps are always on their way.
+// ONE: no adapter has more ranks than a step (R <= 16); then all rows' steps are
+// independent and run four at a time without a branch between them.
+template <bool ONE>
 __global__ __launch_bounds__(256, 4) void lora_up_rows_kernel(LoraArgs a) {
-    constexpr int TM = 16, U = 16;
+    constexpr int TM = 16, U = 8;
     using C = Cols<1>;
     extern __shared__ __align__(16) uint32_t hp[];     // [TM][Rp + 4]: hi | lo << 16
     __shared__ int sexp[TM];
@@ -411,19 +414,38 @@ __global__ __launch_bounds__(256, 4) void lora_up_rows_kernel(LoraArgs a) {
         most = max(most, rank_of(a, id));
     }
     const int groups = (most + 15) >> 4, steps = left > 0 ? count * groups : 0;
-    const int lane_b = C::row(m, 0) * a.R + 8 * (c & 1);
+    // B in the order it lies in memory: one load has the 32 pieces of 16 bytes of
+    // one step in the lower lanes and those of the next in the upper ones
+    const int brow = min((lane & 31) >> 1, left - 1);
+    const uint16_t* bp = a.B + ((int64_t)nw + brow) * a.R + 8 * (lane & 1);
     int lk = 0, lt = 0;                                // the next step to load
     auto load_b = [&](uint4& to) {
-        const int id = __builtin_amdgcn_readlane(list, lk), rank = rank_of(a, id);
-        const uint16_t* p = a.B + ((int64_t)id * a.N + nw) * a.R + 16 * lt;
-        if (left >= 16 && rank >= 16 * (lt + 1)) to = load16(p + lane_b);
-        else to = load8_until(p + (int64_t)(min(C::row(m, 0), left - 1)) * a.R, 8 * (c & 1), rank - 16 * lt);
-        if (++lt == groups) lt = 0, ++lk;
+        int id[2], tt[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            id[e] = __builtin_amdgcn_readlane(list, lk);
+            tt[e] = lt;
+            if (++lt == groups) lt = 0, ++lk;
+            lk = min(lk, count - 1);                   // past the end the last adapter again
+        }
+        const bool up = lane >= 32;
+        const int left_k = (up ? rank_of(a, id[1]) - 16 * tt[1] : rank_of(a, id[0]) - 16 * tt[0]) - 8 * (lane & 1);
+        const int64_t at = (int64_t)(up ? id[1] : id[0]) * a.N * a.R + 16 * (up ? tt[1] : tt[0]);
+        to = make_uint4(0, 0, 0, 0);
+        if (left_k > 0) to = load16(bp + at);
+        if (left_k < 8) {                              // ranks that the adapter has not
+            uint32_t w[4] = {to.x, to.y, to.z, to.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] &= (left_k > 2 * e ? 0xFFFFu : 0u) | (left_k > 2 * e + 1 ? 0xFFFF0000u : 0u);
+            to = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     };
     uint4 bv[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (u < steps) load_b(bv[u]);
+    for (int u = 0; u < U; ++u) {
+        bv[u] = make_uint4(0, 0, 0, 0);
+        if (2 * u < steps) load_b(bv[u]);
+    }
     const int mine = __shfl(win.ids[0], m);
     const float scale = mine >= 0 ? *gptr(a.scale + mine) : 0.f;
 
@@ -454,16 +476,43 @@ __global__ __launch_bounds__(256, 4) void lora_up_rows_kernel(LoraArgs a) {
     f4 acc = {0.f, 0.f, 0.f, 0.f}, d[1] = {acc};
     int k = 0, t = 0;
     const uint32_t sel = c < 2 ? HI : LO;
-    for (int s = 0; s < steps; s += U) {
+    // the operand of lane (m, c) in a step: row m, piece c & 1
+    auto operand = [&](uint4 pair, int e) {
+        const int from = 32 * e + 2 * m + (c & 1);
+        return as_h8(make_uint4(__shfl((int)pair.x, from), __shfl((int)pair.y, from), __shfl((int)pair.z, from),
+                                __shfl((int)pair.w, from)));
+    };
+    auto halves = [&](int t) {
+        const uint32_t* hw = hp + m * ldh + 16 * t + 8 * (c & 1);
+        const u32x4 p0 = *(const u32x4*)hw, p1 = *(const u32x4*)(hw + 4);
+        return as_h8(make_uint4(__builtin_amdgcn_perm(p0[1], p0[0], sel), __builtin_amdgcn_perm(p0[3], p0[2], sel),
+                                __builtin_amdgcn_perm(p1[1], p1[0], sel), __builtin_amdgcn_perm(p1[3], p1[2], sel)));
+    };
+    if constexpr (ONE) {
+        const h8 hv = halves(0);
+#pragma unroll
+        for (int u = 0; u < U; u += 2) {
+            if (2 * u >= steps) continue;
+            // (steps past the last adapter: no row takes their results)
+            f4 r4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                r4[e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(bv[u + e / 2], e & 1), hv, f4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (2 * u + e < steps && mine == __builtin_amdgcn_readlane(list, 2 * u + e)) d[0] = r4[e];
+        }
+    }
+    for (int s = 0; !ONE && s < steps; s += 2 * U) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (s + u < steps) {
-                const uint32_t* hw = hp + m * ldh + 16 * t + 8 * (c & 1);
-                const u32x4 p0 = *(const u32x4*)hw, p1 = *(const u32x4*)(hw + 4);
-                const h8 hv = as_h8(make_uint4(__builtin_amdgcn_perm(p0[1], p0[0], sel), __builtin_amdgcn_perm(p0[3], p0[2], sel),
-                                               __builtin_amdgcn_perm(p1[1], p1[0], sel), __builtin_amdgcn_perm(p1[3], p1[2], sel)));
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_h8(bv[u]), hv, acc, 0, 0, 0);
-                if (s + u + U < steps) load_b(bv[u]);
+            if (s + 2 * u >= steps) continue;
+            const uint4 pair = bv[u];
+            if (s + 2 * u + 2 * U < steps) load_b(bv[u]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (s + 2 * u + e >= steps) continue;
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(pair, e), halves(t), acc, 0, 0, 0);
                 if (++t == groups) {
                     if (mine == __builtin_amdgcn_readlane(list, k)) d[0] = acc;
                     acc = f4{0.f, 0.f, 0.f, 0.f};
@@ -696,7 +745,12 @@ int rank_tiles(int64_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }
 
 // K ranges that leave every wave of a few rows' workgroups one round of loads,
 // four pieces of 64 channels.
-int k_ranges(int K) { return (int)std::min<int64_t>(woq::ceil_div(K, 4 * 4 * 64), LEADER_SPLITS); }
+// More where that would be over three workgroups to a compute unit, which is
+// what its registers hold (64 rows of 8192, three segments, an adapter each: 12.3 -> 11.5 us).
+int k_ranges(const LoraArgs& a) {
+    const int64_t units = (int64_t)a.b * a.nseg * a.groups, room = std::max<int64_t>(1, 3 * woq::compute_units() / units);
+    return (int)std::min<int64_t>(std::min<int64_t>(woq::ceil_div(a.K, 4 * 4 * 64), LEADER_SPLITS), room);
+}
 
 hipError_t launch(const void* kernel, dim3 grid, int threads, size_t lds, hipStream_t s, LoraArgs a) {
     void* argv[] = {&a};
@@ -712,13 +766,14 @@ unsigned count_tiles(LoraArgs& a, int width) {
 }
 
 hipError_t launch_few(LoraArgs a, hipStream_t s) {
-    a.splits = k_ranges(a.K);
     a.groups = (int)woq::ceil_div(a.R, 16);
+    a.splits = k_ranges(a);
     hipError_t e = launch(reinterpret_cast<const void*>(&lora_down_kernel<4, 1, 4, true>),
                           dim3((unsigned)a.b, (unsigned)(a.nseg * a.groups), (unsigned)a.splits), 256, 0, s, a);
     if (e != hipSuccess) return e;
     const unsigned tiles = count_tiles(a, 64);
-    return launch(reinterpret_cast<const void*>(&lora_up_rows_kernel), dim3(tiles, (unsigned)woq::ceil_div(a.b, 16)), 256,
+    return launch(a.R <= 16 ? reinterpret_cast<const void*>(&lora_up_rows_kernel<true>)
+                            : reinterpret_cast<const void*>(&lora_up_rows_kernel<false>), dim3(tiles, (unsigned)woq::ceil_div(a.b, 16)), 256,
                   (size_t)16 * (woq::round_up(a.R, 16) + 4) * 4, s, a);
 }
 
