@@ -93,10 +93,12 @@ struct Window {
 
 // The inner products of RT rank tiles of 16 in one segment (blockIdx.y).  The
 // W waves split the K range and add their sums in LDS in a fixed order.
-//   LEADER (few rows): one workgroup per row (blockIdx.x) and K range
-//     (blockIdx.z); it works if its row is the first of its adapter, for all
-//     rows of that adapter, so distinct adapters run side by side and a shared
-//     one is read once.  The ranges' sums go to the workspace as they are.
+//   LEADER (few rows): one workgroup per row and K range (blockIdx.z); it works
+//     if its row is the 1st, 17th, 33rd .. of its adapter, for it and the next 15,
+//     so distinct adapters, and the parts of one that many rows share, run side by
+//     side.  The ranges' sums go to the workspace as they are.  Rows turn with the
+//     other indexes: of requests of 16 rows each, the first rows would all fall to one
+//     XCD (256 rows of 10696, rank 56, 16 adapters: 115 us instead of 34).
 //   otherwise: one workgroup per window of 32 rows; the workgroups of a window
 //     (blockIdx.z) take its adapters in turn (a packed prompt has one or two in a
 //     window).  h is written scaled and split, ready to be multiplied.
@@ -131,11 +133,11 @@ __global__ __launch_bounds__(64 * W) void lora_down_kernel(LoraArgs a) {
 
     u64 left = LEADER ? 1ull : __ballot(win.ids[0] >= 0);
     for (int turn = 0; left; ++turn) {
-        int id;
+        int id, start = 0;                             // the first of the adapter's rows to take
         u64 of[NW];
         if constexpr (LEADER) {
             left = 0;
-            const int r = blockIdx.x;
+            const int r = (blockIdx.x + blockIdx.y + gridDim.y * blockIdx.z) % (unsigned)a.b;
             id = -1;
 #pragma unroll
             for (int w = 0; w < NW; ++w)
@@ -144,9 +146,9 @@ __global__ __launch_bounds__(64 * W) void lora_down_kernel(LoraArgs a) {
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
                 of[w] = __ballot(win.ids[w] == id);
-                const u64 earlier = r >> 6 > w ? ~0ull : r >> 6 == w ? (1ull << (r & 63)) - 1 : 0;
-                if (of[w] & earlier) return;          // not the first of its adapter
+                start += __popcll(of[w] & (r >> 6 > w ? ~0ull : r >> 6 == w ? (1ull << (r & 63)) - 1 : 0));
             }
+            if (start & 15) return;
         } else {
             id = __builtin_amdgcn_readlane(win.ids[0], __ffsll(left) - 1);
             of[0] = __ballot(win.ids[0] == id);
@@ -167,7 +169,7 @@ __global__ __launch_bounds__(64 * W) void lora_down_kernel(LoraArgs a) {
 #pragma unroll
         for (int i = 0; i < AP; ++i)
             ap[i] = a.A + (((int64_t)id * a.nseg + seg) * a.R + min(j0 + 8 * i + pr, a.R - 1)) * a.lda + 8 * pc;
-        for (int c0 = 0; c0 < total; c0 += 16 * CT) {
+        for (int c0 = start; c0 < total; c0 += LEADER ? WIN : 16 * CT) {
             // columns past the list repeat its first row, or hold anything; their
             // results are dropped
             const bool two = CT == 2 && total - c0 > 16;
@@ -748,7 +750,7 @@ int rank_tiles(int64_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }
 // More where that would be over three workgroups to a compute unit, which is
 // what its registers hold (64 rows of 8192, three segments, an adapter each: 12.3 -> 11.5 us).
 int k_ranges(const LoraArgs& a) {
-    const int64_t units = (int64_t)a.b * a.nseg * a.groups, room = std::max<int64_t>(1, 3 * woq::compute_units() / units);
+    const int64_t units = (int64_t)std::min(a.b, a.count + a.b / 16 + 1) * a.nseg * a.groups, room = std::max<int64_t>(1, 3 * woq::compute_units() / units);
     return (int)std::min<int64_t>(std::min<int64_t>(woq::ceil_div(a.K, 4 * 4 * 64), LEADER_SPLITS), room);
 }
 
@@ -779,11 +781,12 @@ hipError_t launch_few(LoraArgs a, hipStream_t s) {
 
 template <int RT, int D>
 hipError_t launch_many(LoraArgs a, hipStream_t s) {
-    constexpr int SLOTS = 2;
     a.groups = (int)woq::ceil_div(a.R, 16 * RT);
     a.exps = reinterpret_cast<int32_t*>(a.h) + (int64_t)a.b * a.nseg * a.groups * 16 * RT;
+    // workgroups of a window, which take its adapters in turn; most find none left
+    const int slots = std::max(1, std::min(8, a.count));
     hipError_t e = launch(reinterpret_cast<const void*>(&lora_down_kernel<8, RT, D, false>),
-                          dim3((unsigned)woq::ceil_div(a.b, 32), (unsigned)(a.nseg * a.groups), SLOTS), 512, 0, s, a);
+                          dim3((unsigned)woq::ceil_div(a.b, 32), (unsigned)(a.nseg * a.groups), (unsigned)slots), 512, 0, s, a);
     if (e != hipSuccess) return e;
     // tiles a workgroup goes through: more where there is work enough for the device
     const int64_t rows = woq::ceil_div(a.b, 64);
