@@ -353,6 +353,71 @@ def test_adapters_packed_prompts(gpu_lib, lens):
         check_lora(b, N, K, R, S, count, ids, b)
 
 
+@pytest.mark.parametrize("b,N,K,R,S,count", [
+    (257, 40, 72, 8, 1, 17), (683, 130, 200, 16, 1, 7), (1021, 70, 96, 64, 2, 5), (1025, 66, 40, 24, 3, 1500), (4097, 24, 32, 16, 1, 2),
+    (4500, 16, 24, 72, 1, 3), (9000, 8, 16, 8, 1, 2500), (120, 20011, 64, 16, 2, 4), (256, 8210, 48, 40, 1, 30), (200, 20000, 32, 8, 1, 26)])
+def test_adapters_mixed_large_batches(gpu_lib, b, N, K, R, S, count):
+    """Rows of one adapter anywhere in the batch, more adapters than the order
+    has bins, rows without one among them, all of one adapter, none of any."""
+    case("adapters mixed", b, N, K, R, S, count)
+    rng = np.random.default_rng(b + N)
+    check_lora(b, N, K, R, S, count, rng.integers(-1, count + 1, b), 1, pad=1, odd=3)
+    check_lora(b, N, K, R, S, count, np.arange(b) % count, 2, rank=rng.integers(-1, R + 2, count), junk=True, place=True)
+    check_lora(b, N, K, R, S, count, np.full(b, count - 1), 3)
+    check_lora(b, N, K, R, S, count, np.full(b, -7), 4)
+    if count > 1024:
+        check_lora(b, N, K, R, S, count, (np.arange(b) % 2) * 1024 + 3, 5)
+
+
+@pytest.mark.parametrize("b,N,R,count", [(30, 50, 16, 5), (150, 16000, 16, 8), (700, 75, 16, 9), (5000, 20, 72, 6)])
+def test_adapters_bits_do_not_depend_on_the_order_of_rows(gpu_lib, b, N, R, count):
+    """The rows shuffled, and again with those of one adapter side by side: the same bits."""
+    import torch
+    case("adapters shuffled", b, N, R, count)
+    rng = np.random.default_rng(b)
+    A, B, s, ends = lora_pool(count, N, 136, R, 1, rng)
+    pool = woq.DeviceLora(dev(A), dev(B), dev(s))
+    x, base = rng.standard_normal((b, 136)).astype(np.float16), rng.standard_normal((b, N)).astype(np.float16)
+    ids = rng.integers(-1, count, b).astype(np.int32)
+    ws = torch.empty(woq.woq_lora_workspace(pool.desc, b), dtype=torch.uint8, device="cuda")
+
+    def run(at):
+        y = full(b, N, 7, "float16")
+        woq.woq_lora_add(pool.desc, dev(x[at]), dev(ids[at]), dev(base[at]), y, ws)
+        out = np.empty((b, N), np.float16)
+        out[at] = host(y)
+        return out.view(np.uint16)
+
+    first = run(np.arange(b))
+    for at in (np.arange(b), rng.permutation(b), np.argsort(ids, kind="stable")):
+        np.testing.assert_array_equal(run(at), first)
+
+
+def test_adapters_of_a_mixed_batch_captured_and_replayed(gpu_lib):
+    """Replays with other rows and ids than the captured ones, eager calls in between."""
+    import torch
+    case("adapters mixed, captured")
+    rng = np.random.default_rng(12)
+    b, N, K, R, count = 1100, 90, 136, 32, 6
+    A, B, s, ends = lora_pool(count, N, K, R, 1, rng)
+    pool = woq.DeviceLora(dev(A), dev(B), dev(s))
+    inputs = [(dev(rng.standard_normal((b, K)).astype(np.float16)), dev(rng.integers(-1, count, b).astype(np.int32))) for _ in range(3)]
+    x, ids, y = inputs[0][0].clone(), inputs[0][1].clone(), full(b, N, 7, "float16")
+    ws, other = (torch.empty(woq.woq_lora_workspace(pool.desc, b), dtype=torch.uint8, device="cuda") for _ in range(2))
+    woq.woq_lora_add(pool.desc, x, ids, None, y, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        woq.woq_lora_add(pool.desc, x, ids, None, y, ws)
+    for i in (0, 1, 2, 1):
+        x.copy_(inputs[i][0])
+        ids.copy_(inputs[i][1])
+        graph.replay()
+        eager = full(b, N, 7, "float16")
+        woq.woq_lora_add(pool.desc, *inputs[i], None, eager, other)
+        np.testing.assert_array_equal(host(y).view(np.uint16), host(eager).view(np.uint16))
+
+
 @pytest.mark.parametrize("b", [1, 20, 100, 300])
 def test_adapters_of_different_ranks(gpu_lib, b):
     """Entries past an adapter's rank and past K are NaN and stay out of it."""

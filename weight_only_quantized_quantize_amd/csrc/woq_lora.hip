@@ -16,7 +16,12 @@
 // A decode batch is bound by the bytes of the adapters that its rows name, or,
 // at a few rows, by two launches of a few memory round trips each: the kernels
 // keep every load of a round in flight together and have no barrier before the
-// sums meet.  A prompt is bound by the base and the output.
+// sums meet.  One row beside 8192 x 8192, rank 16: 4.2 + 4.5 us; 64 rows beside
+// 10240 x 8192 in three segments, an adapter of rank 16 each: 10-13 + 9.6 us,
+// 75 MB at 3.7 TB/s.  (Both products in one launch, each workgroup computing h
+// for its 1024 outputs: 11.2 and 36 us.)  A prompt is bound by the base and the
+// output: 3001 rows beside 28672 x 3584 in two segments, rank 64: 20 + 92 us,
+// 402 MB at 3.6 TB/s.
 #include <hip/hip_runtime.h>
 
 #include "woq_gemv.h"
@@ -39,6 +44,7 @@ struct LoraArgs {
     uint16_t* y;
     float* h;                 // few rows: sums [splits][b][nseg R]; else halves [b][nseg][groups][hi, lo][16 RT]
     int32_t* exps;            // else: the halves' exponents [b][nseg][groups]
+    int32_t* order;           // else: the rows, those of one adapter side by side; null: as they are
     int64_t ldx, ldbase, ldy, lda;
     int b, N, K, R, count, nseg, splits, groups, per;
     int vec;                  // rows of base and y may be read and written in 16-byte pieces
@@ -77,35 +83,108 @@ __device__ __forceinline__ uint32_t split_halves(float v, int ex) {
 // v_perm selectors: the hi, or the lo, halves of two such words
 constexpr uint32_t HI = 0x05040100u, LO = 0x07060302u;
 
-// The adapters of a window of up to 64 NW rows, found by each wave for itself:
-// a lane holds the ids of rows lane, 64 + lane, ...
-template <int NW>
+// The adapters of a window of up to 64 NW positions, found by each wave for itself:
+// a lane holds the ids of positions lane, 64 + lane, ...
+// ORDER: positions in the order of the rows, if there is one; else rows.
+template <int NW, bool ORDER>
 struct Window {
-    int ids[NW];
+    int row[NW], ids[NW];
     __device__ __forceinline__ void read(const LoraArgs& a, int first, int rows, int lane) {
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            ids[w] = 64 * w + lane < rows ? *gptr(a.ids + first + 64 * w + lane) : -1;
+            row[w] = min(first + 64 * w + lane, a.b - 1);
+            if (ORDER && a.order) row[w] = *gptr(a.order + row[w]);
+            ids[w] = 64 * w + lane < rows ? *gptr(a.ids + row[w]) : -1;
             if ((unsigned)ids[w] >= (unsigned)a.count) ids[w] = -1;
         }
     }
 };
 
+// The order in which a prompt's or a large batch's rows are taken: those of one adapter
+// side by side (of adapters that are equal modulo 1024: only speed depends on
+// it), those without one last.  One workgroup counts and places them; the rows
+// of one adapter come in any order, which no result depends on.
+constexpr int BINS = 1024;
+__global__ __launch_bounds__(BINS) void lora_order_kernel(LoraArgs a) {
+    __shared__ int next[BINS + 1], sums[BINS / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    next[tid] = 0;
+    if (tid == 0) next[BINS] = 0;
+    __syncthreads();
+    // four turns of rows at a time, which for most batches is all of them
+    constexpr int TURNS = 4;
+    int bin[TURNS];
+    auto read = [&](int first) {
+#pragma unroll
+        for (int t = 0; t < TURNS; ++t) bin[t] = *gptr(a.ids + min(first + t * BINS + tid, a.b - 1));
+#pragma unroll
+        for (int t = 0; t < TURNS; ++t)
+            bin[t] = first + t * BINS + tid >= a.b ? -1 : (unsigned)bin[t] < (unsigned)a.count ? bin[t] & (BINS - 1) : BINS;
+    };
+    // the next place in a row's bin; one atomic where a wave's rows agree
+    auto take = [&](int to) {
+        const int first = __builtin_amdgcn_readfirstlane(to);
+        if (__ballot(to == first) == ~0ull) {
+            int at = 0;
+            if (lane == 0 && first >= 0) at = atomicAdd(&next[first], 64);
+            return __builtin_amdgcn_readfirstlane(at) + lane;
+        }
+        return to < 0 ? 0 : atomicAdd(&next[to], 1);
+    };
+    read(0);
+    for (int first = 0;; read(first)) {
+#pragma unroll
+        for (int t = 0; t < TURNS; ++t) take(bin[t]);
+        first += TURNS * BINS;
+        if (first >= a.b) break;
+    }
+    __syncthreads();
+    const int mine = next[tid];
+    int sum = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(sum, d);
+        if (lane >= d) sum += o;
+    }
+    if (lane == 63) sums[wave] = sum;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < BINS / 64; ++w) {
+        before += w < wave ? sums[w] : 0;
+        all += sums[w];
+    }
+    next[tid] = before + sum - mine;
+    if (tid == 0) next[BINS] = all;
+    __syncthreads();
+    if (a.b > TURNS * BINS) read(0);
+    for (int first = 0;; read(first)) {
+#pragma unroll
+        for (int t = 0; t < TURNS; ++t) {
+            const int at = take(bin[t]);
+            if (bin[t] >= 0) *gptr(a.order + at) = first + t * BINS + tid;
+        }
+        first += TURNS * BINS;
+        if (first >= a.b) break;
+    }
+}
+
 // The inner products of RT rank tiles of 16 in one segment (blockIdx.y).  The
 // W waves split the K range and add their sums in LDS in a fixed order.
-//   LEADER (few rows): one workgroup per row and K range (blockIdx.z); it works
+//   LEADER: one workgroup per row and K range (blockIdx.z); it works
 //     if its row is the 1st, 17th, 33rd .. of its adapter, for it and the next 15,
 //     so distinct adapters, and the parts of one that many rows share, run side by
 //     side.  The ranges' sums go to the workspace as they are.  Rows turn with the
-//     other indexes: of requests of 16 rows each, the first rows would all fall to one
-//     XCD (256 rows of 10696, rank 56, 16 adapters: 115 us instead of 34).
-//   otherwise: one workgroup per window of 32 rows; the workgroups of a window
-//     (blockIdx.z) take its adapters in turn (a packed prompt has one or two in a
-//     window).  h is written scaled and split, ready to be multiplied.
+//     other indexes: workgroups go round the eight XCDs, so of requests of 16 rows
+//     each the working ones would all fall to one (256 rows of 10696, rank 56, 16
+//     adapters: 115 us instead of 34).
+//   otherwise: a window of 32 rows, side by side or in order of their adapters; the
+//     workgroups of a window (blockIdx.z) take its adapters in turn.  h is written
+//     scaled and split, ready to be multiplied.
 // A wave reads 64 channels of its rows of A and x at a time, eight adjacent lanes
 // a row, D such pieces ahead, and turns them into operand order in a part of
 // LDS of its own (no barrier): read a lane per row straight into the operands,
-// the address unit bound this kernel (25 us, 3001 rows of 3584, two segments of rank 64).
+// the address unit bound this kernel (3001 rows of 3584, two segments of rank 64:
+// 25 us instead of 20).
 template <int W, int RT, int D, bool LEADER>
 __global__ __launch_bounds__(64 * W) void lora_down_kernel(LoraArgs a) {
     constexpr int NW = LEADER ? 4 : 1, WIN = LEADER ? 256 : 32, KC = 64;
@@ -120,8 +199,9 @@ __global__ __launch_bounds__(64 * W) void lora_down_kernel(LoraArgs a) {
     const int seg = blockIdx.y / a.groups, group = blockIdx.y % a.groups, j0 = group * 16 * RT;
     const int w0 = LEADER ? 0 : blockIdx.x * WIN;
     const int nwin = min(a.b - w0, WIN);
-    Window<NW> win;
+    Window<NW, !LEADER> win;
     win.read(a, w0, nwin, lane);
+    auto row_of = [&](int at) { return LEADER ? at : __shfl(win.row[0], at); };
     uint8_t* mem = lds[wave];
     auto place = [](int row, int ch) { return row * 2 * KC + 16 * (ch ^ (row & 7)); };
     const int pr = lane >> 3, pc = lane & 7;           // row and chunk of this lane in a piece
@@ -177,7 +257,7 @@ __global__ __launch_bounds__(64 * W) void lora_down_kernel(LoraArgs a) {
 #pragma unroll
             for (int i = 0; i < XP; ++i) {
                 const int col = c0 + 8 * i + pr;
-                xp[i] = a.x + (int64_t)(w0 + list[wave][col < total ? col : c0]) * a.ldx + 8 * pc;
+                xp[i] = a.x + (int64_t)row_of(list[wave][col < total ? col : c0]) * a.ldx + 8 * pc;
             }
             uint4 av[D][AP], xv[D][XP];
             auto load = [&](int d, int chunk) {
@@ -252,7 +332,7 @@ __global__ __launch_bounds__(64 * W) void lora_down_kernel(LoraArgs a) {
 #pragma unroll
                     for (int w = 1; w < W; ++w) v[t] += *red(w, CT * t + wave);
                 }
-                const int64_t row = (w0 + list[wave][col < total ? col : c0]);
+                const int64_t row = row_of(list[wave][col < total ? col : c0]);
                 if constexpr (LEADER) {
 #pragma unroll
                     for (int t = 0; t < RT; ++t) {
@@ -362,12 +442,13 @@ __device__ __forceinline__ int tile_segment(const LoraArgs& a, int width, int& n
     return seg;
 }
 
-// The outer products of a decode batch: 16 rows x 64 outputs of one segment per
+// The outer products of few rows: 16 rows x 64 outputs of one segment per
 // workgroup of four waves, one output tile a wave.  Each adapter of the 16 rows
 // gives a tile of results, of which its rows keep theirs.  A step is 16 ranks of
 // one adapter; the operands of the next 2 U steps are always on their way.
 // ONE: no adapter has more ranks than a step (R <= 16); then all rows' steps are
-// independent and run four at a time without a branch between them.
+// independent and run four at a time without a branch between them (64 rows of 64
+// adapters of rank 16 beside 10240 outputs: 9.6 us against 11.4).
 template <bool ONE>
 __global__ __launch_bounds__(256, 4) void lora_up_rows_kernel(LoraArgs a) {
     constexpr int TM = 16, U = 8;
@@ -381,7 +462,7 @@ __global__ __launch_bounds__(256, 4) void lora_up_rows_kernel(LoraArgs a) {
     const int seg = tile_segment(a, 64, n0), r0 = blockIdx.y * TM, rows = min(a.b - r0, TM);
     const int nw = n0 + 16 * wave, left = a.seg_end[seg] - nw;      // this wave's columns
     const bool whole = a.vec && (n0 & 7) == 0 && left >= 16;
-    Window<1> win;
+    Window<1, false> win;
     win.read(a, r0, rows, lane);
     uint32_t v[2] = {0, 0};
     if (a.base && m < rows) C::load(v, a.base + (int64_t)(r0 + m) * a.ldbase + nw, c, left, whole);
@@ -533,7 +614,7 @@ __global__ __launch_bounds__(256, 4) void lora_up_rows_kernel(LoraArgs a) {
     C::store(v, a.y + (int64_t)(r0 + m) * a.ldy + nw, c, left, whole);
 }
 
-// The outer products of a prompt: 64 rows, 16 to each of four waves, x 64
+// The outer products of windows: 64 rows, 16 to each of four waves, x 64
 // outputs at a time, over a.per such tiles; h comes scaled and split and stays in
 // registers.  One adapter of the rows after another, each writing its own rows.
 //
@@ -544,7 +625,7 @@ __global__ __launch_bounds__(256, 4) void lora_up_rows_kernel(LoraArgs a) {
 // (A lane-per-row access costs the address unit a lookup per lane: with it for
 // B, base and y this kernel took 125 us, 3001 rows, 28672 outputs, rank 64; with
 // 32 rows and a B of its own to each wave, and so only two waves on a SIMD, 110;
-// now 93, where copying base to y takes 65.  Two adapters of a window in one pass
+// now 92, where copying base to y takes 65.  Two adapters of a window in one pass
 // measured 114: the registers cost more than the second pass.)
 template <int RT, bool MULTI>
 __global__ __launch_bounds__(256, 4) void lora_up_wide_kernel(LoraArgs a) {
@@ -559,21 +640,29 @@ __global__ __launch_bounds__(256, 4) void lora_up_wide_kernel(LoraArgs a) {
     const int r0 = blockIdx.y * TM, rows = min(a.b - r0, TM);
     const int tiles = min(a.per, (hi - n_first + TN - 1) / TN), groups = MULTI ? a.groups : 1;
     const bool vec = a.vec && (n_first & 3) == 0;
-    Window<1> win;
+    Window<1, true> win;
     win.read(a, r0, rows, lane);
 
     // a lane's rows 16 wave + 4 c + e, its columns 4 m .. 4 m + 3 of the tile
-    const int row0 = 16 * wave + 4 * c;
-    const uint16_t* bp = a.base ? a.base + (int64_t)(r0 + row0) * a.ldbase + n_first + 4 * m : nullptr;
-    uint16_t* yp = a.y + (int64_t)(r0 + row0) * a.ldy + n_first + 4 * m;
+    const int row0 = 16 * wave + 4 * c, hrow = __shfl(win.row[0], 16 * wave + m);
+    int row[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) row[e] = __shfl(win.row[0], row0 + e);
+    // a row's offset is worked out at each use (the empty asm): kept, the offsets
+    // of four rows of base and y cost the registers that the loads ahead need
+    auto at = [](const uint16_t* p, int r, int64_t ld, int n) {
+        asm("" : "+v"(r));
+        return p + r * ld + n;
+    };
+    const int n_lane = n_first + 4 * m;
     uint2 v[4];
-    auto load_base = [&](int i, uint32_t of) {         // bit e of `of`: row row0 + e
+    auto load_base = [&](int i, uint32_t of) {         // bit e of `of`: row[e]
         const int left = hi - n_first - i * TN - 4 * m;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             v[e] = make_uint2(0, 0);
             if (!a.base || !(of >> e & 1)) continue;
-            const uint16_t* p = bp + e * a.ldbase + i * TN;
+            const uint16_t* p = at(a.base, row[e], a.ldbase, n_lane + i * TN);
             if (vec && left >= 4) {
                 v[e] = gload_u2(reinterpret_cast<const uint2*>(p));
             } else {
@@ -588,7 +677,7 @@ __global__ __launch_bounds__(256, 4) void lora_up_wide_kernel(LoraArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if (!(of >> e & 1)) continue;
-            uint16_t* p = yp + e * a.ldy + i * TN;
+            uint16_t* p = const_cast<uint16_t*>(at(a.y, row[e], a.ldy, n_lane + i * TN));
             if (vec && left >= 4) {
                 *(__attribute__((address_space(1))) u32x2*)p = u32x2{v[e].x, v[e].y};
             } else {
@@ -610,15 +699,14 @@ __global__ __launch_bounds__(256, 4) void lora_up_wide_kernel(LoraArgs a) {
     h8 hv[RT];
     int ex[4];
     auto load_h = [&](int g) {
-        const int64_t at = ((int64_t)min(r0 + 16 * wave + m, a.b - 1) * a.nseg + seg) * groups + g;
-        const uint16_t* p = reinterpret_cast<const uint16_t*>(a.h) + at * 32 * RT + 8 * c;
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(a.h) + (((int64_t)hrow * a.nseg + seg) * groups + g) * 32 * RT + 8 * c;
 #pragma unroll
         for (int t = 0; t < RT; ++t) hv[t] = as_h8(load16(p + 32 * t));
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            ex[e] = *gptr(a.exps + ((int64_t)min(r0 + row0 + e, a.b - 1) * a.nseg + seg) * groups + g);
+            ex[e] = *gptr(a.exps + ((int64_t)row[e] * a.nseg + seg) * groups + g);
     };
-    // none of these waits for the adapters to be known
+    // neither of these waits for the adapters to be known
     load_h(0);
     load_base(0, (uint32_t)(~0ull >> (64 - rows) >> row0) & 15u);
     bool once = true;
@@ -737,20 +825,46 @@ __global__ __launch_bounds__(256, 4) void lora_up_wide_kernel(LoraArgs a) {
     }
 }
 
-// Rows up to which a workgroup per row looks for its adapter's other rows.
+// Rows that a workgroup per row may serve: as many as its waves look over.
 constexpr int LEADER_ROWS = 256;
+
+// A workgroup per row (which reads an adapter's A once for 16 of its rows, wherever
+// they are, and its B once for each 16 rows of the batch that have one of it)
+// or windows of rows (which read each of their adapters once, but with the long K
+// of few windows on few compute units).  Both launches, us, row by row | windows, 1
+// to 16 adapters, rows of one side by side or not:
+//   64 rows:  12-18 | 16-35 (10240 x 8192, rank 16), 17-51 | 21-48 (28672 x 3584, rank 64)
+//   128 rows: 15-22 | 16-27, 27-87 | 22-41, and 20-31 | 15-28 (28672 x 3584, rank 16)
+//   192 rows: 21-29 | 19-26, 36-125 | 25-47, 26-40 | 18-33; 19-31 | 28-34 (3584 x 14336)
+//   256 rows: 23-34 | 19-24, 41-163 | 26-43, 31-51 | 19-29; 23-36 | 28-34, 12-21 | 12-18 (1024 x 1024)
+// so wide outputs make windows of 97 rows and more; with fewer than eight rows to an
+// adapter they lose again (128 rows, 64 adapters: 25-34 | 62-66, 28672 x 3584, rank 16).
+bool row_by_row(const LoraArgs& a) {
+    if (a.b > LEADER_ROWS) return false;
+    return a.b <= 96 || (int64_t)a.b * a.N <= 1 << 21 || 8 * (int64_t)a.count > a.b;
+}
+
 // K ranges of a row's inner products, at most, in that form.
 constexpr int LEADER_SPLITS = 16;
+
+// Whether windows take the rows in order of their adapters: one more launch, 3.3 us
+// at 256 rows and 5 at 4096, against windows that go through every adapter of a batch
+// whose rows lie mixed (4096 rows beside 28672 x 3584, rank 64: 16 adapters 910 -> 159 us,
+// 8 487 -> 149, 4 274 -> 142; 1021 rows: 254 -> 65, 138 -> 58, 78 -> 56; 384 rows: 133 ->
+// 52, 71 -> 37, 42 -> 33).  Packed prompts, whose rows lie in order, gain nothing: below
+// this bound they are left as they are.
+bool in_order(const LoraArgs& a) { return (int64_t)(a.count - 1) * a.b >= 4096; }
 
 // 16-rank tiles that a window's workgroup takes together.
 int rank_tiles(int64_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }
 
-// K ranges that leave every wave of a few rows' workgroups one round of loads,
-// four pieces of 64 channels.
-// More where that would be over three workgroups to a compute unit, which is
-// what its registers hold (64 rows of 8192, three segments, an adapter each: 12.3 -> 11.5 us).
+// K ranges that leave every wave of a few rows' workgroups one round of loads, four
+// pieces of 64 channels; fewer where the workgroups that find work would be over three
+// to a compute unit, which is what their registers leave room for (64 rows of 8192,
+// three segments, an adapter each: 12.3 -> 11.5 us).
 int k_ranges(const LoraArgs& a) {
-    const int64_t units = (int64_t)std::min(a.b, a.count + a.b / 16 + 1) * a.nseg * a.groups, room = std::max<int64_t>(1, 3 * woq::compute_units() / units);
+    const int64_t units = (int64_t)std::min(a.b, a.count + a.b / 16 + 1) * a.nseg * a.groups;
+    const int64_t room = std::max<int64_t>(1, 3 * woq::compute_units() / units);
     return (int)std::min<int64_t>(std::min<int64_t>(woq::ceil_div(a.K, 4 * 4 * 64), LEADER_SPLITS), room);
 }
 
@@ -783,9 +897,18 @@ template <int RT, int D>
 hipError_t launch_many(LoraArgs a, hipStream_t s) {
     a.groups = (int)woq::ceil_div(a.R, 16 * RT);
     a.exps = reinterpret_cast<int32_t*>(a.h) + (int64_t)a.b * a.nseg * a.groups * 16 * RT;
-    // workgroups of a window, which take its adapters in turn; most find none left
+    hipError_t e = hipSuccess;
+    if (in_order(a)) {
+        a.order = a.exps + (int64_t)a.b * a.nseg * a.groups;
+        e = launch(reinterpret_cast<const void*>(&lora_order_kernel), dim3(1), BINS, 0, s, a);
+        if (e != hipSuccess) return e;
+    }
+    // workgroups of a window, which take its adapters in turn; those of a window of one
+    // adapter find none left, which costs nothing (1021 rows beside 10240 x 8192, one
+    // adapter: 25.0 us with one and with eight; 16 adapters in windows of their
+    // own 34.3 -> 27.8, 64 63.7 -> 49.9)
     const int slots = std::max(1, std::min(8, a.count));
-    hipError_t e = launch(reinterpret_cast<const void*>(&lora_down_kernel<8, RT, D, false>),
+    e = launch(reinterpret_cast<const void*>(&lora_down_kernel<8, RT, D, false>),
                           dim3((unsigned)woq::ceil_div(a.b, 32), (unsigned)(a.nseg * a.groups), (unsigned)slots), 512, 0, s, a);
     if (e != hipSuccess) return e;
     // tiles a workgroup goes through: more where there is work enough for the device
@@ -833,11 +956,12 @@ extern "C" {
 int64_t woq_lora_workspace(const woq_lora_w* w, int64_t b) {
     if (check_lora_w(w) != WOQ_OK || b < 0) return WOQ_EINVAL;
     if ((w->R & 7) || w->R > WOQ_LORA_MAX_R || b > WOQ_LORA_MAX_ROWS) return WOQ_EUNSUPPORTED;
-    // few rows: the ranges' sums; many: halves and an exponent for each group
-    // of ranks.  No less for more rows, so one workspace serves smaller batches.
+    // row by row: the K ranges' sums; windows: halves, an exponent for each group of
+    // ranks, and the order.  No less for more rows, so that one workspace serves
+    // smaller batches.
     const int64_t few = std::min<int64_t>(b, LEADER_ROWS) * LEADER_SPLITS * w->nseg * w->R * 4;
-    const int64_t width = 16 * rank_tiles(w->R), many = b * w->nseg * woq::ceil_div(w->R, width) * (width * 4 + 4);
-    return std::max<int64_t>(16, b <= LEADER_ROWS ? few : std::max(few, many));
+    const int64_t width = 16 * rank_tiles(w->R), many = b * (w->nseg * woq::ceil_div(w->R, width) * (width * 4 + 4) + 4);
+    return std::max<int64_t>(16, std::max(few, many));
 }
 
 int woq_lora_add(const woq_lora_w* w, const uint16_t* x, int64_t ldx, const int32_t* ids, int64_t b,
@@ -866,12 +990,12 @@ int woq_lora_add(const woq_lora_w* w, const uint16_t* x, int64_t ldx, const int3
     a.count = w->count;
     a.nseg = w->nseg;
     a.splits = a.groups = a.per = 1;
-    a.exps = nullptr;
+    a.exps = a.order = nullptr;
     a.vec = woq::aligned16(y) && (ldy & 7) == 0 && (!base || (woq::aligned16(base) && (ldbase & 7) == 0));
     for (int i = 0; i < WOQ_MAX_SEGMENTS; ++i) a.seg_end[i] = i < w->nseg ? (int)w->seg_end[i] : (int)w->N;
     hipStream_t s = (hipStream_t)stream;
     hipError_t e;
-    if (b <= LEADER_ROWS) e = launch_few(a, s);
+    if (row_by_row(a)) e = launch_few(a, s);
     else if (rank_tiles(a.R) == 1) e = launch_many<1, 4>(a, s);
     else if (rank_tiles(a.R) == 2) e = launch_many<2, 2>(a, s);
     else e = launch_many<4, 2>(a, s);
