@@ -4,7 +4,8 @@
 //   h[r, i] = sum_k A[a][i, k] x[r, k],   a = ids[r],
 //
 // with y = base on rows without an adapter.  Two launches: the inner products
-// h into the workspace, and the outer ones added to the base.
+// h into the workspace, and the outer ones added to the base; before them, in
+// batches of many rows and adapters, one that puts the rows in order.
 //
 // Both run on the fp16 matrix cores with 16 ranks (or 16 outputs) of ONE
 // adapter against 16 rows: rows that share an adapter share its bytes, and a
@@ -16,12 +17,12 @@
 // A decode batch is bound by the bytes of the adapters that its rows name, or,
 // at a few rows, by two launches of a few memory round trips each: the kernels
 // keep every load of a round in flight together and have no barrier before the
-// sums meet.  One row beside 8192 x 8192, rank 16: 4.2 + 4.5 us; 64 rows beside
-// 10240 x 8192 in three segments, an adapter of rank 16 each: 10-13 + 9.6 us,
+// sums meet.  One row beside 8192 x 8192, rank 16: 4.2 + 4.8 us; 64 rows beside
+// 10240 x 8192 in three segments, an adapter of rank 16 each: 10.4 + 9.8 us,
 // 75 MB at 3.7 TB/s.  (Both products in one launch, each workgroup computing h
 // for its 1024 outputs: 11.2 and 36 us.)  A prompt is bound by the base and the
-// output: 3001 rows beside 28672 x 3584 in two segments, rank 64: 20 + 92 us,
-// 402 MB at 3.6 TB/s.
+// output: 3001 rows beside 28672 x 3584 in two segments, 8 adapters of rank 64:
+// 5 + 20 + 90 us, 402 MB at 3.5 TB/s.
 #include <hip/hip_runtime.h>
 
 #include "woq_gemv.h"
@@ -625,7 +626,7 @@ __global__ __launch_bounds__(256, 4) void lora_up_rows_kernel(LoraArgs a) {
 // (A lane-per-row access costs the address unit a lookup per lane: with it for
 // B, base and y this kernel took 125 us, 3001 rows, 28672 outputs, rank 64; with
 // 32 rows and a B of its own to each wave, and so only two waves on a SIMD, 110;
-// now 92, where copying base to y takes 65.  Two adapters of a window in one pass
+// now 90, where copying base to y takes 65.  Two adapters of a window in one pass
 // measured 114: the registers cost more than the second pass.)
 template <int RT, bool MULTI>
 __global__ __launch_bounds__(256, 4) void lora_up_wide_kernel(LoraArgs a) {
@@ -903,10 +904,9 @@ hipError_t launch_many(LoraArgs a, hipStream_t s) {
         e = launch(reinterpret_cast<const void*>(&lora_order_kernel), dim3(1), BINS, 0, s, a);
         if (e != hipSuccess) return e;
     }
-    // workgroups of a window, which take its adapters in turn; those of a window of one
-    // adapter find none left, which costs nothing (1021 rows beside 10240 x 8192, one
-    // adapter: 25.0 us with one and with eight; 16 adapters in windows of their
-    // own 34.3 -> 27.8, 64 63.7 -> 49.9)
+    // workgroups of a window, which take its adapters in turn: of 1021 rows beside
+    // 10240 x 8192, rank 16, 64 adapters side by side 63.7 us with one, 49.9 with eight,
+    // 16 adapters 34.3 and 27.8, and the same 25 where all rows have the only one
     const int slots = std::max(1, std::min(8, a.count));
     e = launch(reinterpret_cast<const void*>(&lora_down_kernel<8, RT, D, false>),
                           dim3((unsigned)woq::ceil_div(a.b, 32), (unsigned)(a.nseg * a.groups), (unsigned)slots), 512, 0, s, a);
