@@ -849,7 +849,7 @@ bool row_by_row(const LoraArgs& a) {
 constexpr int LEADER_SPLITS = 16;
 
 // Whether windows take the rows in order of their adapters: one more launch, 3.3 us
-// at 256 rows and 5 at 4096, against windows that go through every adapter of a batch
+// at 256 rows, 5 at 4096 and 10 at 16384, against windows that go through every adapter of a batch
 // whose rows lie mixed (4096 rows beside 28672 x 3584, rank 64: 16 adapters 910 -> 159 us,
 // 8 487 -> 149, 4 274 -> 142; 1021 rows: 254 -> 65, 138 -> 58, 78 -> 56; 384 rows: 133 ->
 // 52, 71 -> 37, 42 -> 33).  Packed prompts, whose rows lie in order, gain nothing: below
@@ -904,12 +904,14 @@ hipError_t launch_many(LoraArgs a, hipStream_t s) {
         e = launch(reinterpret_cast<const void*>(&lora_order_kernel), dim3(1), BINS, 0, s, a);
         if (e != hipSuccess) return e;
     }
-    // workgroups of a window, which take its adapters in turn: of 1021 rows beside
-    // 10240 x 8192, rank 16, 64 adapters side by side 63.7 us with one, 49.9 with eight,
-    // 16 adapters 34.3 and 27.8, and the same 25 where all rows have the only one
-    const int slots = std::max(1, std::min(8, a.count));
+    // workgroups of a window, which take its adapters in turn, as long as that is two
+    // to a compute unit; those that find none left cost their start.  Eight against one,
+    // beside 1024 x 1024, rank 16, 8 adapters: 2048 rows 14.6 us and 15.1 (two 14.1),
+    // 16384 rows 56 and 36; 2048 rows beside 8192 x 3584 in three segments 35 and 29
+    const int64_t windows = woq::ceil_div(a.b, 32), each = windows * a.nseg * a.groups;
+    const int slots = (int)std::max<int64_t>(1, std::min<int64_t>({8, a.count, 2 * woq::compute_units() / each}));
     e = launch(reinterpret_cast<const void*>(&lora_down_kernel<8, RT, D, false>),
-                          dim3((unsigned)woq::ceil_div(a.b, 32), (unsigned)(a.nseg * a.groups), (unsigned)slots), 512, 0, s, a);
+                          dim3((unsigned)windows, (unsigned)(a.nseg * a.groups), (unsigned)slots), 512, 0, s, a);
     if (e != hipSuccess) return e;
     // tiles a workgroup goes through: more where there is work enough for the device
     const int64_t rows = woq::ceil_div(a.b, 64);
