@@ -418,6 +418,30 @@ def test_adapters_of_a_mixed_batch_captured_and_replayed(gpu_lib):
         np.testing.assert_array_equal(host(y).view(np.uint16), host(eager).view(np.uint16))
 
 
+@pytest.mark.parametrize("R", [8, 32, 64, 72])
+@pytest.mark.parametrize("b", [5, 300])
+def test_adapters_eight_segments_some_empty(gpu_lib, b, R):
+    """Every kernel sees the same tiles of every segment: eight of them, empty
+    ones at the start, inside and at the end, beside ends that are not tiles'."""
+    import torch
+    case("adapters eight segments", b, R)
+    rng = np.random.default_rng(b + R)
+    N, K, count, ends = 260, 72, 3, [0, 1, 66, 66, 130, 259, 260, 260]
+    A = (rng.standard_normal((count, 8 * R, K)) / np.sqrt(K)).astype(np.float16)
+    B = (rng.standard_normal((count, N, R)) * 0.3).astype(np.float16)
+    s = (0.5 + rng.random(count)).astype(np.float32)
+    x, base = rng.standard_normal((b, K)).astype(np.float16), rng.standard_normal((b, N)).astype(np.float16)
+    ids = rng.integers(-1, count, b).astype(np.int32)
+    pool = woq.DeviceLora(dev(A), dev(B), dev(s), segments=ends)
+    ws = torch.empty(woq.woq_lora_workspace(pool.desc, b), dtype=torch.uint8, device="cuda")
+    y = full(b, N + 4, 7, "float16")
+    woq.woq_lora_add(pool.desc, dev(x), dev(ids), dev(base), y, ws)
+    ref, spread = O.lora_add(base, x, ids, A, B, s, ends)
+    g = host(y)
+    within(g[:, :N], ref, np.abs(ref) * (H + 2 * U) + SUB + spread * ((K / 16 + R + 32) * U + 2.0 ** -20))
+    assert np.all(g[:, N:] == 7)
+
+
 @pytest.mark.parametrize("b", [1, 20, 100, 300])
 def test_adapters_of_different_ranks(gpu_lib, b):
     """Entries past an adapter's rank and past K are NaN and stay out of it."""

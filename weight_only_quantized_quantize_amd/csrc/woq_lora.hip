@@ -916,9 +916,12 @@ hipError_t launch_many(LoraArgs a, hipStream_t s) {
     // tiles a workgroup goes through: more where there is work enough for the device
     const int64_t rows = woq::ceil_div(a.b, 64);
     a.per = (int)std::max<int64_t>(1, std::min<int64_t>(4, rows * woq::ceil_div(a.N, 64) / 1024));
+    // counted before the call: the launch takes a copy of a, tile0 included, and the
+    // order in which arguments are made is not defined
+    const unsigned tiles = count_tiles(a, 64 * a.per);
     return launch(a.groups > 1 ? reinterpret_cast<const void*>(&lora_up_wide_kernel<RT, RT == 4>)
                                : reinterpret_cast<const void*>(&lora_up_wide_kernel<RT, false>),
-                  dim3(count_tiles(a, 64 * a.per), (unsigned)rows), 256, 0, s, a);
+                  dim3(tiles, (unsigned)rows), 256, 0, s, a);
 }
 
 int check_lora_w(const woq_lora_w* w) {
