@@ -459,6 +459,12 @@ int woq_add_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* res, int64_t
 #define WOQ_A8_MAX_K 131072
 int woq_qgemm_int8_a8(const woq_int8_w* w, const int8_t* xq, int64_t ldq, const float* xs, int64_t b, uint16_t* y,
                       int64_t ldy, void* stream);
+/*
+ * Rows of activations and of weights that one workgroup of that product takes
+ * for these sizes on the current device (the choice counts its compute units,
+ * 256 where there is no device).
+ */
+int woq_qgemm_int8_a8_tile(int64_t N, int64_t b, int32_t* rows, int32_t* cols);
 
 /* ---------------------------------------------- device ops: adapters */
 

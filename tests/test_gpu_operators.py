@@ -255,6 +255,44 @@ def test_product_segments_and_strides(gpu_lib, b):
         check_a8(N, 700, b, b, ends, ldy, pad)
 
 
+# (N, K, b, tile): every tile of the product, with rows and outputs that end inside
+# it, several rounds of workgroups on the largest, and K of one stage, of an odd and
+# an even number of them, fewer and more than are read ahead
+PRODUCT_TILES = [
+    (100, 1100, 5, (16, 16)), (4100, 600, 13, (16, 32)), (9000, 300, 9, (16, 64)), (28600, 200, 3, (16, 128)),
+    (28600, 50, 15, (16, 128)), (3900, 1000, 33, (32, 32)), (3901, 600, 40, (32, 32)), (8052, 700, 33, (32, 64)), (8053, 260, 40, (32, 64)),
+    (1000, 700, 1000, (64, 64)), (1010, 200, 1001, (64, 64)), (28600, 200, 61, (64, 128)), (28606, 600, 33, (64, 128)),
+    (28600, 100, 64, (64, 128)), (4100, 640, 300, (64, 128)), (4100, 130, 250, (64, 128)), (1000, 300, 3001, (128, 128)),
+    (28670, 200, 70, (128, 128)), (8190, 300, 1021, (128, 256)), (8190, 128, 900, (128, 256)), (28670, 200, 1021, (256, 256)),
+    (28670, 100, 400, (256, 256)), (16390, 400, 1300, (256, 256)), (2000, 333, 5003, (256, 256)),
+]
+
+
+def check_product_tile(N, K, b, ends, ldy, pad):
+    rng = np.random.default_rng(N + K + b)
+    codes, scales, w = a8_weight(N, K, rng, ends)
+    xq = rng.integers(-128, 128, (b, K)).astype(np.int8)
+    xs = (1e-4 + 1e-3 * rng.random(b)).astype(np.float32)
+    y = full(b, ldy, 7, "float16")
+    woq.woq_qgemm_int8_a8(w.desc, padded(xq, up(K, 16) + 16 * pad, 77), dev(xs), y)
+    sums = xq.astype(np.float64) @ codes.T.astype(np.float64)      # integers below 2^53: exact
+    col = np.repeat(np.array(scales, np.float64), np.diff([0] + ends))
+    ref = sums * col[None, :] * xs.astype(np.float64)[:, None]
+    g = host(y)
+    within(g[:, :N], ref, np.abs(ref) * (H + 4 * U) + SUB, (N, K, b))
+    assert np.all(g[:, N:] == 7)
+
+
+@pytest.mark.parametrize("N,K,b,tile", PRODUCT_TILES)
+def test_product_every_tile(gpu_lib, N, K, b, tile):
+    import torch
+    if torch.cuda.get_device_properties(0).multi_processor_count == 256:
+        assert woq.woq_qgemm_int8_a8_tile(N, b) == tile
+    for ends, ldy, pad in (([N], N, 0), ([N // 3, N // 3, N - 7, N], N + 3, 1)):
+        case("product tile", N, K, b, tile, ends, ldy)
+        check_product_tile(N, K, b, ends, ldy, pad)
+
+
 @pytest.mark.parametrize("code", [127, -128])
 def test_product_extreme_sums_stay_exact(gpu_lib, code):
     """Every product at its largest over the longest row: 127 * 128 * 131072 < 2^31."""

@@ -124,6 +124,22 @@ def test_product_refusals(change, status):
     assert call("woq_qgemm_int8_a8", *a.values()) == status
 
 
+def test_product_tiles():
+    """The GPU's cases reach every tile that any size takes (on 256 compute units)."""
+    from test_gpu_operators import PRODUCT_TILES
+    tiles = {woq.woq_qgemm_int8_a8_tile(N, b) for N in list(range(1, 70000, 97)) + [128256, 262144, 1 << 24]
+             for b in (1, 2, 16, 17, 32, 33, 50, 64, 65, 128, 129, 200, 256, 257, 400, 512, 1000, 1021, 3001, 4096, 70000)}
+    assert tiles == {woq.woq_qgemm_int8_a8_tile(N, b) for N, _, b, _ in PRODUCT_TILES}
+    for N, _, b, tile in PRODUCT_TILES:
+        assert woq.woq_qgemm_int8_a8_tile(N, b) == tile, (N, b)
+    for N, b, status in ((0, 1, woq.WOQ_EINVAL), (1, 0, woq.WOQ_EINVAL), (1 << 31, 1, woq.WOQ_EUNSUPPORTED),
+                         (1, 1 << 31, woq.WOQ_EUNSUPPORTED)):
+        with pytest.raises(woq.WoqError) as e:
+            woq.woq_qgemm_int8_a8_tile(N, b)
+        assert e.value.status == status
+    assert call("woq_qgemm_int8_a8_tile", 1, 1, None, None) == woq.WOQ_EINVAL
+
+
 def pool(N=40, K=100, lda=104, R=16, count=3, ends=None, **ptrs):
     w = woq.LoraW()
     ends = [N] if ends is None else ends

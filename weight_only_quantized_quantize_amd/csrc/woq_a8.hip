@@ -290,12 +290,12 @@ const A8Plan PLANS[] = {
 // more than that reuse gains (256 rows of 3584 x 14336: 64 x 64 33.4 us,
 // 64 x 128, half the workgroups, 46).  Of two tiles of one size, the one with more
 // workgroups.
-const A8Plan& choose_plan(const A8Args& a) {
+const A8Plan& choose_plan(int64_t N, int64_t b) {
     const int64_t cus = woq::compute_units();
     const A8Plan* best = nullptr;
     int64_t best_tiles = 0;
     for (const A8Plan& p : PLANS) {
-        const int64_t tiles = woq::ceil_div(a.b, p.bm) * woq::ceil_div(a.N, p.bn);
+        const int64_t tiles = woq::ceil_div(b, p.bm) * woq::ceil_div(N, p.bn);
         if (best && p.bm * p.bn > best->bm * best->bn) break;
         if (tiles <= cus && (!best || tiles > best_tiles)) best = &p, best_tiles = tiles;
     }
@@ -303,6 +303,15 @@ const A8Plan& choose_plan(const A8Args& a) {
 }
 
 }  // namespace
+
+extern "C" int woq_qgemm_int8_a8_tile(int64_t N, int64_t b, int32_t* rows, int32_t* cols) {
+    if (N < 1 || b < 1 || !rows || !cols) return WOQ_EINVAL;
+    if (N > (int64_t)INT32_MAX - 512 || b > (int64_t)INT32_MAX - 512) return WOQ_EUNSUPPORTED;
+    const A8Plan& p = choose_plan(N, b);
+    *rows = p.bm;
+    *cols = p.bn;
+    return WOQ_OK;
+}
 
 extern "C" int woq_qgemm_int8_a8(const woq_int8_w* w, const int8_t* xq, int64_t ldq, const float* xs, int64_t b,
                                  uint16_t* y, int64_t ldy, void* stream) {
@@ -336,7 +345,7 @@ extern "C" int woq_qgemm_int8_a8(const woq_int8_w* w, const int8_t* xq, int64_t 
         a.seg_scale[i] = i < w->nseg ? w->seg_scale[i] : 0.0f;
     }
     a.vec = ((uintptr_t)y & 7u) == 0 && (ldy & 3) == 0;
-    const hipError_t e = choose_plan(a).launch(a, (hipStream_t)stream);
+    const hipError_t e = choose_plan(a.N, a.b).launch(a, (hipStream_t)stream);
     if (e != hipSuccess) {
         woq::set_hip_error((int)e);
         return WOQ_EHIP;

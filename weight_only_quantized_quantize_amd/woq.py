@@ -108,6 +108,7 @@ _SIGS = {
     "woq_add_rmsnorm": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_float, c_float, c_int64, c_int64,
                                 c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p]),
     "woq_qgemm_int8_a8": (c_int, [POINTER(Int8W), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p]),
+    "woq_qgemm_int8_a8_tile": (c_int, [c_int64, c_int64, POINTER(c_int32), POINTER(c_int32)]),
     "woq_lora_add": (c_int, [POINTER(LoraW), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
                              c_int64, c_void_p, c_int64, c_void_p]),
     "woq_lora_workspace": (c_int64, [POINTER(LoraW), c_int64]),
@@ -566,6 +567,14 @@ def woq_qgemm_int8_a8(w: Int8W, xq, xs, y, stream=None, b: int | None = None):
     yp, ldy = _rows(y, "y", _torch.float16, b, w.N)
     _call("woq_qgemm_int8_a8", stream, (xq, xs, y), w, xp, ldq, _vector(xs, "xs", _torch.float32, b), b, yp, ldy)
     return y
+
+
+def woq_qgemm_int8_a8_tile(N: int, b: int):
+    """(rows of activations, rows of weights) that one workgroup of
+    woq_qgemm_int8_a8 takes for these sizes."""
+    rows, cols = c_int32(), c_int32()
+    _check(_lib().woq_qgemm_int8_a8_tile(N, b, ctypes.byref(rows), ctypes.byref(cols)), "woq_qgemm_int8_a8_tile")
+    return rows.value, cols.value
 
 
 def woq_lora_workspace(w: LoraW, b: int) -> int:
