@@ -293,6 +293,16 @@ def test_product_every_tile(gpu_lib, N, K, b, tile):
         check_product_tile(N, K, b, ends, ldy, pad)
 
 
+@pytest.mark.parametrize("N,K,b,rows", [(33000, 200, 1, 16), (66000, 90, 16, 16), (66010, 300, 17, 32), (33003, 140, 61, 64),
+                                        (66000, 150, 100, 128)])
+def test_product_of_wide_weights_and_few_rows(gpu_lib, N, K, b, rows):
+    """More workgroups than compute units: several rounds of a tile no taller than the batch needs."""
+    assert woq.woq_qgemm_int8_a8_tile(N, b)[0] == rows
+    for ends, ldy, pad in (([N], N, 0), ([5, N - 1000, N], N + 5, 2)):
+        case("product wide", N, K, b, rows, ends, ldy)
+        check_product_tile(N, K, b, ends, ldy, pad)
+
+
 @pytest.mark.parametrize("code", [127, -128])
 def test_product_extreme_sums_stay_exact(gpu_lib, code):
     """Every product at its largest over the longest row: 127 * 128 * 131072 < 2^31."""

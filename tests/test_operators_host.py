@@ -140,6 +140,20 @@ def test_product_tiles():
     assert call("woq_qgemm_int8_a8_tile", 1, 1, None, None) == woq.WOQ_EINVAL
 
 
+@pytest.mark.parametrize("N", [1, 1000, 16400, 28672, 32768, 32784, 57344, 65536, 65552, 131072, 152064, 1 << 24])
+def test_product_tiles_are_not_far_taller_than_the_batch(N):
+    """However wide the weight: a workgroup of 128 or 256 rows for a batch of few
+    would multiply mostly rows that are not there."""
+    for b in (1, 2, 8, 15, 16, 17, 31, 32, 33, 50, 61, 64, 65, 100, 128):
+        rows, _ = woq.woq_qgemm_int8_a8_tile(N, b)
+        assert rows <= (64 if b <= 64 else 128), (N, b, rows)
+        if N > 1 << 16:                     # several rounds of workgroups, whatever the tile
+            assert rows == min(r for r in (16, 32, 64, 128) if r >= b), (N, b, rows)
+    for n, b in ((N, 1), (1 << 30, 1), (1 << 30, 33), (1 << 24, 16384)):    # a launch has fewer than 2^32 threads
+        rows, cols = woq.woq_qgemm_int8_a8_tile(n, b)
+        assert -(-n // cols) * -(-b // rows) * 512 < 1 << 32
+
+
 def pool(N=40, K=100, lda=104, R=16, count=3, ends=None, **ptrs):
     w = woq.LoraW()
     ends = [N] if ends is None else ends

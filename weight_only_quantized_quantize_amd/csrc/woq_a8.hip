@@ -263,43 +263,56 @@ hipError_t launch_lds(A8Args a, hipStream_t s) {
 // side are (256 rows of 8192 x 3584: 16.5 against 17.1).
 struct A8Plan {
     int bm, bn;
+    bool rounds;              // of the tiles as tall, the one for several rounds of workgroups
     hipError_t (*launch)(A8Args, hipStream_t);
 };
 const A8Plan PLANS[] = {
-    {16, 16, &launch_lds<16, 16, 1, 1, 8, 512, 2, true>},
-    {16, 32, &launch_lds<16, 32, 1, 2, 4, 512, 2, false>},
-    {16, 64, &launch_lds<16, 64, 1, 4, 2, 256, 2, true>},
-    {32, 32, &launch_lds<32, 32, 1, 2, 4, 512, 2, false>},
-    {16, 128, &launch_lds<16, 128, 1, 4, 2, 256, 2, false>},
-    {32, 64, &launch_lds<32, 64, 1, 2, 4, 256, 2, false>},
-    {64, 64, &launch_lds<64, 64, 2, 2, 4, 256, 2, true>},
-    {64, 128, [](A8Args a, hipStream_t s) {
+    {16, 16, false, &launch_lds<16, 16, 1, 1, 8, 512, 2, true>},
+    {16, 32, false, &launch_lds<16, 32, 1, 2, 4, 512, 2, false>},
+    {16, 64, true, &launch_lds<16, 64, 1, 4, 2, 256, 2, true>},
+    {32, 32, false, &launch_lds<32, 32, 1, 2, 4, 512, 2, false>},
+    {16, 128, false, &launch_lds<16, 128, 1, 4, 2, 256, 2, false>},
+    {32, 64, true, &launch_lds<32, 64, 1, 2, 4, 256, 2, false>},
+    {64, 64, false, &launch_lds<64, 64, 2, 2, 4, 256, 2, true>},
+    {64, 128, true, [](A8Args a, hipStream_t s) {
          return a.b <= 64 ? launch_lds<64, 128, 2, 4, 1, 128, 4, false>(a, s)
                           : launch_lds<64, 128, 1, 4, 2, 128, 4, false>(a, s);
      }},
-    {128, 128, &launch_lds<128, 128, 2, 4, 1, 128, 2, false>},
-    {128, 256, &launch_lds<128, 256, 2, 4, 1, 128, 2, true>},
-    {256, 256, &launch_lds<256, 256, 2, 4, 1, 128, 1, true>},
+    {128, 128, true, &launch_lds<128, 128, 2, 4, 1, 128, 2, false>},
+    {128, 256, false, &launch_lds<128, 256, 2, 4, 1, 128, 2, true>},
+    {256, 256, true, &launch_lds<256, 256, 2, 4, 1, 128, 1, true>},
 };
 
-// The smallest tile that still gives at most one workgroup to a compute unit,
-// else the largest: a second round of workgroups cost more than the reuse
-// that a larger tile adds (256 rows of 8192 x 3584: 64 x 128 tiles 16.5 us,
-// 64 x 64 17.3; 1021 rows: 128 x 256 36.8, 128 x 128 38.9; 509 rows of
-// 28672 x 3584: 256 x 256 60.9, 128 x 256 75.5), and idle compute units cost
-// more than that reuse gains (256 rows of 3584 x 14336: 64 x 64 33.4 us,
-// 64 x 128, half the workgroups, 46).  Of two tiles of one size, the one with more
-// workgroups.
+// The smallest tile that still gives at most one workgroup to a compute unit: a
+// second round of workgroups cost more than the reuse that a larger tile adds
+// (256 rows of 8192 x 3584: 64 x 128 tiles 16.5 us, 64 x 64 17.3; 1021 rows:
+// 128 x 256 36.8, 128 x 128 38.9; 509 rows of 28672 x 3584: 256 x 256 60.9,
+// 128 x 256 75.5), and idle compute units cost more than that reuse gains (256
+// rows of 3584 x 14336: 64 x 64 33.4 us, 64 x 128, half the workgroups, 46).  Of
+// two tiles of one size, the one with more workgroups.
+//
+// Rows of a tile past the batch reuse nothing, and tall tiles read ahead the
+// least: up to 64 rows take no tile of more than 64, and where no tile fits one
+// round, a batch takes several rounds of the lowest one that holds it.  us, that
+// one | the 128 x 256 tile where it fits one round, else 256 x 256:
+//   32784 x 3584:   1 row 25 | 33, 17 rows 29 | 34, 61 rows 38 | 37
+//   57344 x 3584:   1 row 37 | 38, 17 rows 40 | 40, 61 rows 44 | 43
+//   57344 x 8192:   1 row 85 | 103, 17 rows 88 | 105, 61 rows 99 | 111
+//   152064 x 3584:  1 row 91 | 146, 17 rows 101 | 148, 61 rows 111 | 158, 128 rows 130 | 173
+//   256000 x 1024:  1 row 44 | 70, 17 rows 60 | 74, 61 rows 66 | 85, 128 rows 80 | 104
 const A8Plan& choose_plan(int64_t N, int64_t b) {
+    const A8Plan *const largest = PLANS + sizeof(PLANS) / sizeof(PLANS[0]) - 1, *best = nullptr;
     const int64_t cus = woq::compute_units();
-    const A8Plan* best = nullptr;
-    int64_t best_tiles = 0;
+    auto tiles = [&](const A8Plan& p) { return woq::ceil_div(b, p.bm) * woq::ceil_div(N, p.bn); };
     for (const A8Plan& p : PLANS) {
-        const int64_t tiles = woq::ceil_div(b, p.bm) * woq::ceil_div(N, p.bn);
+        if (b <= 64 && p.bm > 64) continue;
         if (best && p.bm * p.bn > best->bm * best->bn) break;
-        if (tiles <= cus && (!best || tiles > best_tiles)) best = &p, best_tiles = tiles;
+        if (tiles(p) <= cus && (!best || tiles(p) > tiles(*best))) best = &p;
     }
-    return best ? *best : PLANS[sizeof(PLANS) / sizeof(PLANS[0]) - 1];
+    if (best) return *best;
+    for (const A8Plan& p : PLANS)      // a launch has fewer than 2^32 threads, 512 to a workgroup
+        if (p.rounds && b <= p.bm && tiles(p) < 1 << 23) return p;
+    return *largest;
 }
 
 }  // namespace
