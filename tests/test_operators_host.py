@@ -228,6 +228,44 @@ def test_binding_refuses_what_the_library_cannot_see():
         woq.DeviceLora(A, B, s, segments=[10, 40])
 
 
+def on_gpu(t, index):
+    """The CPU tensor t, said to lie on a GPU: enough for checks that come before any launch."""
+    import torch
+
+    class Placed(torch.Tensor):
+        def get_device(self):
+            return index
+
+    return t.as_subclass(Placed)
+
+
+def test_binding_refuses_weights_and_pools_of_another_device():
+    import torch
+    half = torch.float16
+    x, ids = on_gpu(torch.zeros(2, 64, dtype=half), 0), on_gpu(torch.zeros(2, dtype=torch.int32), 0)
+    y, ws = on_gpu(torch.zeros(2, 40, dtype=half), 0), on_gpu(torch.zeros(1 << 16, dtype=torch.uint8), 0)
+    q, qs = on_gpu(torch.zeros(2, 64, dtype=torch.int8), 0), on_gpu(torch.zeros(2), 0)
+
+    host_weight = woq.DeviceInt8([(np.zeros((40, 64), np.int8), 1.0)], device="cpu")
+    assert host_weight.desc.device == -1
+    with pytest.raises(ValueError, match="woq_qgemm_int8_a8: the weight"):
+        woq.woq_qgemm_int8_a8(host_weight.desc, q, qs, y)
+    w = pool(K=64, lda=64)
+    assert w.device is None                       # a descriptor made by hand says nothing
+    w.device = 1
+    with pytest.raises(ValueError, match="woq_lora_add: the pool"):
+        woq.woq_lora_add(w, x, ids, None, y, ws)
+
+    class Pool:
+        desc = w
+
+    st = woq.Stack.__new__(woq.Stack)
+    st.n, st.handle, st._in, st._out, st._pin, st._pout = 2, None, [x], [y], None, None
+    with pytest.raises(ValueError, match="woq_stack_run_lora: the pool"):
+        st.run_lora(2, [None, Pool()], ids, ws)
+    del st.handle
+
+
 def test_stack_with_adapters_refusals():
     one = (ctypes.c_void_p * 1)(P)
     for args in ((None, one, one, 1, one, P, P, 1 << 20, None),):

@@ -44,6 +44,7 @@ class Int4oGeom(ctypes.Structure):
 class Int8W(ctypes.Structure):
     _fields_ = [("codes", c_void_p), ("N", c_int64), ("K", c_int64), ("nseg", c_int32),
                 ("seg_end", c_int64 * MAX_SEGMENTS), ("seg_scale", c_float * MAX_SEGMENTS)]
+    device = None       # index of the GPU that holds the codes (-1: host memory), where it is known
 
 
 class Int4oW(ctypes.Structure):
@@ -64,6 +65,7 @@ class LoraW(ctypes.Structure):
     _fields_ = [("A", c_void_p), ("B", c_void_p), ("scale", c_void_p), ("rank", c_void_p), ("N", c_int64),
                 ("K", c_int64), ("lda", c_int64), ("R", c_int32), ("count", c_int32), ("nseg", c_int32),
                 ("seg_end", c_int64 * MAX_SEGMENTS)]
+    device = None       # index of the GPU that holds the pool, where it is known
 
 
 FMT_INT8, FMT_INT4O = 1, 2
@@ -507,16 +509,20 @@ def _vector(t, what: str, dtype, n: int):
     return t.data_ptr()
 
 
-def _call(name: str, stream, tensors, *args):
+def _call(name: str, stream, tensors, *args, held=()):
     """Call the C entry point ``name`` on ``stream``, or on the current stream
     of the device that holds the tensors (None entries aside), with that device
-    current."""
+    current.  ``held``: pairs of a name and the device of what the call reads
+    through a descriptor (None: not known)."""
     dev = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{name}: tensors on {tensors[0].device} and {t.device}")
     if dev < 0:
         raise ValueError(f"{name}: the tensors are not on the GPU")
+    for what, at in held:
+        if at is not None and at != dev:
+            raise ValueError(f"{name}: {what} lies on device {at}, the tensors on {tensors[0].device}")
     # torch.cuda.current_stream() builds a Stream object, 2.7 us a call; this
     # reads the same handle
     raw = _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
@@ -565,7 +571,8 @@ def woq_qgemm_int8_a8(w: Int8W, xq, xs, y, stream=None, b: int | None = None):
         b = xq.shape[0]
     xp, ldq = _rows(xq, "xq", _torch.int8, b, -(-w.K // 16) * 16)
     yp, ldy = _rows(y, "y", _torch.float16, b, w.N)
-    _call("woq_qgemm_int8_a8", stream, (xq, xs, y), w, xp, ldq, _vector(xs, "xs", _torch.float32, b), b, yp, ldy)
+    _call("woq_qgemm_int8_a8", stream, (xq, xs, y), w, xp, ldq, _vector(xs, "xs", _torch.float32, b), b, yp, ldy,
+          held=(("the weight", w.device),))
     return y
 
 
@@ -599,7 +606,8 @@ def woq_lora_add(w: LoraW, x, ids, base, y, workspace, stream=None, b: int | Non
     if not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous")
     _call("woq_lora_add", stream, (x, ids, base, y, workspace), w, xp, ldx, _vector(ids, "ids", _torch.int32, b), b,
-          bp, ldb, yp, ldy, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+          bp, ldb, yp, ldy, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+          held=(("the pool", w.device),))
     return y
 
 
@@ -618,6 +626,7 @@ class DeviceInt8:
         self.N, self.K = q.shape
         self.codes = torch.from_numpy(woq_layout_int8(q)).to(device)
         self.desc = Int8W()
+        self.desc.device = self.codes.get_device()
         self.desc.codes = self.codes.data_ptr()
         self.desc.N, self.desc.K, self.desc.nseg = self.N, K, len(parts)
         end = 0
@@ -688,6 +697,7 @@ class DeviceLora:
         if any(t is not None and (t.device != A.device or not t.is_cuda) for t in (A, B, scale, rank)):
             raise ValueError("the pool's tensors have to be on one GPU")
         d = self.desc = LoraW()
+        d.device = A.get_device()
         d.A, d.B = _vector(A, "A", half, 0), _vector(B, "B", half, 0)
         d.scale = _vector(scale, "scale", _torch.float32, count)
         d.rank = None if rank is None else _vector(rank, "rank", _torch.int32, count)
@@ -746,7 +756,8 @@ class Stack:
             raise ValueError("workspace: must be contiguous")
         _call("woq_stack_run_lora", stream, (*self._in, *self._out, ids, workspace), self.handle, self._pin, self._pout,
               b, self._pools(adapters), _vector(ids, "ids", _torch.int32, b), workspace.data_ptr(),
-              workspace.numel() * workspace.element_size())
+              workspace.numel() * workspace.element_size(),
+              held=[(f"the pool of step {i}", p.desc.device) for i, p in enumerate(adapters) if p is not None])
 
     def launches(self, b: int) -> int:
         n = c_int32()
