@@ -466,6 +466,57 @@ def test_adapters_of_a_mixed_batch_captured_and_replayed(gpu_lib):
         np.testing.assert_array_equal(host(y).view(np.uint16), host(eager).view(np.uint16))
 
 
+def by_adapter(base, x, ids, A, B, scale, ends, rank=None):
+    """O.lora_add, all rows of an adapter at once."""
+    y, spread = base.astype(np.float64), np.zeros(base.shape)
+    count, N, R = B.shape
+    for a in range(count):
+        rows = np.flatnonzero(ids == a)
+        k = R if rank is None else min(max(int(rank[a]), 0), R)
+        if k == 0 or rows.size == 0:
+            continue
+        xr, lo = x[rows].astype(np.float64), 0
+        for i, end in enumerate(ends):
+            down = A[a, i * R:i * R + k, :x.shape[1]].astype(np.float64).T
+            up_ = B[a, lo:end, :k].astype(np.float64).T
+            y[rows, lo:end] += float(scale[a]) * (xr @ down @ up_)
+            spread[rows, lo:end] = abs(float(scale[a])) * (np.abs(xr) @ np.abs(down) @ np.abs(up_))
+            lo = end
+    return y, spread
+
+
+@pytest.mark.parametrize("R", [8, 24, 40, 72])
+@pytest.mark.parametrize("b,N,S", [(2100, 4100, 1), (2100, 4103, 3), (4100, 4100, 2), (4099, 4201, 3)])
+def test_adapters_of_wide_outputs_and_many_rows(gpu_lib, b, N, S, R):
+    """Each workgroup goes through two (2100 rows) or four tiles of outputs, with
+    segments that end inside its span: from a base, in place and without one,
+    adapters' rows side by side (windows of one or several) and mixed, rows without one."""
+    import torch
+    rng = np.random.default_rng(b + N + R)
+    K, count = 40, 5
+    rank = rng.integers(0, R + 1, count)
+    A, B, scale, ends = lora_pool(count, N, K, R, S, rng, rank, junk=True)
+    pool = woq.DeviceLora(dev(A), dev(B), dev(scale), dev(rank.astype(np.int32)), K, ends)
+    x, base = rng.standard_normal((b, K)).astype(np.float16), rng.standard_normal((b, N)).astype(np.float16)
+    xd = padded(x, up(K, 8) + 8, np.float16(np.nan))
+    ws = torch.full((woq.woq_lora_workspace(pool.desc, b) // 4 + 4,), float("nan"), device="cuda")
+    mixed = rng.integers(-1, count + 1, b)
+    for ids, odd, form in ((mixed, 0, "place"), (np.sort(mixed), 3, "base"), (np.sort(mixed), 4, "place"),
+                           (np.where(mixed < 0, -1, 1), 1, "none"), (mixed, 1, "base")):
+        case("adapters wide", b, N, K, R, S, odd, form)
+        bd = padded(base, N + odd, np.float16(7))
+        y = bd if form == "place" else full(b, N + odd, 7, "float16")
+        woq.woq_lora_add(pool.desc, xd, dev(ids.astype(np.int32)), None if form == "none" else bd, y, ws)
+        zero = np.zeros_like(base) if form == "none" else base
+        ref, spread = by_adapter(zero, x, ids, A, B, scale, ends, rank)
+        g = host(y)
+        within(g[:, :N], ref, np.abs(ref) * (H + 2 * U) + SUB + spread * ((K / 16 + R + 32) * U + 2.0 ** -20), form)
+        off = (ids < 0) | (ids >= count)
+        np.testing.assert_array_equal(g[off, :N], zero[off])
+        assert np.all(g[:, N:] == 7)
+    assert np.all(np.isnan(host(ws)[-4:]))
+
+
 @pytest.mark.parametrize("R", [8, 32, 64, 72])
 @pytest.mark.parametrize("b", [5, 300])
 def test_adapters_eight_segments_some_empty(gpu_lib, b, R):
