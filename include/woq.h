@@ -497,7 +497,11 @@ typedef struct {
  * The adapters of many requests beside one shared projection: for r < b, n < N
  *   y[r, n] = fp16(base[r, n] + scale[a] * sum_{j < rank[a]} B[a][n, j] h[r, j])
  *   h[r, j] = sum_k A[a][seg(n) * R + j, k] * x[r, k],        a = ids[r],
- * accumulated in fp32; base is the projection's output (null: zeros).  ids
+ * both sums accumulated in fp32; base is the projection's output (null: zeros).
+ * Between them h is not rounded to fp16 but carried as two fp16 halves under a
+ * power of two for the row and segment (or every 16, 32 or 64 ranks of it): each
+ * h[r, j] is off by at most 2^-23 of itself or 2^-38 of the largest of the row
+ * and segment, whichever is more.  ids
  * int32 [b] in device memory names each row's adapter; a row whose id lies
  * outside [0, count) has none: y = base.  Rows of one adapter may stand
  * anywhere, so a decode batch of mixed requests and a packed prompt are the

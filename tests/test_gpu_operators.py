@@ -589,6 +589,42 @@ def test_adapters_inner_products_of_any_size(gpu_lib, scale):
         within(host(y), ref, np.abs(ref) * (H + 2 * U) + SUB + spread * ((K / 16 + R + 32) * U + 2.0 ** -20))
 
 
+@pytest.mark.parametrize("b", [3, 90, 300])
+@pytest.mark.parametrize("R", [8, 16, 24, 64])
+def test_adapters_inner_products_far_apart(gpu_lib, b, R):
+    """One rank of every row is larger than another by up to 2^40, and outputs whose B
+    has a zero for the large one see the small one alone, to 2^-23 of itself or 2^-38
+    of the large one.  The inner products are exact (two terms of 11 bits each, in
+    different places); the base takes away the fp16 result, so that the rest shows in
+    the output: it is off by that, by an fp32 rounding of the sum, and by its own
+    rounding to fp16."""
+    import torch
+    case("adapters far apart", b, R)
+    rng = np.random.default_rng(b + R)
+    K, N = 8, 40
+    A = np.zeros((1, R, K), np.float16)
+    A[0, 0, 0], A[0, R - 1, 1], A[0, R - 1, 2] = 1, 1, 1
+    small = (1 + rng.integers(0, 1024, b) / 1024.0) * 2.0 ** rng.integers(-10, 1, b)
+    x = np.zeros((b, K), np.float16)
+    x[:, 1] = small
+    x[:, 2] = small * 2.0 ** -12 * (1 - rng.integers(1, 1024, b) / 2048.0)      # below half a step of x[:, 1]
+    x[:, 0] = 2.0 ** rng.integers(-8, 16, b)
+    A[0, 0, 0] = 2.0 ** 15
+    B = np.zeros((1, N, R), np.float16)
+    B[0, :, R - 1] = 1
+    B[0, N // 2:, 0] = 2.0 ** -15
+    h0, h1 = x[:, 0].astype(np.float64) * 2.0 ** 15, x[:, 1].astype(np.float64) + x[:, 2].astype(np.float64)
+    base = np.zeros((b, N), np.float16)
+    base[:, :N // 2] = -h1.astype(np.float16)[:, None]
+    pool = woq.DeviceLora(dev(A), dev(B), torch.ones(1, device="cuda"))
+    y = full(b, N, 7, "float16")
+    ws = torch.empty(woq.woq_lora_workspace(pool.desc, b), dtype=torch.uint8, device="cuda")
+    woq.woq_lora_add(pool.desc, dev(x), dev(np.zeros(b, np.int32)), dev(base), y, ws)
+    g, rest = host(y)[:, :N // 2], (h1 + base[:, 0])[:, None]
+    lost = np.maximum(2.0 ** -23 * h1, 2.0 ** -38 * np.maximum(h0, h1))[:, None]
+    within(g, np.broadcast_to(rest, g.shape), lost + 2 * U * h1[:, None] + H * (np.abs(rest) + lost) + SUB)
+
+
 def test_adapters_rows_do_not_touch_each_other(gpu_lib):
     """A NaN or an infinity in one row's input stays in that row; the other rows' bits
     do not depend on it, nor on which rows share the call."""

@@ -10,9 +10,12 @@
 // Both run on the fp16 matrix cores with 16 ranks (or 16 outputs) of ONE
 // adapter against 16 rows: rows that share an adapter share its bytes, and a
 // result column belongs to one row, so rows never mix.  h is not rounded to
-// fp16 on the way: the ranks of a row are scaled by a power of two to below
-// 2^14 and split into two fp16 halves, hi + lo, at least 22 bits; one 16x16x32
-// step multiplies 16 ranks of B with both.
+// fp16 on the way: the ranks of a row are scaled by a power of two, the largest
+// to [2^13, 2^14), and split into two fp16 halves, hi + lo; one 16x16x32 step
+// multiplies 16 ranks of B with both.  What that loses of a rank is at most 2^-23
+// of it (two roundings to 11 bits) or, where lo is subnormal, 2^-25 after
+// scaling: 2^-38 of the row's largest.  (fp32 matrix instructions, which would
+// lose nothing, have a sixteenth of the fp16 rate.)
 //
 // A decode batch is bound by the bytes of the adapters that its rows name, or,
 // at a few rows, by two launches of a few memory round trips each: the kernels
