@@ -7,11 +7,13 @@
 // layout, bytes code + 128; flipping the top bit of a byte gives the code in
 // two's complement (one v_xor_b32 per four codes).
 //
-// Few rows are bound by the weights' bytes (one row of 8192 x 3584 7.1 us, 4.1
-// TB/s, of which 1.55 are the launch; 61 rows of 28672 x 3584 24 us, 4.4 TB/s),
-// many by the matrix cores (4095 rows of 28672 x 3584 411-424 us, 2.0 POP/s); between
-// them tiles small enough to fill the device are bound by what LDS moves
-// (509 rows of 3584 x 14336 47.6 us, 1.1 POP/s).  Both operands pass through LDS: a
+// Few rows are bound by the weights' bytes (one row of 8192 x 3584 8.4 us from
+// HBM, 3.5 TB/s, 7.1-7.3 where three such weights in turn stay in the last-level
+// cache, 1.55 of either the launch; 61 rows of 28672 x 3584 23-24 us, 4.4-4.6
+// TB/s, 224 of the 256 compute units at work), many by the matrix cores (4095
+// rows of 28672 x 3584 411-430 us, 1.96-2.05 POP/s, level with the library's
+// product of that shape); between them tiles small enough to fill the device are
+// bound by what LDS moves (509 rows of 3584 x 14336 48 us, 1.1 POP/s).  Both operands pass through LDS: a
 // lane per row, the matrix instruction's order, would cost the address unit a
 // lookup per lane and, of the weights, a load per row of tiles.
 #include <hip/hip_runtime.h>

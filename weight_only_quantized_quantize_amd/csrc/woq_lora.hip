@@ -18,14 +18,18 @@
 // lose nothing, have a sixteenth of the fp16 rate.)
 //
 // A decode batch is bound by the bytes of the adapters that its rows name, or,
-// at a few rows, by two launches of a few memory round trips each: the kernels
-// keep every load of a round in flight together and have no barrier before the
-// sums meet.  One row beside 8192 x 8192, rank 16: 4.2 + 4.8 us; 64 rows beside
+// at a few rows, by two launches of a few memory round trips each.  The inner
+// kernel has the ids, then every load of a wave together, and no barrier before
+// the sums meet; the outer one has three dependent rounds, the ids with base and
+// h, the first operands of B, the rest of them; ranks per adapter add a wait to
+// each of its loads (64 rows of rank 16: 22.1 us, with a rank array 26.8).  One row beside 8192 x 8192, rank 16: 4.2 + 4.8 us; 64 rows beside
 // 10240 x 8192 in three segments, an adapter of rank 16 each: 10.4 + 9.8 us,
 // 75 MB at 3.7 TB/s.  (Both products in one launch, each workgroup computing h
 // for its 1024 outputs: 11.2 and 36 us.)  A prompt is bound by the base and the
 // output: 3001 rows beside 28672 x 3584 in two segments, 8 adapters of rank 64:
-// 5 + 20 + 90 us, 402 MB at 3.5 TB/s.
+// 5 + 20 + 90 us, 402 MB at 3.5 TB/s; every tile of the outer kernel waits for the
+// stores of the one before and for its own base.  Ranks above 64 go through h and B
+// in groups and spill 12 registers: rank 72 takes 237 us there, 128 244.
 #include <hip/hip_runtime.h>
 
 #include "woq_gemv.h"
