@@ -519,6 +519,129 @@ int woq_lora_add(const woq_lora_w* w, const uint16_t* x, int64_t ldx, const int3
                  int64_t workspace_bytes, void* stream);
 int64_t woq_lora_workspace(const woq_lora_w* w, int64_t b);
 
+/* ------------------------------- device ops: between the products of a step */
+
+/*
+ * A paged cache of keys and values in device memory, owned by the caller.  k and
+ * v hold [n_pages][heads][page][dim] values, 16-byte aligned: fp16
+ * (WOQ_CACHE_FP16), or for WOQ_CACHE_INT8 one byte each, code + 128 as in the
+ * INT8 device layout, with an fp32 scale for every token and head in k_scale and
+ * v_scale [n_pages][heads][page] (16-byte aligned; null for fp16): the INT8 scheme
+ * of woq_quantize_int8 over the dim values of a head.  A slot names a token's place:
+ * slot = page index * page + offset in the page.  dim is a multiple of 16, at
+ * most WOQ_CACHE_MAX_DIM; page, the tokens of a page, a multiple of 16, at most
+ * WOQ_CACHE_MAX_PAGE; heads <= WOQ_CACHE_MAX_HEADS; n_pages * page < 2^31.
+ */
+#define WOQ_CACHE_FP16 1
+#define WOQ_CACHE_INT8 2
+#define WOQ_CACHE_MAX_DIM 256
+#define WOQ_CACHE_MAX_PAGE 65536
+#define WOQ_CACHE_MAX_HEADS 1024
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t n_pages;
+    int32_t fmt, heads, page, dim;
+} woq_cache;
+
+/*
+ * Write the keys and values of b new tokens into a cache and turn queries and
+ * keys by their positions on the way.  Row r of k and v (fp16 [b, ld], heads *
+ * dim values) goes to slots[r] (int32 in device memory); a row whose slot lies
+ * outside [0, n_pages * page) is not written.  Slots of one call must differ
+ * from each other.  Where rope is not null, the first rot values of every head
+ * of k, and of q (fp16 [b, ldq], q_heads * dim values; null: none), are turned
+ * in fp32 before anything is rounded: pair i (0 <= i < rot / 2) becomes
+ *   (a cos - b sin, b cos + a sin)
+ * with cos = rope[pos[r] * rot + i], sin = rope[pos[r] * rot + rot / 2 + i]
+ * (fp32 [n_pos][rot] in device memory), a and b the values i and i + rot / 2 of
+ * the head, or 2 i and 2 i + 1 where interleaved is 1.  The turned q goes to
+ * q_out as fp16, which may be q with the same leading dimension.  q, k and v of
+ * a row whose position lies outside [0, n_pos) become NaN where the rotation
+ * would read the table.  INT8: scale = fp32(max |v| / 127) over the head's
+ * values, code = clamp(rne(fp32(v / scale)), +-127), bit for bit
+ * woq_quantize_int8 of the (turned) values; a head of zeros has scale 0 and
+ * codes 0, one with a NaN or an infinity scale NaN and codes 0.  q without rope
+ * is WOQ_EINVAL; rot is a multiple of 16, 16 <= rot <= dim.  fp16 rows are
+ * 16-byte aligned with leading dimensions that are multiples of 8; rope is
+ * 16-byte aligned.  Tokens of the cache that no slot names keep their values.
+ * b * (q_heads + 2 heads) < 2^31; b = 0 is a no-op.
+ */
+int woq_cache_write(const woq_cache* c, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                    const int32_t* slots, int64_t b, const uint16_t* q, int64_t ldq, int32_t q_heads, uint16_t* q_out,
+                    int64_t ldq_out, const float* rope, int64_t n_pos, int32_t rot, int32_t interleaved,
+                    const int32_t* pos, void* stream);
+
+/*
+ * Read tokens back from a cache as fp16 rows: for r < n, row r of k_out (fp16
+ * [n, ldk], heads * dim values) holds the keys at slots[r], row r of v_out the
+ * values (either may be null): the stored fp16, or fp16(fp32(code * scale)) as
+ * woq_embed_int8 restores a row.  A slot outside [0, n_pages * page) gives
+ * zeros; slots may repeat.  Rows are 16-byte aligned, leading dimensions
+ * multiples of 8.  2 n heads < 2^31; n = 0 is a no-op.
+ */
+int woq_cache_read(const woq_cache* c, const int32_t* slots, int64_t n, uint16_t* k_out, int64_t ldk,
+                   uint16_t* v_out, int64_t ldv, void* stream);
+
+/*
+ * Attention of one new token per row over a paged cache.  For r < b and every
+ * query head h (which meets the cache's head h / (q_heads / heads)):
+ *   y[r, h] = sum_t softmax_t(z)[t] v[t],   z[t] = scale * (q[r, h] . k[t]),
+ * or z[t] = softcap * tanh(scale * (q . k) / softcap) where softcap > 0.  Row r
+ * sees the tokens max(0, len - window) <= t < len (window 0: all t < len), len =
+ * lens[r] (int32 in device memory) clamped to [0, max_pages * page]; token t
+ * stands at offset t % page of page pages[r * ldpages + t / page] (int32 in
+ * device memory, max_pages entries used of a row).  A page index outside [0,
+ * n_pages) is a page that is not there: its tokens are not seen.  Entries of
+ * pages without a visible token are not read, and what stands at tokens that are
+ * not seen does not matter (NaN or infinity).  A row that sees nothing gives zeros.
+ * Several new tokens of one sequence are rows with the same pages and rising
+ * lens.  q fp16 [b, ldq] and y fp16 [b, ldy] with q_heads * dim values, 16-byte
+ * aligned, leading dimensions multiples of 8; q_heads is a multiple of heads.
+ * Scores, softmax and sums are fp32; the weights of the values (the softmax's
+ * numerators, times the token's scale where there is one) are rounded to fp16
+ * under a power of two of their own for the matrix cores.  y may be q with the
+ * same leading dimension.  workspace: at least woq_attn_decode_workspace bytes of device memory,
+ * 16-byte aligned, owned by the caller, its contents on return unspecified;
+ * calls that share it must not overlap.  Deterministic for given inputs on one
+ * device model.  q_heads <= WOQ_ATTN_MAX_HEADS, b <= WOQ_ATTN_MAX_ROWS,
+ * max_pages * page < 2^31; b = 0 is a no-op.
+ */
+#define WOQ_ATTN_MAX_HEADS 4096
+#define WOQ_ATTN_MAX_ROWS 65536
+int woq_attn_decode(const woq_cache* c, const uint16_t* q, int64_t ldq, int32_t q_heads, const int32_t* pages,
+                    int64_t ldpages, int64_t max_pages, const int32_t* lens, int64_t b, float scale, float softcap,
+                    int32_t window, uint16_t* y, int64_t ldy, void* workspace, int64_t workspace_bytes, void* stream);
+/* Bytes for batches of up to b rows, or a negative status for bad sizes. */
+int64_t woq_attn_decode_workspace(const woq_cache* c, int32_t q_heads, int64_t b);
+
+/*
+ * The next token of every row from its logits (fp16 [b, ld], N of them; 16-byte
+ * aligned, ld a multiple of 8) and a given random number.  Row r, with w[i] =
+ * exp((logit[i] - max) / temperature[r]), goes through its tokens from the
+ * largest logit down, equal ones by rising index, and keeps
+ *   the first top_k[r] (all where top_k[r] <= 0), of those
+ *   the ones with w >= min_p[r] (all where min_p[r] is not > 0; above 1 counts
+ *   as 1), of those
+ *   the shortest beginning whose sum of w reaches top_p[r] times the sum of all
+ *   that are left, one at least (all where top_p[r] is not < 1);
+ * token[r] is the first kept one at which the running sum of w exceeds u[r]
+ * times the kept sum, prob[r] its share of the kept sum.  u is taken into [0, 1 -
+ * 2^-24] (a NaN as 0).  A row whose temperature is not > 0 takes its largest logit.  Logits that
+ * are NaN or -infinity are never taken; several +infinity share the draw.  A row
+ * without any other gives token -1 and prob 0.  temperature, top_p, min_p and u
+ * are fp32 [b], top_k int32 [b], in device memory; temperature null: 1, top_k,
+ * top_p, min_p null: off.  token int32 [b], prob fp32 [b] (may be null).  Weights
+ * and their sums are 64-bit; what a row's draw gives depends on that row alone.
+ * N <= WOQ_SAMPLE_MAX_N, b < 2^31; b = 0 is a no-op.
+ */
+#define WOQ_SAMPLE_MAX_N (1 << 24)
+int woq_sample(const uint16_t* logits, int64_t ld, int64_t N, int64_t b, const float* temperature,
+               const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* token,
+               float* prob, void* stream);
+
 /* --------------------------------------------------------- layer stack */
 
 #define WOQ_FMT_INT8  1

@@ -1,0 +1,627 @@
+"""GPU tests of the operators between a decode step's products and behind its
+head (woq_cache_write, woq_cache_read, woq_attn_decode, woq_sample) against their
+float64 definitions.
+
+Tolerances count roundings: U = 2^-24 is half a step of fp32, H = 2^-11 of fp16,
+SUB = 2^-25 half the spacing of fp16's subnormals.
+
+* rotation: two products and a sum, at most 3 U of |a c| + |b s|.
+* codes of turned keys: |v / scale - code| <= 1/2 plus that error over the scale,
+  and 127 * 2 U of the scale's own; values nothing turns are bit for bit the
+  encoder's.
+* attention: a score is a sum of dim exact products in fp32, then at most 8
+  roundings (its factors, the exponential's argument): (dim + 8) U of its terms'
+  magnitudes (reach), and as much again for the row's largest score; a weight's
+  rounding to fp16 is H of it, exponential, logarithm and reciprocal 2^-20, its
+  argument 2^-22 for the token's scale; the sums of n tokens are at most n / 16 + 96
+  roundings long, twice (values and weights): all of them relative to spread =
+  sum p |v|.  Weights below 2^-40 of the largest may be lost: n 2^-40 max |v|.
+  The result is rounded to fp16.
+* a token is the definition's, exactly; its share is rounded to fp32 once.
+"""
+import numpy as np
+import pytest
+
+import oracle as O
+from weight_only_quantized_quantize_amd import woq
+
+pytestmark = pytest.mark.gpu
+
+H, SUB, U = 2.0 ** -11, 2.0 ** -25, 2.0 ** -24
+
+
+def case(*a):
+    print("case:", *a, flush=True)
+
+
+def dev(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def host(t):
+    import torch
+    torch.cuda.synchronize()
+    return t.cpu().numpy()
+
+
+def within(y, ref, tol, what=""):
+    y = y.astype(np.float64)
+    err = np.abs(y - ref)
+    bad = ~(err <= tol)
+    assert not bad.any(), (what, np.argwhere(bad)[:4], y[bad][:4], ref[bad][:4], np.broadcast_to(tol, err.shape)[bad][:4])
+
+
+class Cache:
+    """A cache on the device and on the host: random contents, or a poison that no
+    call may read as a value (NaN scales, NaN values)."""
+
+    def __init__(self, n_pages, heads, page, dim, int8=True, seed=0, poison=False):
+        import torch
+        rng = np.random.default_rng(seed)
+        shape = (n_pages, heads, page, dim)
+        self.shape, self.int8, self.heads, self.page, self.dim = shape, int8, heads, page, dim
+        self.k, self.v = (rng.standard_normal(shape).astype(np.float16) for _ in range(2))
+        self.k[..., ::7] *= 4
+        self.ks = self.vs = None
+        if int8:
+            self.ks, self.vs = (np.abs(t).max(-1).astype(np.float32) / np.float32(127) for t in (self.k, self.v))
+            self.k, self.v = (np.clip(np.rint(t.astype(np.float32) / s[..., None]), -127, 127).astype(np.int64)
+                              for t, s in ((self.k, self.ks), (self.v, self.vs)))
+            self.k, self.v = (self.k + 128).astype(np.uint8), (self.v + 128).astype(np.uint8)
+        if poison:
+            for t in (self.k, self.v):
+                t[...] = 255 if int8 else np.nan
+            if int8:
+                self.ks[...] = self.vs[...] = np.nan
+        self.upload()
+
+    def upload(self):
+        self.d = woq.DeviceCache(dev(self.k), dev(self.v), *((dev(self.ks), dev(self.vs)) if self.int8 else ()))
+        self.desc = self.d.desc
+
+    def values(self, which):
+        """float64 [n_pages, heads, page, dim] of the host's copy."""
+        t, s = (self.k, self.ks) if which == "k" else (self.v, self.vs)
+        return (t.astype(np.float64) - 128) * s[..., None].astype(np.float64) if self.int8 else t.astype(np.float64)
+
+    def tokens(self, which, slots):
+        v, slots = self.values(which), np.asarray(slots)
+        return v[slots // self.page, :, slots % self.page]
+
+    def now(self):
+        """What the device holds: (k, v, k scales, v scales)."""
+        return tuple(None if t is None else host(t) for t in (self.d.k, self.d.v, self.d.k_scale, self.d.v_scale))
+
+
+# ------------------------------------------------------------ write and read
+
+def rope_table(n_pos, rot):
+    a = np.arange(n_pos)[:, None] * 10000.0 ** (-np.arange(0, rot, 2) / rot)
+    return np.concatenate([np.cos(a), np.sin(a)], 1).astype(np.float32)
+
+
+def check_write(c, b, q_heads, rot, interleaved, slots, pos, seed=0, n_pos=50, pad=0, special=False):
+    """One call with q, k and v side by side in rows that are wider by ``pad``;
+    everything that no slot names has to stay."""
+    import torch
+    rng = np.random.default_rng(seed)
+    D, Hk = c.dim, c.heads
+    n, m = q_heads * D, Hk * D
+    x = rng.standard_normal((b, n + 2 * m + pad)).astype(np.float16) * np.float16(3)
+    if special:
+        x[0, n:n + D] = 0
+        x[1, n + m:n + m + D] = np.nan
+        x[2, n + D - 1] = np.inf
+    before = c.now()
+    xd = dev(x)
+    rope = rope_table(n_pos, rot) if rot else None
+    out = torch.full((b, n + 8), 7.0, dtype=torch.float16, device="cuda")
+    kw = dict(rope=dev(rope), pos=dev(np.asarray(pos, np.int32)), interleaved=interleaved) if rot else {}
+    if q_heads:
+        kw.update(q=xd[:, :n], q_out=out[:, :n])
+    slots = np.asarray(slots, np.int32)
+    woq.woq_cache_write(c.desc, xd[:, n:n + m], xd[:, n + m:n + 2 * m], dev(slots), **kw)
+    after = c.now()
+    parts = {"q": x[:, :n].reshape(b, q_heads, D), "k": x[:, n:n + m].reshape(b, Hk, D),
+             "v": x[:, n + m:n + 2 * m].reshape(b, Hk, D)}
+    ref, mag = {}, {}
+    with np.errstate(invalid="ignore"):
+        for name, t in parts.items():
+            if rot and name != "v":
+                at = np.clip(pos, 0, n_pos - 1)
+                ref[name] = O.rotate(t, rope, at, interleaved)
+                mag[name] = np.abs(ref[name])
+                # |a c| + |b s| is at most |a| + |b|
+                a = np.abs(t.astype(np.float64))
+                pair = np.arange(D)
+                i = pair[:rot]
+                pair[:rot] = (i ^ 1) if interleaved else (i + rot // 2) % rot
+                mag[name][..., :rot] = (a + a[..., pair])[..., :rot]
+                lost = [r for r in range(b) if not 0 <= pos[r] < n_pos]
+                for r in lost:
+                    ref[name][r, :, :rot] = np.nan
+            else:
+                ref[name], mag[name] = t.astype(np.float64), np.zeros(t.shape)
+    if q_heads:
+        got = host(out)
+        assert np.all(got[:, n:] == 7)
+        y, want = got[:, :n].reshape(b, q_heads, D), ref["q"]
+        np.testing.assert_array_equal(np.isnan(y), np.isnan(want))
+        ok = ~np.isnan(want)
+        within(y[ok], want[ok], np.abs(want[ok]) * H + 4 * U * mag["q"][ok] + SUB, "q")
+    named = np.zeros(before[0].shape[:3], bool)
+    for r, s in enumerate(slots):
+        if not 0 <= s < c.shape[0] * c.page:
+            continue
+        p, o = divmod(int(s), c.page)
+        named[p, :, o] = True
+        for i, name in enumerate(("k", "v")):
+            turned = rot and name == "k"
+            for h in range(Hk):
+                want, stored = ref[name][r, h], after[i][p, h, o]
+                if not c.int8:
+                    np.testing.assert_array_equal(np.isnan(stored), np.isnan(want))
+                    if not turned:
+                        np.testing.assert_array_equal(stored.view(np.uint16), parts[name][r, h].view(np.uint16))
+                    elif np.all(np.isfinite(want)):
+                        within(stored, want, np.abs(want) * H + 4 * U * mag[name][r, h] + SUB, name)
+                    continue
+                scale = after[2 + i][p, h, o]
+                if not np.all(np.isfinite(want)):
+                    assert np.isnan(scale) and np.all(stored == 128), (r, name, h)
+                elif not turned:
+                    codes, s1 = O.quantize_int8(parts[name][r, h][None].astype(np.float32))
+                    assert np.float32(s1) == scale
+                    np.testing.assert_array_equal(stored.astype(int) - 128, codes[0])
+                elif not want.any():
+                    assert scale == 0 and np.all(stored == 128)
+                else:
+                    true = np.abs(want).max() / 127
+                    slack = 4 * U * mag[name][r, h].max()
+                    assert abs(scale - true) <= slack / 127 + true * 2 * U
+                    within(stored.astype(int) - 128, want / true, 0.5 + 2 * slack / true + 127 * 4 * U, name)
+                    assert np.all(np.abs(stored.astype(int) - 128) <= 127)
+    for i in range(4):
+        if before[i] is not None:
+            keep = ~named
+            np.testing.assert_array_equal(after[i][keep].view(np.uint8), before[i][keep].view(np.uint8))
+
+
+@pytest.mark.parametrize("int8", [True, False])
+@pytest.mark.parametrize("heads,dim,page,b,q_heads,rot,inter", [
+    (1, 16, 16, 1, 1, 16, False), (8, 128, 16, 1, 64, 128, False), (8, 256, 64, 3, 16, 256, True),
+    (5, 96, 48, 33, 20, 32, False), (3, 80, 32, 7, 3, 80, True), (12, 64, 128, 5, 12, 64, False),
+    (2, 48, 16, 100, 0, 0, False), (1, 240, 16, 9, 2, 224, False), (4, 112, 96, 20, 4, 16, True),
+    (7, 32, 16, 64, 0, 32, True)])
+def test_write_sizes(gpu_lib, int8, heads, dim, page, b, q_heads, rot, inter):
+    case("write", int8, heads, dim, page, b, q_heads, rot, inter)
+    rng = np.random.default_rng(b)
+    c = Cache(-(-b // page) + 2, heads, page, dim, int8, seed=1)
+    slots = rng.permutation(c.shape[0] * page)[:b]
+    if b > 4:
+        slots[[1, 3]] = -1, c.shape[0] * page
+    check_write(c, b, q_heads, rot, inter, slots, rng.integers(0, 50, b), pad=8 * (b % 3))
+
+
+@pytest.mark.parametrize("int8", [True, False])
+@pytest.mark.parametrize("rot", [0, 64])
+def test_write_rows_of_zeros_nan_and_infinity(gpu_lib, int8, rot):
+    c = Cache(3, 2, 16, 64, int8)
+    check_write(c, 6, 4 if rot else 0, rot, False, [5, 40, 17, 0, 47, 31], [0, 1, 49, 3, 50, -1], special=True)
+
+
+def test_write_keeps_distant_places_and_ties(gpu_lib):
+    """A head whose scale is a power of two: halves go to the even code; the first
+    and the last slot; -1, -2^31 and 2^31 - 1 are no slots."""
+    import torch
+    c = Cache(4, 1, 16, 64, True)
+    x = np.zeros((2, 64), np.float16)
+    x[0] = np.arange(64) / 2 - 16
+    x[0, 63] = 127
+    x[1] = -x[0]
+    rows = dev(np.concatenate([x, x[:1], x[:1], x[:1]]))
+    slots = np.array([0, 63, -1, -2 ** 31, 2 ** 31 - 1], np.int32)
+    woq.woq_cache_write(c.desc, rows, rows, dev(slots))
+    k, v, ks, vs = c.now()
+    assert ks[0, 0, 0] == 1 and ks[3, 0, 15] == 1
+    np.testing.assert_array_equal(k[0, 0, 0].astype(int) - 128, np.rint(x[0].astype(float)))
+    np.testing.assert_array_equal(v[3, 0, 15].astype(int) - 128, np.rint(x[1].astype(float)))
+    out = torch.empty(5, 64, dtype=torch.float16, device="cuda")
+    woq.woq_cache_read(c.desc, dev(slots), out)
+    got = host(out)
+    np.testing.assert_array_equal(got[:2], np.rint(x.astype(float)))
+    assert not got[2:].any()
+
+
+def test_write_turns_q_in_place_and_leaves_rows_behind(gpu_lib):
+    import torch
+    rng = np.random.default_rng(3)
+    c = Cache(2, 2, 16, 64, True)
+    x = rng.standard_normal((9, 4 * 64 + 256)).astype(np.float16)
+    xd, rope, pos = dev(x), rope_table(30, 32), rng.integers(0, 30, 9).astype(np.int32)
+    woq.woq_cache_write(c.desc, xd[:, 256:384], xd[:, 384:], dev(np.arange(9, dtype=np.int32)), q=xd[:, :256],
+                        q_out=xd[:, :256], rope=dev(rope), pos=dev(pos), b=7)
+    got = host(xd)
+    np.testing.assert_array_equal(got[7:], x[7:])
+    np.testing.assert_array_equal(got[:, 256:], x[:, 256:])
+    ref = O.rotate(x[:7, :256].reshape(7, 4, 64), rope, pos).reshape(7, 256)
+    within(got[:7, :256], ref, np.abs(ref) * H + 4 * U * 12 + SUB)
+
+
+@pytest.mark.parametrize("int8", [True, False])
+@pytest.mark.parametrize("heads,dim,page,n", [(1, 16, 16, 1), (8, 128, 16, 133), (3, 80, 48, 77), (8, 256, 64, 40),
+                                              (5, 64, 32, 1000), (1, 112, 16, 5)])
+def test_read_back(gpu_lib, int8, heads, dim, page, n):
+    """Slots in any order, some twice, some that are none; one of the two alone."""
+    import torch
+    case("read", int8, heads, dim, page, n)
+    rng = np.random.default_rng(n)
+    c = Cache(9, heads, page, dim, int8, seed=2)
+    slots = rng.integers(0, 9 * page, n)
+    if n > 4:
+        slots[[0, 3]] = -5, 9 * page
+    width = heads * dim
+    k, v = (torch.full((n + 1, width + 16), 7.0, dtype=torch.float16, device="cuda") for _ in range(2))
+    idx = dev(slots.astype(np.int32))
+    for ko, vo in ((k[:, :width], v[:, :width]), (k[:, :width], None), (None, v[:, :width])):
+        for t in (k, v):
+            t.fill_(7.0)
+        woq.woq_cache_read(c.desc, idx, ko, vo, n=n)
+        for t, asked, which in ((k, ko, "k"), (v, vo, "v")):
+            got = host(t)
+            assert np.all(got[n] == 7) and np.all(got[:, width:] == 7)
+            if asked is None:
+                assert np.all(got == 7)
+                continue
+            on = (slots >= 0) & (slots < 9 * page)
+            ref = c.tokens(which, np.where(on, slots, 0)).reshape(n, width)
+            if int8:           # the product in fp32, then fp16, both to nearest even
+                p, o = np.where(on, slots, 0) // page, np.where(on, slots, 0) % page
+                codes, scale = ((c.k, c.ks) if which == "k" else (c.v, c.vs))
+                ref = ((codes[p, :, o].astype(np.float32) - 128) * scale[p, :, o][..., None]).reshape(n, width)
+            ref = np.where(on[:, None], ref, 0).astype(np.float16)
+            np.testing.assert_array_equal(got[:n, :width], ref)
+
+
+# --------------------------------------------------------------- attention
+
+def tables(rng, c, lens, width=None, spare=0):
+    """Pages of a shuffled pool for every row, -1 behind the last."""
+    need = [-(-max(int(n), 0) // c.page) for n in lens]
+    W = max(max(need), 1) if width is None else width
+    order = rng.permutation(c.shape[0])
+    t = np.full((len(lens), W + spare), -1, np.int32)
+    first = 0
+    for r, n in enumerate(need):
+        n = min(n, W)
+        t[r, :n] = order[first:first + n]
+        first += n
+    assert first <= c.shape[0]
+    return t
+
+
+def check_attention(c, q_heads, lens, seed=0, window=0, softcap=0.0, scale=None, pages=None, spread=1.0, got=None,
+                    q=None, width=None):
+    import torch
+    rng = np.random.default_rng(seed)
+    b, D = len(lens), c.dim
+    n = q_heads * D
+    if q is None:
+        q = (rng.standard_normal((b, n)) * spread).astype(np.float16)
+    if pages is None:
+        pages = tables(rng, c, lens, width)
+    scale = D ** -0.5 if scale is None else scale
+    y = torch.full((b + 1, n + 8), 7.0, dtype=torch.float16, device="cuda")
+    size = woq.woq_attn_decode_workspace(c.desc, q_heads, b)
+    ws = torch.full((size // 4 + 64,), float("nan"), device="cuda")
+    if got is None:
+        wide = np.full((b, n + 24), np.nan, np.float16)
+        wide[:, :n] = q
+        woq.woq_attn_decode(c.desc, dev(wide)[:, :n], dev(pages), dev(np.asarray(lens, np.int32)), y[:, :n], ws[:size // 4],
+                            scale=scale, softcap=softcap, window=window, b=b)
+        got = host(y)
+        assert np.all(got[b] == 7) and np.all(got[:, n:] == 7)
+        assert np.all(np.isnan(host(ws)[size // 4:]))
+        got = got[:b, :n]
+    for r in range(b):
+        end = min(max(int(lens[r]), 0), pages.shape[1] * c.page)
+        t = np.arange(max(0, end - window) if window else 0, end)
+        at = pages[r, t // c.page].astype(np.int64)
+        on = (at >= 0) & (at < c.shape[0])
+        slots = at[on] * c.page + t[on] % c.page
+        K, V = c.tokens("k", slots), c.tokens("v", slots)
+        ref, mag, reach = O.attend(q[r].reshape(q_heads, D), K, V, scale, softcap)
+        m = len(slots)
+        dz = reach * (D + 8) * U
+        rel = H + 3 * dz + 2.0 ** -19 + 2 * (m / 16 + 96) * U + softcap * 2.0 ** -21
+        tol = mag * rel + np.abs(ref) * H + SUB + (m * 2.0 ** -40 * np.abs(V).max() if m else 0)
+        within(got[r].reshape(q_heads, D), ref, tol, ("row", r, "of", b, "len", int(lens[r])))
+    return got
+
+
+@pytest.mark.parametrize("int8", [True, False])
+@pytest.mark.parametrize("heads,q_heads,dim,page", [
+    (8, 64, 128, 16), (8, 16, 256, 64), (8, 32, 128, 48), (12, 12, 64, 16), (5, 20, 96, 32), (1, 16, 128, 128),
+    (1, 40, 64, 16), (2, 6, 80, 16), (1, 1, 16, 16), (1, 17, 256, 16), (3, 3, 240, 32), (2, 66, 48, 16), (4, 28, 128, 256)])
+def test_attention_head_layouts(gpu_lib, int8, heads, q_heads, dim, page):
+    case("attention", int8, heads, q_heads, dim, page)
+    lens = [300, 1, 0, 15, 16, 17, 31, 32, 33, 127, 128, 129, 255]
+    c = Cache(sum(-(-n // page) for n in lens) + 2, heads, page, dim, int8, seed=heads)
+    check_attention(c, q_heads, lens, seed=dim)
+
+
+@pytest.mark.parametrize("int8", [True, False])
+@pytest.mark.parametrize("b", [1, 2, 3, 7, 64, 257])
+def test_attention_batches(gpu_lib, int8, b):
+    rng = np.random.default_rng(b)
+    lens = rng.integers(0, 200, b)
+    lens[0] = 199
+    case("attention batch", int8, b)
+    c = Cache(int(sum(-(-lens // 16))) + 1, 2, 16, 64, int8, seed=b)
+    check_attention(c, 8, lens, seed=b)
+
+
+@pytest.mark.parametrize("int8,heads,q_heads,dim,page,lens", [
+    (True, 8, 64, 128, 64, [5000]), (False, 2, 4, 256, 48, [6001, 3]), (True, 1, 8, 128, 16, [30001]),
+    (True, 2, 16, 64, 256, [9000, 0, 1, 12000, 77]), (False, 1, 3, 80, 32, [20011])])
+def test_attention_long(gpu_lib, int8, heads, q_heads, dim, page, lens):
+    case("attention long", int8, heads, q_heads, dim, page, lens)
+    c = Cache(sum(-(-n // page) for n in lens) + 1, heads, page, dim, int8, seed=7)
+    check_attention(c, q_heads, lens, seed=3)
+
+
+@pytest.mark.parametrize("int8", [True, False])
+@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 100, 128, 333, 100000])
+def test_attention_window(gpu_lib, int8, window):
+    """What lies outside the window is poison, and its pages are not there."""
+    case("attention window", int8, window)
+    lens = [0, 1, 2, 16, 17, 100, 128, 129, 500, 333, 431]
+    page = 16
+    rng = np.random.default_rng(window)
+    c = Cache(sum(-(-n // page) for n in lens) + 1, 2, page, 64, int8, seed=5, poison=True)
+    good = Cache(c.shape[0], 2, page, 64, int8, seed=5)
+    pages = tables(rng, c, lens)
+    for r, n in enumerate(lens):
+        for t in range(max(0, n - window), n):
+            p, o = pages[r, t // page], t % page
+            for a in ("k", "v", "ks", "vs"):
+                if getattr(c, a) is not None:
+                    getattr(c, a)[p, :, o] = getattr(good, a)[p, :, o]
+        pages[r, :max(0, n - window) // page] = 2 ** 31 - 1
+    c.upload()
+    check_attention(c, 4, lens, seed=window, window=window, pages=pages)
+
+
+@pytest.mark.parametrize("int8", [True, False])
+def test_attention_does_not_see_past_the_end(gpu_lib, int8):
+    """Poison behind the last token of every row, in its page and in others."""
+    lens = [1, 5, 16, 20, 31, 33, 64, 100, 250]
+    rng = np.random.default_rng(1)
+    for page in (16, 64):
+        c = Cache(sum(-(-n // page) for n in lens) + 1, 2, page, 128, int8, seed=6, poison=True)
+        good = Cache(c.shape[0], 2, page, 128, int8, seed=6)
+        pages = tables(rng, c, lens, width=-(-250 // page) + 3)
+        for r, n in enumerate(lens):
+            for t in range(n):
+                for a in ("k", "v", "ks", "vs"):
+                    if getattr(c, a) is not None:
+                        getattr(c, a)[pages[r, t // page], :, t % page] = getattr(good, a)[pages[r, t // page], :, t % page]
+            pages[r, -(-n // page):] = pages[0, 0]       # entries behind the last page name some other
+        c.upload()
+        check_attention(c, 16, lens, pages=pages)
+
+
+@pytest.mark.parametrize("int8", [True, False])
+def test_attention_pages_that_are_not_there(gpu_lib, int8):
+    lens = [200, 200, 40, 16, 90]
+    c = Cache(50, 2, 16, 64, int8, seed=8)
+    rng = np.random.default_rng(2)
+    pages = tables(rng, c, lens)
+    pages[0, [0, 3, 4, 12]] = -1, 50, -2 ** 31, 2 ** 31 - 1
+    pages[2] = -7                                        # nothing left: zeros
+    pages[3, 0] = 50
+    pages[4, 1:5] = -1
+    got = check_attention(c, 6, lens, pages=pages)
+    assert not got[2].any() and not got[3].any()
+
+
+def test_attention_lengths_outside_the_table(gpu_lib):
+    """Lengths below zero are zero, above the table's pages all of them."""
+    c = Cache(12, 1, 16, 64, True, seed=9)
+    pages = np.arange(12, dtype=np.int32).reshape(4, 3)
+    got = check_attention(c, 2, [-1, -2 ** 31, 49, 2 ** 31 - 1], pages=pages)
+    assert not got[:2].any() and got[2].any()
+
+
+@pytest.mark.parametrize("int8", [True, False])
+@pytest.mark.parametrize("softcap,scale,spread", [(50.0, None, 1.0), (5.0, 0.5, 3.0), (0.0, 1.0, 4.0), (0.0, -0.3, 1.0),
+                                                  (0.0, 0.0, 1.0), (30.0, 0.0625, 20.0), (0.0, 2.0, 8.0)])
+def test_attention_scores(gpu_lib, int8, softcap, scale, spread):
+    """Flat, sharp and bounded scores; a negative scale."""
+    case("attention scores", int8, softcap, scale, spread)
+    lens = [700, 33, 2, 150]
+    c = Cache(80, 2, 16, 128, int8, seed=10)
+    check_attention(c, 6, lens, softcap=softcap, scale=scale, spread=spread, seed=4)
+
+
+def test_attention_scales_far_apart(gpu_lib):
+    """Values whose scales differ by many powers of two, heads of zeros, and the
+    largest values where the weights are smallest."""
+    c = Cache(24, 2, 16, 64, True, seed=11)
+    rng = np.random.default_rng(5)
+    c.vs *= 2.0 ** rng.integers(-25, 12, c.vs.shape).astype(np.float32)
+    c.v[3:5], c.vs[3:5] = 128, 0
+    c.upload()
+    check_attention(c, 8, [300, 64], seed=6)
+    check_attention(c, 8, [300, 64], seed=6, spread=6.0)
+    # one token decides, with a scale far below that of the tokens that count for nothing
+    c = Cache(4, 1, 16, 64, True, seed=12)
+    q = np.ones((1, 64), np.float16)
+    c.k[...], c.vs[...] = 128 - 100, 2.0 ** 10
+    c.k[2, 0, 5], c.vs[2, 0, 5] = 128 + 100, 2.0 ** -14
+    c.ks[...] = 1.0
+    c.upload()
+    pages = np.arange(4, dtype=np.int32)[None]
+    check_attention(c, 1, [64], q=q, pages=pages, scale=0.01)
+    # heads of zeros only
+    c.v[...], c.vs[...] = 128, 0
+    c.upload()
+    assert not check_attention(c, 1, [64], q=q, pages=pages).any()
+
+
+def test_attention_of_what_is_not_finite(gpu_lib):
+    """A NaN among the visible makes its head NaN, and no other."""
+    for int8 in (True, False):
+        c = Cache(20, 2, 16, 64, int8, seed=13)
+        rng = np.random.default_rng(6)
+        pages = tables(rng, c, [100, 100])
+        p = pages[0, 3]
+        if int8:
+            c.ks[p, 0, 2] = np.nan
+        else:
+            c.k[p, 0, 2, 9] = np.nan
+        c.upload()
+        q = rng.standard_normal((2, 256)).astype(np.float16)
+        import torch
+        y = torch.empty(2, 256, dtype=torch.float16, device="cuda")
+        ws = torch.empty(woq.woq_attn_decode_workspace(c.desc, 4, 2), dtype=torch.uint8, device="cuda")
+        woq.woq_attn_decode(c.desc, dev(q), dev(pages), dev(np.array([100, 100], np.int32)), y, ws)
+        got = host(y)
+        assert np.all(np.isnan(got[0, :128])) and np.all(np.isfinite(got[0, 128:])) and np.all(np.isfinite(got[1]))
+
+
+def test_attention_over_its_queries_and_rows_of_a_sequence(gpu_lib):
+    """y over q; four new tokens of one sequence as rows with the same pages and
+    rising lengths give what each alone gives, bit for bit."""
+    import torch
+    c = Cache(20, 2, 16, 64, True, seed=14)
+    rng = np.random.default_rng(7)
+    q = rng.standard_normal((4, 256)).astype(np.float16)
+    pages = np.repeat(rng.permutation(20)[None, :9], 4, 0).astype(np.int32)
+    lens = np.array([130, 131, 132, 133], np.int32)
+    qd = dev(q)
+    ws = torch.empty(woq.woq_attn_decode_workspace(c.desc, 4, 4), dtype=torch.uint8, device="cuda")
+    woq.woq_attn_decode(c.desc, qd, dev(pages), dev(lens), qd, ws)
+    check_attention(c, 4, lens, q=q, pages=pages, got=host(qd))
+
+
+# ----------------------------------------------------------------- sampling
+
+def check_sample(x, u, T=None, k=None, p=None, m=None, pad=0):
+    import torch
+    b, N = x.shape
+    ld = -(-N // 8) * 8 + 8 * pad
+    wide = np.full((b, ld), 60000, np.float16)           # what stands behind a row is not a logit
+    wide[:, :N] = x
+    xd = dev(wide)
+    token = torch.full((b + 1,), -7, dtype=torch.int32, device="cuda")
+    prob = torch.full((b + 1,), -7.0, device="cuda")
+
+    def of(a, t):
+        return None if a is None else dev(np.broadcast_to(np.asarray(a, t), (b,)).copy())
+
+    f = np.float32
+    woq.woq_sample(xd, of(u, f), token, temperature=of(T, f), top_k=of(k, np.int32), top_p=of(p, f), min_p=of(m, f),
+                   prob=prob, N=N)
+    got, share = host(token), host(prob)
+    assert got[b] == -7 and share[b] == -7
+
+    def at(a, r, none):
+        return none if a is None else float(np.broadcast_to(np.asarray(a, f), (b,))[r])
+
+    for r in range(b):
+        want, ref = O.sample(x[r], at(u, r, 0), at(T, r, 1.0), int(at(k, r, 0)), at(p, r, 1.0), at(m, r, 0.0))
+        assert got[r] == want, (r, got[r], want, x[r, got[r]] if got[r] >= 0 else None, x[r, want])
+        assert abs(share[r] - ref) <= ref * 2 * U, (r, share[r], ref)
+    return got[:b]
+
+
+def logits(b, N, seed, spread=3.0):
+    rng = np.random.default_rng(seed)
+    x = (rng.standard_normal((b, N)) * spread).astype(np.float16)
+    x[::2, 3::17] = -np.inf
+    return x, rng
+
+
+@pytest.mark.parametrize("N", [1, 2, 7, 8, 9, 63, 511, 512, 513, 1000, 8191, 32000, 128256])
+def test_sample_sizes(gpu_lib, N):
+    case("sample", N)
+    b = 24 if N < 10000 else 6
+    x, rng = logits(b, N, N)
+    u = rng.random(b).astype(np.float32)
+    check_sample(x, u)
+    check_sample(x, u, T=rng.choice([0.0, 0.3, 1.0, 2.5], b), k=rng.choice([0, 1, 2, 50, 2 ** 30], b), pad=1)
+    check_sample(x, u, p=rng.choice([0.1, 0.5, 0.95, 1.0], b), m=rng.choice([0.0, 0.01, 0.2], b))
+    check_sample(x, u, T=rng.choice([0.5, 1.0], b), k=rng.choice([5, 40, 400], b), p=rng.choice([0.3, 0.9], b),
+                 m=rng.choice([0.0, 0.05], b), pad=2)
+
+
+@pytest.mark.parametrize("spread", [0.0, 1e-3, 0.1, 30.0, 3000.0])
+def test_sample_flat_and_sharp(gpu_lib, spread):
+    case("sample spread", spread)
+    x, rng = logits(16, 5000, 3, spread)
+    u = rng.random(16).astype(np.float32)
+    check_sample(x, u)
+    check_sample(x, u, T=0.7, p=0.9)
+    check_sample(x, u, k=37, m=0.5)
+
+
+def test_sample_every_draw_of_a_few_tokens(gpu_lib):
+    """Numbers at, before and behind the steps of equal weights, and out of range."""
+    x = np.zeros((16, 4), np.float16)
+    u = np.array([0, 0.2499, 0.25, 0.26, 0.4999, 0.5, 0.7499, 0.75, 0.9999, 1 - 2.0 ** -24, 1.0, 2.0, -1.0, np.nan,
+                  np.inf, -np.inf], np.float32)
+    got = check_sample(x, u)
+    np.testing.assert_array_equal(got, [0, 0, 1, 1, 1, 2, 2, 3, 3, 3, 3, 3, 0, 0, 3, 0])
+
+
+def test_sample_what_can_not_be_taken(gpu_lib):
+    x, rng = logits(10, 3000, 5)
+    x[0], x[1] = np.nan, -np.inf
+    x[2, 100:], x[2, :100] = np.nan, -np.inf
+    x[2, 77] = -65504
+    x[3, [5, 9, 2000]] = np.inf
+    x[4] = np.where(np.arange(3000) % 2, np.float16(-0.0), np.float16(0.0))
+    x[5, 1234] = np.nan
+    u = rng.random(10).astype(np.float32)
+    got = check_sample(x, u)
+    assert got[0] == got[1] == -1 and got[2] == 77 and got[3] in (5, 9, 2000)
+    check_sample(x, u, T=0.0)
+    check_sample(x, u, T=1e-30, k=7, p=0.9, m=0.3)
+    check_sample(x, u, T=np.inf)
+    check_sample(x, u, T=np.nan)
+    check_sample(x, u, k=-3, p=np.nan, m=np.nan)
+    check_sample(x, u, p=-1.0)
+    check_sample(x, u, p=0.0, k=100)
+    check_sample(x, u, m=1.0)
+    check_sample(x, u, m=5.0)
+
+
+@pytest.mark.parametrize("N", [65535, 65536, 65537, 131080, 200003])
+def test_sample_more_equal_logits_than_16_bits_count(gpu_lib, N):
+    """One value, two values on either side of zero, and one value among others."""
+    case("sample equal", N)
+    rng = np.random.default_rng(N)
+    x = np.zeros((9, N), np.float16)
+    x[1], x[2] = -5, 7
+    x[3] = np.where(rng.random(N) < 0.5, np.float16(1.0), np.float16(-1.0))
+    x[4:] = rng.standard_normal((5, N)) * 2
+    x[5, rng.random(N) < 0.9] = -1.5
+    x[6, rng.random(N) < 0.9] = 1.5
+    x[7, rng.random(N) < 0.95] = 0.25
+    x[8, :] = -np.inf
+    x[8, N // 2:] = 3
+    u = rng.random(9).astype(np.float32)
+    check_sample(x, u)
+    check_sample(x, u, T=0.8, p=0.9, m=0.01)
+    check_sample(x, u, k=[1, 70000, N, N - 1, 1000, 66000, 60000, 65536, 30000])
+    check_sample(x, u, k=66000, p=0.999)
+
+
+def test_sample_rows_do_not_touch_each_other(gpu_lib):
+    x, rng = logits(300, 1000, 8)
+    u = rng.random(300).astype(np.float32)
+    together = check_sample(x, u, p=0.9)
+    for r in (0, 17, 299):
+        assert check_sample(x[r:r + 1], u[r:r + 1], p=0.9)[0] == together[r]

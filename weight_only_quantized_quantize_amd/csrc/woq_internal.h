@@ -29,6 +29,15 @@ int lora_check(const woq_lora_w* w, const uint16_t* x, int64_t ldx, const int32_
                const uint16_t* base, int64_t ldbase, const uint16_t* y, int64_t ldy, const void* workspace,
                int64_t workspace_bytes);
 
+// The checks of a cache's descriptor: WOQ_EINVAL, WOQ_EALIGN and
+// WOQ_EUNSUPPORTED in that order.
+int cache_check(const woq_cache* c);
+
+// The argument checks of woq_attn_decode, in its order; nothing is launched.
+int attn_check(const woq_cache* c, const uint16_t* q, int64_t ldq, int32_t q_heads, const int32_t* pages,
+               int64_t ldpages, int64_t max_pages, const int32_t* lens, int64_t b, float scale, float softcap,
+               int32_t window, const uint16_t* y, int64_t ldy, const void* workspace, int64_t workspace_bytes);
+
 // Launch step i of a stack with the given step contents (the entry itself or
 // a copy whose weight pointers were moved); argument checks as woq_stack_run.
 int stack_run_step(woq_stack* st, int64_t i, const woq_stack_step* s, const uint16_t* x, uint16_t* y, int64_t b,

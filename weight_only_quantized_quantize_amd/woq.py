@@ -68,7 +68,14 @@ class LoraW(ctypes.Structure):
     device = None       # index of the GPU that holds the pool, where it is known
 
 
+class Cache(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p), ("n_pages", c_int64),
+                ("fmt", c_int32), ("heads", c_int32), ("page", c_int32), ("dim", c_int32)]
+    device = None       # index of the GPU that holds the cache, where it is known
+
+
 FMT_INT8, FMT_INT4O = 1, 2
+CACHE_FP16, CACHE_INT8 = 1, 2
 
 _LIB = None
 _torch = None       # torch, imported with the library
@@ -114,6 +121,14 @@ _SIGS = {
     "woq_lora_add": (c_int, [POINTER(LoraW), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
                              c_int64, c_void_p, c_int64, c_void_p]),
     "woq_lora_workspace": (c_int64, [POINTER(LoraW), c_int64]),
+    "woq_cache_write": (c_int, [POINTER(Cache), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                c_int32, c_void_p, c_int64, c_void_p, c_int64, c_int32, c_int32, c_void_p, c_void_p]),
+    "woq_cache_read": (c_int, [POINTER(Cache), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p]),
+    "woq_attn_decode": (c_int, [POINTER(Cache), c_void_p, c_int64, c_int32, c_void_p, c_int64, c_int64, c_void_p, c_int64,
+                                c_float, c_float, c_int32, c_void_p, c_int64, c_void_p, c_int64, c_void_p]),
+    "woq_attn_decode_workspace": (c_int64, [POINTER(Cache), c_int32, c_int64]),
+    "woq_sample": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                           c_void_p, c_void_p]),
     "woq_stack_create": (c_int, [POINTER(StackStep), c_int32, c_int64, POINTER(c_void_p)]),
     "woq_stack_run": (c_int, [c_void_p, POINTER(c_void_p), POINTER(c_void_p), c_int64, c_void_p]),
     "woq_stack_run_lora": (c_int, [c_void_p, POINTER(c_void_p), POINTER(c_void_p), c_int64, POINTER(c_void_p),
@@ -611,6 +626,113 @@ def woq_lora_add(w: LoraW, x, ids, base, y, workspace, stream=None, b: int | Non
     return y
 
 
+# --------------------------------- device ops: between the products of a step
+
+def _optional(t, what: str, dtype, n: int):
+    return None if t is None else _vector(t, what, dtype, n)
+
+
+def woq_cache_write(c: Cache, k, v, slots, q=None, q_out=None, rope=None, pos=None, interleaved: bool = False,
+                    stream=None, b: int | None = None):
+    """Write the rows k and v (fp16 [b, >= heads * dim]) into the slots (int32
+    [b]; one outside the cache is skipped) of a cache (DeviceCache.desc).  With
+    ``rope`` (fp32 [positions, rot]: cosines, then sines) the heads of k, and of
+    q (fp16 [b, q_heads * dim]) into q_out, are turned by the angles of the
+    positions pos (int32 [b]) first."""
+    _lib()
+    half, i32 = _torch.float16, _torch.int32
+    if b is None:
+        b = k.shape[0]
+    width = c.heads * c.dim
+    kp, ldk = _rows(k, "k", half, b, width)
+    vp, ldv = _rows(v, "v", half, b, width)
+    if (q is None) != (q_out is None) or (rope is None) != (pos is None):
+        raise ValueError("q goes with q_out, rope with pos")
+    qp, ldq, q_heads, op, ldo = None, 0, 0, None, 0
+    if q is not None:
+        q_heads, rest = divmod(q.shape[1], c.dim)
+        if rest or not q_heads:
+            raise ValueError(f"q: {q.shape[1]} values a row are not heads of {c.dim}")
+        qp, ldq = _rows(q, "q", half, b, q.shape[1])
+        op, ldo = _rows(q_out, "q_out", half, b, q.shape[1])
+    rp, n_pos, rot, pp = None, 0, 0, None
+    if rope is not None:
+        if rope.dim() != 2:
+            raise ValueError("rope: expected [positions, rot]")
+        n_pos, rot = rope.shape
+        rp, pp = _vector(rope, "rope", _torch.float32, 0), _vector(pos, "pos", i32, b)
+    _call("woq_cache_write", stream, (k, v, slots, q, q_out, rope, pos), c, kp, ldk, vp, ldv,
+          _vector(slots, "slots", i32, b), b, qp, ldq, q_heads, op, ldo, rp, n_pos, rot, int(interleaved), pp,
+          held=(("the cache", c.device),))
+
+
+def woq_cache_read(c: Cache, slots, k_out=None, v_out=None, stream=None, n: int | None = None):
+    """Read the tokens at slots (int32 [n]) of a cache back into fp16 rows of
+    heads * dim values, keys into k_out, values into v_out; a slot outside the
+    cache gives zeros."""
+    _lib()
+    if n is None:
+        n = slots.shape[0]
+    width = c.heads * c.dim
+    kp, ldk = (None, 0) if k_out is None else _rows(k_out, "k_out", _torch.float16, n, width)
+    vp, ldv = (None, 0) if v_out is None else _rows(v_out, "v_out", _torch.float16, n, width)
+    _call("woq_cache_read", stream, (slots, k_out, v_out), c, _vector(slots, "slots", _torch.int32, n), n, kp, ldk, vp,
+          ldv, held=(("the cache", c.device),))
+
+
+def woq_attn_decode_workspace(c: Cache, q_heads: int, b: int) -> int:
+    """Bytes of the workspace of woq_attn_decode for batches of up to b rows."""
+    n = _lib().woq_attn_decode_workspace(ctypes.byref(c), q_heads, b)
+    if n < 0:
+        _check(n, "woq_attn_decode_workspace")
+    return n
+
+
+def woq_attn_decode(c: Cache, q, pages, lens, y, workspace, scale: float | None = None, softcap: float = 0.0,
+                    window: int = 0, stream=None, b: int | None = None):
+    """y (fp16 [b, q_heads * dim]) = attention of the query rows q over the
+    first lens[r] (int32 [b]) tokens of the cache's pages pages[r] (int32 [b,
+    W]), or the last ``window`` of them; scale defaults to dim ** -0.5."""
+    _lib()
+    half = _torch.float16
+    if b is None:
+        b = q.shape[0]
+    width = q.shape[1]
+    q_heads, rest = divmod(width, c.dim)
+    if rest:
+        raise ValueError(f"q: {width} values a row are not heads of {c.dim}")
+    qp, ldq = _rows(q, "q", half, b, width)
+    yp, ldy = _rows(y, "y", half, b, width)
+    W = pages.shape[1]
+    tp, ldt = _rows(pages, "pages", _torch.int32, b, W)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    _call("woq_attn_decode", stream, (q, pages, lens, y, workspace), c, qp, ldq, q_heads, tp, ldt, W,
+          _vector(lens, "lens", _torch.int32, b), b, c.dim ** -0.5 if scale is None else scale, softcap, window, yp, ldy,
+          workspace.data_ptr(), workspace.numel() * workspace.element_size(), held=(("the cache", c.device),))
+    return y
+
+
+def woq_sample(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None, prob=None, N: int | None = None,
+               stream=None, b: int | None = None):
+    """token (int32 [b]) = the next token of every row of logits (fp16 [b, >= N])
+    drawn with the number u[r] (fp32 [b], in [0, 1)) from what top_k (int32
+    [b]), min_p and top_p (fp32 [b]) keep at a temperature (fp32 [b]; 0: the
+    largest logit); prob (fp32 [b]) receives its share."""
+    _lib()
+    f32, i32 = _torch.float32, _torch.int32
+    if b is None:
+        b = logits.shape[0]
+    if N is None:
+        N = logits.shape[1]
+    lp, ld = _rows(logits, "logits", _torch.float16, b, N)
+    _call("woq_sample", stream, (logits, temperature, top_k, top_p, min_p, u, token, prob), lp, ld, N, b,
+          _optional(temperature, "temperature", f32, b), _optional(top_k, "top_k", i32, b),
+          _optional(top_p, "top_p", f32, b), _optional(min_p, "min_p", f32, b), _vector(u, "u", f32, b),
+          _vector(token, "token", i32, b), _optional(prob, "prob", f32, b))
+    return token
+
+
 # ------------------------------------------------- device-resident weights
 
 class DeviceInt8:
@@ -704,6 +826,44 @@ class DeviceLora:
         d.N, d.K, d.lda, d.R, d.count, d.nseg = N, K, A.shape[2], R, count, len(segments)
         for i, e in enumerate(segments):
             d.seg_end[i] = e
+
+
+class DeviceCache:
+    """A paged cache of keys and values (woq_cache) over device tensors, which it
+    keeps: k and v [pages, heads, page, dim], fp16, or uint8 (code + 128) with
+    fp32 scales k_scale and v_scale [pages, heads, page]."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        _lib()
+        int8 = k_scale is not None
+        if int8 != (v_scale is not None) or k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v are [pages, heads, page, dim], with a scale each or none")
+        n_pages, heads, page, dim = k.shape
+        tensors = [t for t in (k, v, k_scale, v_scale) if t is not None]
+        if any(t.device != k.device or not t.is_cuda for t in tensors):
+            raise ValueError("the cache's tensors have to be on one GPU")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        d = self.desc = Cache()
+        d.device = k.get_device()
+        dtype = _torch.uint8 if int8 else _torch.float16
+        d.k, d.v = _vector(k, "k", dtype, 0), _vector(v, "v", dtype, 0)
+        if int8:
+            n = n_pages * heads * page
+            d.k_scale = _vector(k_scale, "k_scale", _torch.float32, n)
+            d.v_scale = _vector(v_scale, "v_scale", _torch.float32, n)
+        d.n_pages, d.heads, d.page, d.dim = n_pages, heads, page, dim
+        d.fmt = CACHE_INT8 if int8 else CACHE_FP16
+
+    @classmethod
+    def empty(cls, n_pages: int, heads: int, page: int, dim: int, int8: bool = True, device="cuda"):
+        """A cache of its own tensors; what its slots hold is unspecified until written."""
+        _lib()
+        shape, f32 = (n_pages, heads, page, dim), _torch.float32
+        dtype = _torch.uint8 if int8 else _torch.float16
+        k, v = (_torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+        if not int8:
+            return cls(k, v)
+        return cls(k, v, *(_torch.empty(shape[:3], dtype=f32, device=device) for _ in range(2)))
 
 
 # ------------------------------------------------------------- stack runner
