@@ -3,8 +3,6 @@
 //   z[t] = scale (q . k[t]), or softcap tanh(scale (q . k[t]) / softcap),
 //   y = sum_t e^(z[t] - m) v[t] / sum_t e^(z[t] - m),   m = max_t z[t].
 //
-// One wave per row and query head: a lane takes every 64th token for the scores,
-// then every 64th value of the head for the sums.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -16,6 +14,12 @@ namespace {
 
 using namespace woqk;
 
+constexpr int WAVES = 4, T = 64 * WAVES;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float NONE = -__builtin_huge_valf();
+constexpr float LEAST = 0x1p-60f;   // a smaller scale of values counts as this: its values are zero in fp16 either way
+constexpr float TOP = 15.0f;        // the largest weight is 2^15, so that fp16 holds weights 2^-40 of it
+
 struct AttnArgs {
     const uint8_t* k;
     const uint8_t* v;
@@ -25,60 +29,507 @@ struct AttnArgs {
     const int32_t* pages;
     const int32_t* lens;
     uint16_t* y;
+    int64_t* head;            // workspace: positions of a workgroup, then the units before every row and of all
+    float* sums;              // [2 * workgroups][rows of a tile][dim]
+    float* stats;             // [2 * workgroups][16][2]: the reference of the weights, their sum
     int64_t ldq, ldpages, ldy, n_pages, capacity;
     float scale, softcap;
-    int heads, group, page, dim, window;
+    int heads, group, page, dim, window, b, tiles, per_tile;
 };
 
-__global__ __launch_bounds__(64) void attn_decode_kernel(AttnArgs a) {
-    __shared__ float qs[WOQ_CACHE_MAX_DIM];
-    const int lane = threadIdx.x, hq = blockIdx.x % (a.heads * a.group), r = blockIdx.x / (a.heads * a.group);
-    const int h = hq / a.group;
-    for (int d = lane; d < a.dim; d += 64) qs[d] = h_to_f(a.q[r * a.ldq + (int64_t)hq * a.dim + d]);
-    __syncthreads();
-    const int64_t len = min((int64_t)max(a.lens[r], 0), a.capacity);
-    const int64_t first = a.window > 0 ? max((int64_t)0, len - a.window) : 0;
-    float m = -INFINITY, total = 0.0f, acc[4] = {};
-    for (int64_t t0 = first; t0 < len; t0 += 64) {
-        const int64_t t = t0 + lane;
-        float z = -INFINITY;
-        int64_t at = -1;
-        if (t < len) {
-            const int64_t page = a.pages[r * a.ldpages + t / a.page];
-            if (page >= 0 && page < a.n_pages) at = (page * a.heads + h) * a.page + t % a.page;
+// What row r sees: tokens first .. len - 1, in sixteens s0 .. s1 - 1 and units of
+// two of them.
+struct Span {
+    int len, first, s0, s1, units;
+};
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int r) {
+    Span s;
+    const int64_t len = min((int64_t)max(*gptr(a.lens + r), 0), a.capacity);
+    s.len = (int)len;
+    s.first = a.window > 0 ? max(0, s.len - a.window) : 0;
+    s.s0 = s.first >> 4;
+    s.s1 = (int)((len + 15) >> 4);
+    s.units = (s.s1 - s.s0 + 1) >> 1;
+    return s;
+}
+
+// The bytes that a lane loads of a sixteen of tokens: of the keys 16 bytes of one
+// token's row at a time (token lane % 16), of the values its E = DP / 16 channels of
+// four tokens (4 (lane / 16) ..), as the matrix instructions want them.
+template <int DP, bool INT8>
+struct Tile {
+    static constexpr int E = DP / 16;
+    static constexpr int NK = INT8 ? DP / 64 : DP / 32;        // 16-byte pieces of a key
+    static constexpr int WV = INT8 ? E / 4 : E / 2;            // words of a token's values
+    uint4 k[2][NK];
+    uint32_t v[8][WV];
+    f4 ks[2], vs[2];
+};
+
+template <int W>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&v)[W]) {
+    if constexpr (W == 1) {
+        v[0] = *gptr(reinterpret_cast<const uint32_t*>(p));
+    } else if constexpr (W == 2) {
+        const uint2 w = gload_u2(reinterpret_cast<const uint2*>(p));
+        v[0] = w.x, v[1] = w.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+            const uint4 w = gload_u4(reinterpret_cast<const uint4*>(p) + i);
+            v[4 * i] = w.x, v[4 * i + 1] = w.y, v[4 * i + 2] = w.z, v[4 * i + 3] = w.w;
         }
-        if (at >= 0) {
-            float s = 0.0f;
-            for (int d = 0; d < a.dim; ++d)
-                s += qs[d] * (a.ks ? (float)((int)a.k[at * a.dim + d] - 128)
-                                   : h_to_f(reinterpret_cast<const uint16_t*>(a.k)[at * a.dim + d]));
-            z = s * a.scale * (a.ks ? a.ks[at] : 1.0f);
-            if (a.softcap > 0.0f) z = a.softcap * tanhf(z / a.softcap);
-        }
-        // a NaN score stays: the row becomes NaN
-        float top = z;
-        for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-        const float next = fmaxf(m, top), base = next == -INFINITY ? 0.0f : next;
-        const float keep = expf(m - base);
-        const float p = at >= 0 ? expf(z - base) : 0.0f;
-        total = total * keep + p;
-        const float pv = p * (a.vs && at >= 0 ? a.vs[at] : 1.0f);
-        for (int i = 0; i < 4; ++i) acc[i] *= keep;
-        for (int j = 0; j < 64 && t0 + j < len; ++j) {
-            const float pj = __shfl(pv, j);
-            const int64_t aj = __shfl(at, j);
-            if (aj < 0) continue;
-            for (int i = 0; i < 4; ++i)
-                if (lane + 64 * i < a.dim)
-                    acc[i] += pj * (a.ks ? (float)((int)a.v[aj * a.dim + lane + 64 * i] - 128)
-                                         : h_to_f(reinterpret_cast<const uint16_t*>(a.v)[aj * a.dim + lane + 64 * i]));
-        }
-        m = next;
     }
-    for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
-    for (int i = 0; i < 4; ++i)
-        if (lane + 64 * i < a.dim)
-            a.y[r * a.ldy + (int64_t)hq * a.dim + lane + 64 * i] = f_to_h(total == 0.0f ? 0.0f : acc[i] / total);
+}
+
+__device__ __forceinline__ h8 pack8(h2 a, h2 b, h2 c, h2 d) {
+    return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// One segment of one row, key head and tile of up to 16 query heads: units u0 ..
+// u1 - 1, divided among the waves.
+template <int DP, bool INT8, bool EXACT>
+__global__ __launch_bounds__(T) void attn_split_kernel(AttnArgs a) {
+    using Mem = Tile<DP, INT8>;
+    constexpr int E = Mem::E, NK = Mem::NK, WV = Mem::WV, SIZE = INT8 ? 1 : 2;
+    constexpr int EC = E < 8 ? E : 8, ROW = 16 * EC + 4;       // channels of a lane joined at a time
+    __shared__ __align__(16) float join[WAVES * 16 * ROW];
+    __shared__ float join_m[WAVES][16], join_l[WAVES][16];
+    __shared__ int64_t scan[WAVES], found[2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
+    const int HH = a.heads * a.tiles;
+
+    // the units before every row; all positions (row, head, tile, unit) in order, an
+    // equal count of them to every workgroup
+    int64_t mine = 0, before = 0, total = 0;
+    const int each = (a.b + T - 1) / T, lo = min(a.b, tid * each), hi = min(a.b, lo + each);
+    for (int r = lo; r < hi; ++r) mine += span_of(a, r).units;
+    if (a.b > 1) {
+        int64_t s = mine;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t o = __shfl_up(s, d);
+            if (lane >= d) s += o;
+        }
+        if (lane == 63) scan[wave] = s;
+        __syncthreads();
+        before = s - mine;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            if (w < wave) before += scan[w];
+            total += scan[w];
+        }
+    } else {
+        total = __shfl(span_of(a, 0).units, 0);
+    }
+    const int64_t positions = total * HH;
+    const int64_t per = max((int64_t)WAVES, (positions + gridDim.x - 1) / gridDim.x);
+    if (blockIdx.x == 0) {
+        int64_t at = before;
+        for (int r = lo; r < hi; ++r) {
+            *gptr(a.head + 1 + r) = at;
+            at += span_of(a, r).units;
+        }
+        if (tid == 0) {
+            *gptr(a.head) = per;
+            *gptr(a.head + 1 + a.b) = total;
+        }
+    }
+    int64_t pos = blockIdx.x * per;
+    const int64_t begin = pos, end = min(positions, pos + per);
+    if (pos >= end) return;
+    if (a.b > 1) {
+        if (before * HH <= pos && pos < (before + mine) * HH) {
+            int64_t at = before;
+            int r = lo;
+            for (; r < hi; ++r) {
+                const int n = span_of(a, r).units;
+                if (pos < (at + n) * HH) break;
+                at += n;
+            }
+            found[0] = r, found[1] = at;
+        }
+        __syncthreads();
+    } else if (tid == 0) {
+        found[0] = found[1] = 0;
+    }
+    if (a.b == 1) __syncthreads();
+    int r = (int)found[0];
+    int64_t base = found[1] * HH;
+    r = __builtin_amdgcn_readfirstlane(r);
+    Span sp = span_of(a, r);
+
+    // where a lane's pieces of a sixteen stand in bytes; channels past dim are read
+    // from the row's start and meet a query of zero
+    const int dim = EXACT ? DP : a.dim;
+    uint32_t ko[NK], vo[4];
+    bool kin[NK];
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+        const int d = INT8 ? 64 * i + 16 * g : 32 * i + 8 * g;
+        kin[i] = EXACT || d < dim;
+        ko[i] = (uint32_t)(m * dim + (kin[i] ? d : 0)) * SIZE;
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) vo[t] = (uint32_t)((4 * g + t) * dim + (EXACT || E * m < dim ? E * m : 0)) * SIZE;
+    const int spp = a.page >> 4;              // sixteens of a page
+
+    while (pos < end) {
+        const int64_t rel = pos - base;
+        const int hh = (int)(rel / sp.units), u0 = (int)(rel - (int64_t)hh * sp.units);
+        const int u1 = (int)min((int64_t)sp.units, u0 + (end - pos));
+        const int h = hh / a.tiles, tile = hh - h * a.tiles;
+        const int heads = min(16, a.group - 16 * tile);          // query heads of this tile
+        const int q0 = h * a.group + 16 * tile;
+        const int share = (u1 - u0 + WAVES - 1) / WAVES;
+        const int ub = min(u1, u0 + wave * share), ue = min(u1, ub + share);
+
+        h8 q[DP / 32];
+        {
+            const uint16_t* row = a.q + r * a.ldq + (int64_t)(q0 + m) * dim;
+#pragma unroll
+            for (int i = 0; i < DP / 32; ++i) {
+                const int d = INT8 ? 64 * (i / 2) + 16 * g + 8 * (i & 1) : 32 * i + 8 * g;
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (m < heads && (EXACT || d < dim)) w = gload_u4(reinterpret_cast<const uint4*>(row + d));
+                q[i] = __builtin_bit_cast(h8, w);
+            }
+        }
+        f4 acc[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = f4{0, 0, 0, 0};
+        float top = NONE, sum = 0.0f;
+
+        // page of the sixteen sb + lane and its place there; -1 where it is not
+        int sb = sp.s0 + 2 * ub, pg = -1, po = 0;
+        auto fetch = [&](int s, int& page, int& off) {
+            page = -1;
+            off = 0;
+            if (s < sp.s1) {
+                const int p = (int)((uint32_t)s / (uint32_t)spp);
+                page = *gptr(a.pages + r * a.ldpages + p);
+                off = s - p * spp;
+                if (page < 0 || page >= a.n_pages) page = -1;
+            }
+        };
+        Mem t;
+        bool there[2];
+        int64_t at[2];                        // first token of the two sixteens
+        auto place = [&](int u) {
+            const int s = sp.s0 + 2 * u;
+            if (s - sb >= 64) {
+                sb += 64;
+                fetch(sb + lane, pg, po);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int p = __builtin_amdgcn_readlane(pg, s - sb + j), o = __builtin_amdgcn_readlane(po, s - sb + j);
+                there[j] = p >= 0;
+                at[j] = (((int64_t)max(p, 0) * a.heads + h) * spp + (p >= 0 ? o : 0)) * 16;
+            }
+        };
+        auto load_k = [&] {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint8_t* p = a.k + at[j] * dim * SIZE;
+#pragma unroll
+                for (int i = 0; i < NK; ++i) t.k[j][i] = gload_nt(reinterpret_cast<const uint4*>(p + ko[i]));
+                if constexpr (INT8) t.ks[j] = *(__attribute__((address_space(1))) const f4*)(a.ks + at[j] + 4 * g);
+            }
+        };
+        auto load_v = [&] {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint8_t* p = a.v + at[j] * dim * SIZE;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) load_words<WV>(p + vo[i], t.v[4 * j + i]);
+                if constexpr (INT8) t.vs[j] = *(__attribute__((address_space(1))) const f4*)(a.vs + at[j] + 4 * g);
+            }
+        };
+
+        if (ub < ue) {
+            fetch(sb + lane, pg, po);
+            place(ub);
+            load_k();
+            load_v();
+        }
+        for (int u = ub; u < ue; ++u) {
+            const int t0 = 16 * (sp.s0 + 2 * u);
+            const bool whole = there[0] && there[1] && t0 >= sp.first && t0 + 32 <= sp.len;
+            // scores: lane (g, m) gets tokens 4 g .. 4 g + 3 of both sixteens for head m
+            float z[8];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                f4 s = {0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < NK; ++i) {
+                    if constexpr (INT8) {
+                        const uint32_t w[4] = {t.k[j][i].x, t.k[j][i].y, t.k[j][i].z, t.k[j][i].w};
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            h2 c[4];
+                            int8_pairs(w[2 * e], c[0], c[1]);
+                            int8_pairs(w[2 * e + 1], c[2], c[3]);
+                            s = __builtin_amdgcn_mfma_f32_16x16x32_f16(pack8(c[0], c[1], c[2], c[3]), q[2 * i + e], s, 0, 0, 0);
+                        }
+                    } else {
+                        uint4 w = t.k[j][i];
+                        if (!EXACT && !kin[i]) w = make_uint4(0, 0, 0, 0);
+                        s = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, w), q[i], s, 0, 0, 0);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float x = s[i] * a.scale;
+                    if constexpr (INT8) x *= t.ks[j][i];
+                    if (a.softcap > 0.0f) {
+                        // tanh(x) = 1 - 2 / (1 + e^2x)
+                        const float e2 = __builtin_amdgcn_exp2f(2.0f * LOG2E * x / a.softcap);
+                        x = a.softcap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e2));
+                    }
+                    z[4 * j + i] = x * LOG2E;
+                }
+            }
+            float inv[8];                     // of the values' scales
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                inv[i] = 1.0f;
+                if constexpr (INT8) {
+                    const float s = fmaxf(t.vs[i >> 2][i & 3], LEAST);
+                    // a scale that is NaN stays one
+                    const float sv = t.vs[i >> 2][i & 3] != t.vs[i >> 2][i & 3] ? t.vs[i >> 2][i & 3] : s;
+                    z[i] += __builtin_amdgcn_logf(sv);
+                    inv[i] = __builtin_amdgcn_rcpf(sv);
+                }
+            }
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
+                    const bool seen = there[i >> 2] && tok >= sp.first && tok < sp.len;
+                    if (!seen) {
+                        z[i] = NONE;
+                        inv[i] = 0.0f;
+                        if constexpr (!INT8) {
+#pragma unroll
+                            for (int w = 0; w < WV; ++w) t.v[i][w] = 0;
+                        }
+                    }
+                }
+            }
+            if (u + 1 < ue) {
+                place(u + 1);
+                load_k();
+            }
+            float most = z[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) most = fmaxf(most, z[i]);
+            most = fmaxf(most, __shfl_xor(most, 16));
+            most = fmaxf(most, __shfl_xor(most, 32));
+            if (__any(most > top)) {
+                const float next = fmaxf(top, most), keep = __builtin_amdgcn_exp2f(top - (next == NONE ? 0.0f : next));
+                top = next;
+                sum *= keep;
+#pragma unroll
+                for (int i = 0; i < E; ++i) acc[i] *= keep;
+            }
+            const float ref = (top == NONE ? 0.0f : top) - TOP;
+            f16 w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float e = __builtin_amdgcn_exp2f(z[i] - ref);
+                sum = fmaf(e, inv[i], sum);
+                w[i] = (f16)e;
+            }
+            const h8 weights = {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
+            // sums: rows of the product are the channels E (lane % 16) + i
+            if constexpr (INT8) {
+#pragma unroll
+                for (int c = 0; c < WV; ++c) {
+                    h2 p[4][4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t e = t.v[2 * x][c], o = t.v[2 * x + 1][c];
+                        int8_pairs(__builtin_amdgcn_perm(o, e, 0x05010400u), p[0][x], p[1][x]);
+                        int8_pairs(__builtin_amdgcn_perm(o, e, 0x07030602u), p[2][x], p[3][x]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        acc[4 * c + x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pack8(p[x][0], p[x][1], p[x][2], p[x][3]),
+                                                                                weights, acc[4 * c + x], 0, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < WV; ++c) {
+                    h2 p[2][4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t e = t.v[2 * x][c], o = t.v[2 * x + 1][c];
+                        p[0][x] = as_h2(__builtin_amdgcn_perm(o, e, 0x05040100u));
+                        p[1][x] = as_h2(__builtin_amdgcn_perm(o, e, 0x07060302u));
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        acc[2 * c + x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pack8(p[x][0], p[x][1], p[x][2], p[x][3]),
+                                                                                weights, acc[2 * c + x], 0, 0, 0);
+                }
+            }
+            if (u + 1 < ue) load_v();
+        }
+
+        // join the waves
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        if (g == 0) {
+            join_m[wave][m] = top;
+            join_l[wave][m] = sum;
+        }
+        __syncthreads();
+        float all = join_m[0][m];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) all = fmaxf(all, join_m[w][m]);
+        const float keep = __builtin_amdgcn_exp2f(top - (all == NONE ? 0.0f : all));
+        const int hq = tid >> 4, piece = tid & 15;               // of the joined tile: head, lane's channels
+        float ref = join_m[0][hq], l = 0.0f;
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) ref = fmaxf(ref, join_m[w][hq]);
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w)
+            l += join_l[w][hq] * __builtin_amdgcn_exp2f(join_m[w][hq] - (ref == NONE ? 0.0f : ref));
+        const bool complete = u0 == 0 && u1 == sp.units;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (pos != begin);
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int c = 0; c < E / EC; ++c) {
+            if (c) __syncthreads();
+            if (m < heads) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float* o = join + (wave * 16 + m) * ROW + (4 * g + i) * EC;
+#pragma unroll
+                    for (int e = 0; e < EC; e += 4)
+                        *reinterpret_cast<f4*>(o + e) = f4{acc[EC * c + e][i] * keep, acc[EC * c + e + 1][i] * keep,
+                                                           acc[EC * c + e + 2][i] * keep, acc[EC * c + e + 3][i] * keep};
+                }
+            }
+            __syncthreads();
+            const int d = E * piece + EC * c;
+            if (hq < heads && d < dim) {
+                f4 o[EC / 4];
+#pragma unroll
+                for (int e = 0; e < EC / 4; ++e) {
+                    o[e] = f4{0, 0, 0, 0};
+#pragma unroll
+                    for (int w = 0; w < WAVES; ++w)
+                        o[e] += *reinterpret_cast<const f4*>(join + (w * 16 + hq) * ROW + piece * EC + 4 * e);
+                }
+                if (complete) {
+                    uint16_t* out = a.y + r * a.ldy + (int64_t)(q0 + hq) * dim + d;
+#pragma unroll
+                    for (int e = 0; e < EC / 4; ++e) {
+                        const uint2 p = {(uint32_t)f_to_h(o[e][0] * inv) | (uint32_t)f_to_h(o[e][1] * inv) << 16,
+                                         (uint32_t)f_to_h(o[e][2] * inv) | (uint32_t)f_to_h(o[e][3] * inv) << 16};
+                        *(__attribute__((address_space(1))) u32x2*)(out + 4 * e) = u32x2{p.x, p.y};
+                    }
+                } else {
+                    float* out = a.sums + (slot * a.per_tile + hq) * dim + d;
+#pragma unroll
+                    for (int e = 0; e < EC / 4; ++e) *(__attribute__((address_space(1))) f4*)(out + 4 * e) = o[e];
+                }
+            }
+        }
+        if (!complete && piece == 0 && hq < heads) {
+            *gptr(a.stats + (slot * 16 + hq) * 2) = ref;
+            *gptr(a.stats + (slot * 16 + hq) * 2 + 1) = l;
+        }
+        __syncthreads();                      // the next segment writes the same memory
+
+        pos += u1 - u0;
+        if (pos < end && pos == base + (int64_t)sp.units * HH) {
+            base = pos;
+            do {
+                ++r;
+                sp = span_of(a, r);
+            } while (sp.units == 0);
+        }
+    }
+}
+
+// Rows that several workgroups share: their parts in order, each under the power of
+// two of its own; rows that see nothing are zeros.  A workgroup for every row and
+// query head, sixteen parts at a time.
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+    __shared__ float red[16][WOQ_CACHE_MAX_DIM + 4], red_l[16];
+    const int tid = threadIdx.x, part = tid >> 4, piece = tid & 15;
+    const int q_heads = a.heads * a.group, r = blockIdx.x / q_heads, hq = blockIdx.x - r * q_heads;
+    const int h = hq / a.group, in = hq - h * a.group, tile = in >> 4, row = in & 15;
+    const int64_t per = *gptr(a.head), first = *gptr(a.head + 1 + r), units = *gptr(a.head + 2 + r) - first;
+    uint16_t* out = a.y + r * a.ldy + (int64_t)hq * a.dim;
+    if (units == 0) {
+        for (int d = tid; d < a.dim; d += 256) *gptr(out + d) = 0;
+        return;
+    }
+    const int64_t p0 = first * (a.heads * a.tiles) + (int64_t)(h * a.tiles + tile) * units, p1 = p0 + units - 1;
+    const int64_t w0 = p0 / per, w1 = p1 / per;
+    if (w0 == w1) return;
+    // the first workgroup's part is its last segment, the others' their first
+    auto slot = [&](int64_t w) { return 2 * w + (w == w0 && w * per < p0); };
+    float ref = NONE;
+    for (int64_t w = w0; w <= w1; ++w) ref = fmaxf(ref, *gptr(a.stats + (slot(w) * 16 + row) * 2));
+    const float zero = ref == NONE ? 0.0f : ref;
+    float l = 0.0f, o[WOQ_CACHE_MAX_DIM / 16] = {};
+    const int e = a.dim / 16;                 // channels of a thread
+    for (int64_t w = w0 + part; w <= w1; w += 16) {
+        const float* st = a.stats + (slot(w) * 16 + row) * 2;
+        const float keep = __builtin_amdgcn_exp2f(*gptr(st) - zero);
+        const float* s = a.sums + (slot(w) * a.per_tile + row) * a.dim + piece * e;
+        l = fmaf(*gptr(st + 1), keep, l);
+#pragma unroll
+        for (int i = 0; i < WOQ_CACHE_MAX_DIM / 16; ++i)
+            if (i < e) o[i] = fmaf(*gptr(s + i), keep, o[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < WOQ_CACHE_MAX_DIM / 16; ++i)
+        if (i < e) red[part][piece * e + i] = o[i];
+    if (piece == 0) red_l[part] = l;
+    __syncthreads();
+    if (tid >= a.dim) return;
+    float s = 0.0f, t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        s += red[i][tid];
+        t += red_l[i];
+    }
+    *gptr(out + tid) = f_to_h(t == 0.0f ? 0.0f : s / t);
+}
+
+// Workgroups of a split: as many as keep two on a compute unit.
+int workgroups() { return 2 * woq::compute_units(); }
+
+struct Layout {
+    int64_t sums, stats, bytes;
+    int tiles, per_tile;
+};
+Layout layout(const woq_cache* c, int32_t q_heads, int64_t b) {
+    Layout l;
+    const int group = q_heads / c->heads, n = 2 * workgroups();
+    l.tiles = (group + 15) / 16;
+    l.per_tile = std::min(group, 16);
+    l.sums = woq::round_up((b + 2) * 8, 16);
+    l.stats = l.sums + (int64_t)n * l.per_tile * c->dim * 4;
+    l.bytes = l.stats + (int64_t)n * 16 * 2 * 4;
+    return l;
+}
+
+template <int DP, bool INT8>
+const void* split_kernel(int dim) {
+    return dim == DP ? reinterpret_cast<const void*>(&attn_split_kernel<DP, INT8, true>)
+                     : reinterpret_cast<const void*>(&attn_split_kernel<DP, INT8, false>);
+}
+template <bool INT8>
+const void* split_kernel(int dim) {
+    return dim <= 64 ? split_kernel<64, INT8>(dim) : dim <= 128 ? split_kernel<128, INT8>(dim)
+                                                                : split_kernel<256, INT8>(dim);
 }
 
 bool half_rows_ok(const void* p, int64_t ld) { return woq::aligned16(p) && (ld & 7) == 0; }
@@ -102,7 +553,9 @@ int attn_check(const woq_cache* c, const uint16_t* q, int64_t ldq, int32_t q_hea
     if (!half_rows_ok(q, ldq) || !half_rows_ok(y, ldy) || ((uintptr_t)pages & 3u) || ((uintptr_t)lens & 3u) ||
         !aligned16(workspace))
         return WOQ_EALIGN;
-    if (q_heads > WOQ_ATTN_MAX_HEADS || b > WOQ_ATTN_MAX_ROWS || max_pages > INT32_MAX / c->page)
+    // the launch that joins has 256 threads for every row and head, fewer than 2^32
+    if (q_heads > WOQ_ATTN_MAX_HEADS || b > WOQ_ATTN_MAX_ROWS || b * q_heads >= 1 << 24 ||
+        max_pages > INT32_MAX / c->page)
         return WOQ_EUNSUPPORTED;
     if (workspace_bytes < woq_attn_decode_workspace(c, q_heads, b)) return WOQ_EINVAL;
     return WOQ_OK;
@@ -114,8 +567,8 @@ extern "C" int64_t woq_attn_decode_workspace(const woq_cache* c, int32_t q_heads
     const int rc = woq::cache_check(c);
     if (rc == WOQ_EINVAL || b < 0 || q_heads < 1 || q_heads % c->heads) return WOQ_EINVAL;
     if (rc) return rc;
-    if (q_heads > WOQ_ATTN_MAX_HEADS || b > WOQ_ATTN_MAX_ROWS) return WOQ_EUNSUPPORTED;
-    return 16;
+    if (q_heads > WOQ_ATTN_MAX_HEADS || b > WOQ_ATTN_MAX_ROWS || b * q_heads >= 1 << 24) return WOQ_EUNSUPPORTED;
+    return layout(c, q_heads, b).bytes;
 }
 
 extern "C" int woq_attn_decode(const woq_cache* c, const uint16_t* q, int64_t ldq, int32_t q_heads,
@@ -146,9 +599,20 @@ extern "C" int woq_attn_decode(const woq_cache* c, const uint16_t* q, int64_t ld
     a.page = c->page;
     a.dim = c->dim;
     a.window = window;
+    a.b = (int)b;
+    const Layout l = layout(c, q_heads, b);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.head = reinterpret_cast<int64_t*>(ws);
+    a.sums = reinterpret_cast<float*>(ws + l.sums);
+    a.stats = reinterpret_cast<float*>(ws + l.stats);
+    a.tiles = l.tiles;
+    a.per_tile = l.per_tile;
     void* argv[] = {&a};
-    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(&attn_decode_kernel),
-                                         dim3((unsigned)(b * q_heads)), dim3(64), argv, 0, (hipStream_t)stream);
+    const void* split = c->fmt == WOQ_CACHE_INT8 ? split_kernel<true>(c->dim) : split_kernel<false>(c->dim);
+    hipError_t e = hipLaunchKernel(split, dim3((unsigned)workgroups()), dim3(T), argv, 0, (hipStream_t)stream);
+    if (e == hipSuccess)
+        e = hipLaunchKernel(reinterpret_cast<const void*>(&attn_join_kernel), dim3((unsigned)(b * q_heads)), dim3(256),
+                            argv, 0, (hipStream_t)stream);
     if (e != hipSuccess) {
         woq::set_hip_error((int)e);
         return WOQ_EHIP;
