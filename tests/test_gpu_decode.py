@@ -345,10 +345,13 @@ def check_attention(c, q_heads, lens, seed=0, window=0, softcap=0.0, scale=None,
     (8, 64, 128, 16), (8, 16, 256, 64), (8, 32, 128, 48), (12, 12, 64, 16), (5, 20, 96, 32), (1, 16, 128, 128),
     (1, 40, 64, 16), (2, 6, 80, 16), (1, 1, 16, 16), (1, 17, 256, 16), (3, 3, 240, 32), (2, 66, 48, 16), (4, 28, 128, 256)])
 def test_attention_head_layouts(gpu_lib, int8, heads, q_heads, dim, page):
+    """Over tables of just the pages needed and over wide ones: a short table's
+    rows are a workgroup's whole, a long one's are divided."""
     case("attention", int8, heads, q_heads, dim, page)
     lens = [300, 1, 0, 15, 16, 17, 31, 32, 33, 127, 128, 129, 255]
     c = Cache(sum(-(-n // page) for n in lens) + 2, heads, page, dim, int8, seed=heads)
     check_attention(c, q_heads, lens, seed=dim)
+    check_attention(c, q_heads, lens, seed=dim, width=2000 // page)
 
 
 @pytest.mark.parametrize("int8", [True, False])
@@ -360,11 +363,14 @@ def test_attention_batches(gpu_lib, int8, b):
     case("attention batch", int8, b)
     c = Cache(int(sum(-(-lens // 16))) + 1, 2, 16, 64, int8, seed=b)
     check_attention(c, 8, lens, seed=b)
+    check_attention(c, 8, lens, seed=b, width=100)
 
 
 @pytest.mark.parametrize("int8,heads,q_heads,dim,page,lens", [
     (True, 8, 64, 128, 64, [5000]), (False, 2, 4, 256, 48, [6001, 3]), (True, 1, 8, 128, 16, [30001]),
-    (True, 2, 16, 64, 256, [9000, 0, 1, 12000, 77]), (False, 1, 3, 80, 32, [20011])])
+    (True, 2, 16, 64, 256, [9000, 0, 1, 12000, 77]), (False, 1, 3, 80, 32, [20011]),
+    (True, 2, 2, 64, 16, [0] * 40 + [700] + [0] * 300 + [3, 40] * 60 + [0] * 40),
+    (False, 3, 60, 16, 16, [2000, 1, 0, 5000]), (True, 8, 128, 256, 16, [1000, 3000])])
 def test_attention_long(gpu_lib, int8, heads, q_heads, dim, page, lens):
     case("attention long", int8, heads, q_heads, dim, page, lens)
     c = Cache(sum(-(-n // page) for n in lens) + 1, heads, page, dim, int8, seed=7)
@@ -391,6 +397,9 @@ def test_attention_window(gpu_lib, int8, window):
         pages[r, :max(0, n - window) // page] = 2 ** 31 - 1
     c.upload()
     check_attention(c, 4, lens, seed=window, window=window, pages=pages)
+    wide = np.full((len(lens), 77), -1, np.int32)
+    wide[:, :pages.shape[1]] = pages
+    check_attention(c, 4, lens, seed=window, window=window, pages=wide)
 
 
 @pytest.mark.parametrize("int8", [True, False])
@@ -398,10 +407,10 @@ def test_attention_does_not_see_past_the_end(gpu_lib, int8):
     """Poison behind the last token of every row, in its page and in others."""
     lens = [1, 5, 16, 20, 31, 33, 64, 100, 250]
     rng = np.random.default_rng(1)
-    for page in (16, 64):
+    for page, more in ((16, 3), (64, 3), (16, 40)):
         c = Cache(sum(-(-n // page) for n in lens) + 1, 2, page, 128, int8, seed=6, poison=True)
         good = Cache(c.shape[0], 2, page, 128, int8, seed=6)
-        pages = tables(rng, c, lens, width=-(-250 // page) + 3)
+        pages = tables(rng, c, lens, width=-(-250 // page) + more)
         for r, n in enumerate(lens):
             for t in range(n):
                 for a in ("k", "v", "ks", "vs"):
@@ -422,8 +431,10 @@ def test_attention_pages_that_are_not_there(gpu_lib, int8):
     pages[2] = -7                                        # nothing left: zeros
     pages[3, 0] = 50
     pages[4, 1:5] = -1
-    got = check_attention(c, 6, lens, pages=pages)
-    assert not got[2].any() and not got[3].any()
+    for more in (0, 60):
+        wide = np.concatenate([pages, np.full((5, more), 3, np.int32)], 1)
+        got = check_attention(c, 6, lens, pages=wide)
+        assert not got[2].any() and not got[3].any()
 
 
 def test_attention_lengths_outside_the_table(gpu_lib):

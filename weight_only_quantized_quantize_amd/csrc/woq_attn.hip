@@ -29,8 +29,9 @@ struct AttnArgs {
     const int32_t* pages;
     const int32_t* lens;
     uint16_t* y;
-    int64_t* head;            // workspace: positions of a workgroup, then the units before every row and of all
-    float* sums;              // [2 * workgroups][rows of a tile][dim]
+    int4* cuts;               // workspace, of every workgroup: row, key head and tile, and how many parts the span
+                              // has that it begins and others go on with (0: there is none)
+    float* sums;              // [2 * workgroups][heads of a tile][dim]
     float* stats;             // [2 * workgroups][16][2]: the reference of the weights, their sum
     int64_t ldq, ldpages, ldy, n_pages, capacity;
     float scale, softcap;
@@ -86,25 +87,62 @@ __device__ __forceinline__ h8 pack8(h2 a, h2 b, h2 c, h2 d) {
     return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// One segment of one row, key head and tile of up to 16 query heads: units u0 ..
-// u1 - 1, divided among the waves.
-template <int DP, bool INT8, bool EXACT>
-__global__ __launch_bounds__(T) void attn_split_kernel(AttnArgs a) {
+// The parts that the waves of a workgroup leave of spans they do not hold whole: the
+// first and the last of each, in order.
+template <int N>
+struct Parts {
+    int row[N], head[N];                      // row -1: none; key head and tile
+    int begins[N], ends[N];                   // whether the part holds the span's first and last unit
+    int64_t stop[N];                          // the position behind the span
+    float ref[N][16], sum[N][16];
+};
+
+// Outputs of one span (or part of one): lane (g, m) has channels E (4 g + i) + e of
+// head m in acc[e][i].
+template <int E>
+__device__ __forceinline__ void store_lane(uint16_t* out, const f4 (&acc)[E], float inv, int g, int dim) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int d = E * (4 * g + i);
+        if (d >= dim) continue;
+        uint32_t w[E / 2];
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e)
+            w[e] = (uint32_t)f_to_h(acc[2 * e][i] * inv) | (uint32_t)f_to_h(acc[2 * e + 1][i] * inv) << 16;
+        if constexpr (E == 4) {
+            *(__attribute__((address_space(1))) u32x2*)(out + d) = u32x2{w[0], w[1]};
+        } else {
+#pragma unroll
+            for (int e = 0; e < E / 2; e += 4)
+                gstore_u4(reinterpret_cast<uint4*>(out + d + 2 * e), make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]));
+        }
+    }
+}
+
+// All positions (row, key head, tile of 16 query heads, unit) in order, an equal
+// count of them to every workgroup and in it to every wave (FLAT); or a span, all
+// units of a row, head and tile, to every workgroup.  What a wave holds of a span that
+// it does not hold whole goes through LDS to its neighbours, and of a span that the
+// workgroup does not hold whole through the workspace to the joining launch.
+template <int DP, bool INT8, bool EXACT, int WAVES, bool FLAT>
+__global__ __launch_bounds__(64 * WAVES) void attn_split_kernel(AttnArgs a) {
     using Mem = Tile<DP, INT8>;
-    constexpr int E = Mem::E, NK = Mem::NK, WV = Mem::WV, SIZE = INT8 ? 1 : 2;
-    constexpr int EC = E < 8 ? E : 8, ROW = 16 * EC + 4;       // channels of a lane joined at a time
-    __shared__ __align__(16) float join[WAVES * 16 * ROW];
-    __shared__ float join_m[WAVES][16], join_l[WAVES][16];
-    __shared__ int64_t scan[WAVES], found[2];
+    constexpr int T = 64 * WAVES, E = Mem::E, NK = Mem::NK, WV = Mem::WV, SIZE = INT8 ? 1 : 2;
+    constexpr int PARTS = FLAT ? 2 * WAVES : WAVES;
+    constexpr int ROW = DP + 4;               // floats of a head in LDS: 16 heads in different banks
+    extern __shared__ __align__(16) float join[];              // [PARTS][per_tile][ROW]
+    __shared__ Parts<PARTS> parts;
+    __shared__ int64_t scan[WAVES], found[WAVES][2];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
     const int HH = a.heads * a.tiles;
 
-    // the units before every row; all positions (row, head, tile, unit) in order, an
-    // equal count of them to every workgroup
-    int64_t mine = 0, before = 0, total = 0;
-    const int each = (a.b + T - 1) / T, lo = min(a.b, tid * each), hi = min(a.b, lo + each);
-    for (int r = lo; r < hi; ++r) mine += span_of(a, r).units;
-    if (a.b > 1) {
+    int64_t pos, end, base, per = 0;          // this wave's positions; where its row's begin
+    int r, hh = 0, ub = 0;                    // its row, key head and tile, and first unit there
+    Span sp;
+    if constexpr (FLAT) {
+        int64_t mine = 0, before = 0, total = 0;
+        const int each = (a.b + T - 1) / T, lo = min(a.b, tid * each), hi = min(a.b, lo + each);
+        for (int i = lo; i < hi; ++i) mine += span_of(a, i).units;
         int64_t s = mine;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -119,45 +157,54 @@ __global__ __launch_bounds__(T) void attn_split_kernel(AttnArgs a) {
             if (w < wave) before += scan[w];
             total += scan[w];
         }
-    } else {
-        total = __shfl(span_of(a, 0).units, 0);
-    }
-    const int64_t positions = total * HH;
-    const int64_t per = max((int64_t)WAVES, (positions + gridDim.x - 1) / gridDim.x);
-    if (blockIdx.x == 0) {
-        int64_t at = before;
-        for (int r = lo; r < hi; ++r) {
-            *gptr(a.head + 1 + r) = at;
-            at += span_of(a, r).units;
+        const int64_t positions = total * HH;
+        per = max((int64_t)WAVES, (positions + gridDim.x - 1) / gridDim.x);
+        const int64_t first = blockIdx.x * per, last = min(positions, first + per);
+        if (first >= last) {
+            if (tid == 0) a.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+            return;
         }
-        if (tid == 0) {
-            *gptr(a.head) = per;
-            *gptr(a.head + 1 + a.b) = total;
-        }
-    }
-    int64_t pos = blockIdx.x * per;
-    const int64_t begin = pos, end = min(positions, pos + per);
-    if (pos >= end) return;
-    if (a.b > 1) {
-        if (before * HH <= pos && pos < (before + mine) * HH) {
+        const int64_t share = (last - first + WAVES - 1) / WAVES;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const int64_t p = first + w * share;
+            if (p >= last || p < before * HH || p >= (before + mine) * HH) continue;
             int64_t at = before;
-            int r = lo;
-            for (; r < hi; ++r) {
-                const int n = span_of(a, r).units;
-                if (pos < (at + n) * HH) break;
+            int i = lo;
+            for (; i < hi - 1; ++i) {
+                const int n = span_of(a, i).units;
+                if (p < (at + n) * HH) break;
                 at += n;
             }
-            found[0] = r, found[1] = at;
+            found[w][0] = i, found[w][1] = at;
         }
         __syncthreads();
-    } else if (tid == 0) {
-        found[0] = found[1] = 0;
+        pos = first + wave * share;
+        end = min(last, pos + share);
+        r = pos < end ? __builtin_amdgcn_readfirstlane((int)found[wave][0]) : 0;
+        base = pos < end ? found[wave][1] * HH : 0;
+        sp = span_of(a, r);
+        if (pos < end) {
+            hh = (int)((pos - base) / sp.units);
+            ub = (int)(pos - base - (int64_t)hh * sp.units);
+        }
+    } else {
+        r = blockIdx.x / HH;
+        sp = span_of(a, r);
+        hh = blockIdx.x - r * HH;
+        const int share = (sp.units + WAVES - 1) / WAVES;
+        if (sp.units == 0) {
+            const int h = hh / a.tiles, tile = hh - h * a.tiles, n = min(16, a.group - 16 * tile) * a.dim;
+            uint16_t* out = a.y + r * a.ldy + (int64_t)(h * a.group + 16 * tile) * a.dim;
+            for (int d = tid; d < n; d += T) *gptr(out + d) = 0;
+            return;
+        }
+        base = 0;
+        ub = min(sp.units, wave * share);
+        pos = ub;
+        end = min(sp.units, ub + share);
     }
-    if (a.b == 1) __syncthreads();
-    int r = (int)found[0];
-    int64_t base = found[1] * HH;
-    r = __builtin_amdgcn_readfirstlane(r);
-    Span sp = span_of(a, r);
+    if (lane < PARTS / WAVES) parts.row[PARTS / WAVES * wave + lane] = -1;
 
     // where a lane's pieces of a sixteen stand in bytes; channels past dim are read
     // from the row's start and meet a query of zero
@@ -174,15 +221,12 @@ __global__ __launch_bounds__(T) void attn_split_kernel(AttnArgs a) {
     for (int t = 0; t < 4; ++t) vo[t] = (uint32_t)((4 * g + t) * dim + (EXACT || E * m < dim ? E * m : 0)) * SIZE;
     const int spp = a.page >> 4;              // sixteens of a page
 
-    while (pos < end) {
-        const int64_t rel = pos - base;
-        const int hh = (int)(rel / sp.units), u0 = (int)(rel - (int64_t)hh * sp.units);
-        const int u1 = (int)min((int64_t)sp.units, u0 + (end - pos));
+    int part = 0;
+    for (; pos < end; ++hh, ub = 0) {
+        const int ue = (int)min((int64_t)sp.units, ub + (end - pos));
         const int h = hh / a.tiles, tile = hh - h * a.tiles;
         const int heads = min(16, a.group - 16 * tile);          // query heads of this tile
         const int q0 = h * a.group + 16 * tile;
-        const int share = (u1 - u0 + WAVES - 1) / WAVES;
-        const int ub = min(u1, u0 + wave * share), ue = min(u1, ub + share);
 
         h8 q[DP / 32];
         {
@@ -377,159 +421,179 @@ __global__ __launch_bounds__(T) void attn_split_kernel(AttnArgs a) {
             if (u + 1 < ue) load_v();
         }
 
-        // join the waves
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
-        if (g == 0) {
-            join_m[wave][m] = top;
-            join_l[wave][m] = sum;
-        }
-        __syncthreads();
-        float all = join_m[0][m];
-#pragma unroll
-        for (int w = 1; w < WAVES; ++w) all = fmaxf(all, join_m[w][m]);
-        const float keep = __builtin_amdgcn_exp2f(top - (all == NONE ? 0.0f : all));
-        const int hq = tid >> 4, piece = tid & 15;               // of the joined tile: head, lane's channels
-        float ref = join_m[0][hq], l = 0.0f;
-#pragma unroll
-        for (int w = 1; w < WAVES; ++w) ref = fmaxf(ref, join_m[w][hq]);
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w)
-            l += join_l[w][hq] * __builtin_amdgcn_exp2f(join_m[w][hq] - (ref == NONE ? 0.0f : ref));
-        const bool complete = u0 == 0 && u1 == sp.units;
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (pos != begin);
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-        for (int c = 0; c < E / EC; ++c) {
-            if (c) __syncthreads();
+        if (ub == 0 && ue == sp.units) {
+            if (m < heads)
+                store_lane<E>(a.y + r * a.ldy + (int64_t)(q0 + m) * dim, acc, sum == 0.0f ? 0.0f : 1.0f / sum, g, dim);
+        } else {
+            const int at = PARTS / WAVES * wave + part++;
+            if (lane == 0) {
+                parts.row[at] = r, parts.head[at] = hh;
+                parts.begins[at] = ub == 0, parts.ends[at] = ue == sp.units;
+                parts.stop[at] = base + (int64_t)(hh + 1) * sp.units;
+            }
+            if (g == 0) parts.ref[at][m] = top, parts.sum[at][m] = sum;
             if (m < heads) {
+                float* o = join + (at * a.per_tile + m) * ROW + 4 * E * g;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float* o = join + (wave * 16 + m) * ROW + (4 * g + i) * EC;
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int e = 0; e < EC; e += 4)
-                        *reinterpret_cast<f4*>(o + e) = f4{acc[EC * c + e][i] * keep, acc[EC * c + e + 1][i] * keep,
-                                                           acc[EC * c + e + 2][i] * keep, acc[EC * c + e + 3][i] * keep};
-                }
-            }
-            __syncthreads();
-            const int d = E * piece + EC * c;
-            if (hq < heads && d < dim) {
-                f4 o[EC / 4];
-#pragma unroll
-                for (int e = 0; e < EC / 4; ++e) {
-                    o[e] = f4{0, 0, 0, 0};
-#pragma unroll
-                    for (int w = 0; w < WAVES; ++w)
-                        o[e] += *reinterpret_cast<const f4*>(join + (w * 16 + hq) * ROW + piece * EC + 4 * e);
-                }
-                if (complete) {
-                    uint16_t* out = a.y + r * a.ldy + (int64_t)(q0 + hq) * dim + d;
-#pragma unroll
-                    for (int e = 0; e < EC / 4; ++e) {
-                        const uint2 p = {(uint32_t)f_to_h(o[e][0] * inv) | (uint32_t)f_to_h(o[e][1] * inv) << 16,
-                                         (uint32_t)f_to_h(o[e][2] * inv) | (uint32_t)f_to_h(o[e][3] * inv) << 16};
-                        *(__attribute__((address_space(1))) u32x2*)(out + 4 * e) = u32x2{p.x, p.y};
-                    }
-                } else {
-                    float* out = a.sums + (slot * a.per_tile + hq) * dim + d;
-#pragma unroll
-                    for (int e = 0; e < EC / 4; ++e) *(__attribute__((address_space(1))) f4*)(out + 4 * e) = o[e];
-                }
+                    for (int e = 0; e < E; e += 4)
+                        *reinterpret_cast<f4*>(o + E * i + e) = f4{acc[e][i], acc[e + 1][i], acc[e + 2][i], acc[e + 3][i]};
             }
         }
-        if (!complete && piece == 0 && hq < heads) {
-            *gptr(a.stats + (slot * 16 + hq) * 2) = ref;
-            *gptr(a.stats + (slot * 16 + hq) * 2 + 1) = l;
-        }
-        __syncthreads();                      // the next segment writes the same memory
-
-        pos += u1 - u0;
-        if (pos < end && pos == base + (int64_t)sp.units * HH) {
+        pos += ue - ub;
+        if (FLAT && pos < end && hh == HH - 1) {
             base = pos;
+            hh = -1;
             do {
                 ++r;
                 sp = span_of(a, r);
             } while (sp.units == 0);
         }
     }
+
+    // the parts of one span after another, an output or a part of the workgroup's;
+    // lane k looks at part k
+    __syncthreads();
+    int4 cut = make_int4(0, 0, 0, 0);         // the span that this workgroup begins and others end
+    const int at = min(lane, PARTS - 1), row_k = parts.row[at], head_k = parts.head[at];
+    uint64_t rest = __ballot(lane < PARTS && row_k >= 0);
+    while (rest) {
+        const int k0 = __builtin_ctzll(rest);
+        const int row = __builtin_amdgcn_readlane(row_k, k0), hh = __builtin_amdgcn_readlane(head_k, k0);
+        const uint64_t these = rest & __ballot(row_k == row && head_k == hh);
+        rest &= ~these;
+        const int h = hh / a.tiles, tile = hh - h * a.tiles, heads = min(16, a.group - 16 * tile);
+        const bool begins = parts.begins[k0], ends = parts.ends[63 - __builtin_clzll(these)];
+        const int64_t slot = 2 * (int64_t)blockIdx.x + begins;
+        if (FLAT && begins && !ends)
+            cut = make_int4(row, hh, (int)((parts.stop[k0] - 1) / per - blockIdx.x) + 1, 0);
+        for (int i = tid; i < heads * (DP / 4); i += T) {
+            const int hq = i / (DP / 4), d = 4 * (i - hq * (DP / 4));
+            if (!EXACT && d >= dim) continue;
+            float ref = NONE, l = 0.0f, refs[PARTS];
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) {
+                refs[k] = these >> k & 1 ? parts.ref[k][hq] : NONE;
+                ref = fmaxf(ref, refs[k]);
+            }
+            const float zero = ref == NONE ? 0.0f : ref;
+            f4 o = {0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) {
+                if (!(these >> k & 1)) continue;
+                const float keep = __builtin_amdgcn_exp2f(refs[k] - zero);
+                l = fmaf(parts.sum[k][hq], keep, l);
+                o += *reinterpret_cast<const f4*>(join + (k * a.per_tile + hq) * ROW + d) * keep;
+            }
+            if (begins && ends) {
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                uint16_t* out = a.y + row * a.ldy + (int64_t)(h * a.group + 16 * tile + hq) * dim + d;
+                *(__attribute__((address_space(1))) u32x2*)out =
+                    u32x2{(uint32_t)f_to_h(o[0] * inv) | (uint32_t)f_to_h(o[1] * inv) << 16,
+                          (uint32_t)f_to_h(o[2] * inv) | (uint32_t)f_to_h(o[3] * inv) << 16};
+            } else {
+                *(__attribute__((address_space(1))) f4*)(a.sums + (slot * a.per_tile + hq) * dim + d) = o;
+                if (d == 0) {
+                    *gptr(a.stats + (slot * 16 + hq) * 2) = ref;
+                    *gptr(a.stats + (slot * 16 + hq) * 2 + 1) = l;
+                }
+            }
+        }
+    }
+    if (FLAT && tid == 0) a.cuts[blockIdx.x] = cut;
 }
 
-// Rows that several workgroups share: their parts in order, each under the power of
-// two of its own; rows that see nothing are zeros.  A workgroup for every row and
-// query head, sixteen parts at a time.
+// The span that workgroup x of the split began and others went on with, its head y:
+// their parts in order, each under the power of two of its own.  And the rows that see
+// nothing, which are zeros.
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-    __shared__ float red[16][WOQ_CACHE_MAX_DIM + 4], red_l[16];
-    const int tid = threadIdx.x, part = tid >> 4, piece = tid & 15;
-    const int q_heads = a.heads * a.group, r = blockIdx.x / q_heads, hq = blockIdx.x - r * q_heads;
-    const int h = hq / a.group, in = hq - h * a.group, tile = in >> 4, row = in & 15;
-    const int64_t per = *gptr(a.head), first = *gptr(a.head + 1 + r), units = *gptr(a.head + 2 + r) - first;
-    uint16_t* out = a.y + r * a.ldy + (int64_t)hq * a.dim;
-    if (units == 0) {
-        for (int d = tid; d < a.dim; d += 256) *gptr(out + d) = 0;
-        return;
+    __shared__ __align__(16) float red[16][WOQ_CACHE_MAX_DIM];
+    __shared__ float red_l[16];
+    const int tid = threadIdx.x;
+    if (blockIdx.y == 0) {
+        const int n = a.heads * a.group * a.dim;
+        for (int r = blockIdx.x; r < a.b; r += gridDim.x) {
+            if (span_of(a, r).units) continue;
+            for (int d = tid; d < n; d += 256) *gptr(a.y + r * a.ldy + d) = 0;
+        }
     }
-    const int64_t p0 = first * (a.heads * a.tiles) + (int64_t)(h * a.tiles + tile) * units, p1 = p0 + units - 1;
-    const int64_t w0 = p0 / per, w1 = p1 / per;
-    if (w0 == w1) return;
-    // the first workgroup's part is its last segment, the others' their first
-    auto slot = [&](int64_t w) { return 2 * w + (w == w0 && w * per < p0); };
+    const int4 cut = a.cuts[blockIdx.x];
+    if (cut.z == 0) return;
+    const int h = cut.y / a.tiles, tile = cut.y - h * a.tiles, hq = blockIdx.y;
+    if (hq >= min(16, a.group - 16 * tile)) return;
+    // four channels to a thread, every 4th, 8th or 16th part to a wave or part of one
+    const int lanes = a.dim <= 64 ? 16 : a.dim <= 128 ? 32 : 64, parts = 256 / lanes;
+    const int part = tid / lanes, d = 4 * (tid - part * lanes);
+    // the first workgroup's part is its second, the others' their first
+    auto slot = [&](int i) { return 2 * ((int64_t)blockIdx.x + i) + (i == 0); };
     float ref = NONE;
-    for (int64_t w = w0; w <= w1; ++w) ref = fmaxf(ref, *gptr(a.stats + (slot(w) * 16 + row) * 2));
-    const float zero = ref == NONE ? 0.0f : ref;
-    float l = 0.0f, o[WOQ_CACHE_MAX_DIM / 16] = {};
-    const int e = a.dim / 16;                 // channels of a thread
-    for (int64_t w = w0 + part; w <= w1; w += 16) {
-        const float* st = a.stats + (slot(w) * 16 + row) * 2;
-        const float keep = __builtin_amdgcn_exp2f(*gptr(st) - zero);
-        const float* s = a.sums + (slot(w) * a.per_tile + row) * a.dim + piece * e;
-        l = fmaf(*gptr(st + 1), keep, l);
+    for (int i = tid & 63; i < cut.z; i += 64) ref = fmaxf(ref, *gptr(a.stats + (slot(i) * 16 + hq) * 2));
 #pragma unroll
-        for (int i = 0; i < WOQ_CACHE_MAX_DIM / 16; ++i)
-            if (i < e) o[i] = fmaf(*gptr(s + i), keep, o[i]);
+    for (int s = 1; s < 64; s <<= 1) ref = fmaxf(ref, __shfl_xor(ref, s));
+    if (ref == NONE) ref = 0.0f;
+    float l = 0.0f;
+    f4 o = {0, 0, 0, 0};
+    if (d < a.dim) {
+#pragma unroll 4
+        for (int i = part; i < cut.z; i += parts) {
+            const float* st = a.stats + (slot(i) * 16 + hq) * 2;
+            const float keep = __builtin_amdgcn_exp2f(*gptr(st) - ref);
+            l = fmaf(*gptr(st + 1), keep, l);
+            o += *(__attribute__((address_space(1))) const f4*)(a.sums + (slot(i) * a.per_tile + hq) * a.dim + d) * keep;
+        }
+        *reinterpret_cast<f4*>(&red[part][d]) = o;
+        if (d == 0) red_l[part] = l;
     }
-#pragma unroll
-    for (int i = 0; i < WOQ_CACHE_MAX_DIM / 16; ++i)
-        if (i < e) red[part][piece * e + i] = o[i];
-    if (piece == 0) red_l[part] = l;
     __syncthreads();
     if (tid >= a.dim) return;
     float s = 0.0f, t = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < parts; ++i) {
         s += red[i][tid];
         t += red_l[i];
     }
-    *gptr(out + tid) = f_to_h(t == 0.0f ? 0.0f : s / t);
+    *gptr(a.y + cut.x * a.ldy + (int64_t)(h * a.group + 16 * tile + hq) * a.dim + tid) = f_to_h(t == 0.0f ? 0.0f : s / t);
 }
 
 // Workgroups of a split: as many as keep two on a compute unit.
 int workgroups() { return 2 * woq::compute_units(); }
 
+// Where the capacity is no more than this, a workgroup takes a span whole and there is nothing to join.
+constexpr int64_t DIRECT = 512;
+
 struct Layout {
     int64_t sums, stats, bytes;
     int tiles, per_tile;
 };
-Layout layout(const woq_cache* c, int32_t q_heads, int64_t b) {
+Layout layout(const woq_cache* c, int32_t q_heads) {
     Layout l;
     const int group = q_heads / c->heads, n = 2 * workgroups();
     l.tiles = (group + 15) / 16;
     l.per_tile = std::min(group, 16);
-    l.sums = woq::round_up((b + 2) * 8, 16);
+    l.sums = workgroups() * 16;
     l.stats = l.sums + (int64_t)n * l.per_tile * c->dim * 4;
     l.bytes = l.stats + (int64_t)n * 16 * 2 * 4;
     return l;
 }
 
+struct Kernel {
+    const void* f;
+    int waves, dim;           // dim: that of its registers
+};
 template <int DP, bool INT8>
-const void* split_kernel(int dim) {
-    return dim == DP ? reinterpret_cast<const void*>(&attn_split_kernel<DP, INT8, true>)
-                     : reinterpret_cast<const void*>(&attn_split_kernel<DP, INT8, false>);
+Kernel split_kernel(int dim, bool flat) {
+#define WOQ_ATTN(E, W, F) Kernel{reinterpret_cast<const void*>(&attn_split_kernel<DP, INT8, E, W, F>), W, DP}
+    if (flat) return dim == DP ? WOQ_ATTN(true, 4, true) : WOQ_ATTN(false, 4, true);
+    return dim == DP ? WOQ_ATTN(true, 8, false) : WOQ_ATTN(false, 8, false);
+#undef WOQ_ATTN
 }
 template <bool INT8>
-const void* split_kernel(int dim) {
-    return dim <= 64 ? split_kernel<64, INT8>(dim) : dim <= 128 ? split_kernel<128, INT8>(dim)
-                                                                : split_kernel<256, INT8>(dim);
+Kernel split_kernel(int dim, bool flat) {
+    return dim <= 64    ? split_kernel<64, INT8>(dim, flat)
+           : dim <= 128 ? split_kernel<128, INT8>(dim, flat)
+                        : split_kernel<256, INT8>(dim, flat);
 }
 
 bool half_rows_ok(const void* p, int64_t ld) { return woq::aligned16(p) && (ld & 7) == 0; }
@@ -568,7 +632,7 @@ extern "C" int64_t woq_attn_decode_workspace(const woq_cache* c, int32_t q_heads
     if (rc == WOQ_EINVAL || b < 0 || q_heads < 1 || q_heads % c->heads) return WOQ_EINVAL;
     if (rc) return rc;
     if (q_heads > WOQ_ATTN_MAX_HEADS || b > WOQ_ATTN_MAX_ROWS || b * q_heads >= 1 << 24) return WOQ_EUNSUPPORTED;
-    return layout(c, q_heads, b).bytes;
+    return layout(c, q_heads).bytes;
 }
 
 extern "C" int woq_attn_decode(const woq_cache* c, const uint16_t* q, int64_t ldq, int32_t q_heads,
@@ -600,19 +664,25 @@ extern "C" int woq_attn_decode(const woq_cache* c, const uint16_t* q, int64_t ld
     a.dim = c->dim;
     a.window = window;
     a.b = (int)b;
-    const Layout l = layout(c, q_heads, b);
+    const Layout l = layout(c, q_heads);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    a.head = reinterpret_cast<int64_t*>(ws);
+    a.cuts = reinterpret_cast<int4*>(ws);
     a.sums = reinterpret_cast<float*>(ws + l.sums);
     a.stats = reinterpret_cast<float*>(ws + l.stats);
     a.tiles = l.tiles;
     a.per_tile = l.per_tile;
     void* argv[] = {&a};
-    const void* split = c->fmt == WOQ_CACHE_INT8 ? split_kernel<true>(c->dim) : split_kernel<false>(c->dim);
-    hipError_t e = hipLaunchKernel(split, dim3((unsigned)workgroups()), dim3(T), argv, 0, (hipStream_t)stream);
-    if (e == hipSuccess)
-        e = hipLaunchKernel(reinterpret_cast<const void*>(&attn_join_kernel), dim3((unsigned)(b * q_heads)), dim3(256),
-                            argv, 0, (hipStream_t)stream);
+    hipStream_t s = (hipStream_t)stream;
+    const bool flat = a.capacity > DIRECT;
+    const Kernel k = c->fmt == WOQ_CACHE_INT8 ? split_kernel<true>(c->dim, flat) : split_kernel<false>(c->dim, flat);
+    const size_t lds = (size_t)(flat ? 2 : 1) * k.waves * l.per_tile * (k.dim + 4) * 4;
+    const unsigned grid = flat ? (unsigned)workgroups() : (unsigned)(b * c->heads * l.tiles);
+    hipError_t e = hipSuccess;
+    if (lds > 64 << 10) e = hipFuncSetAttribute(k.f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e == hipSuccess) e = hipLaunchKernel(k.f, dim3(grid), dim3(64 * k.waves), argv, lds, s);
+    if (e == hipSuccess && flat)
+        e = hipLaunchKernel(reinterpret_cast<const void*>(&attn_join_kernel), dim3(grid, l.per_tile),
+                            dim3(256), argv, 0, s);
     if (e != hipSuccess) {
         woq::set_hip_error((int)e);
         return WOQ_EHIP;
