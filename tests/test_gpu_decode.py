@@ -16,7 +16,11 @@ SUB = 2^-25 half the spacing of fp16's subnormals.
   argument 2^-22 for the token's scale; the sums of n tokens are at most n / 16 + 96
   roundings long, twice (values and weights): all of them relative to spread =
   sum p |v|.  Weights below 2^-40 of the largest may be lost: n 2^-40 max |v|.
-  The result is rounded to fp16.
+  The result is rounded to fp16.  INT8 bytes u = code + 128 are multiplied as they
+  are and 128 times the factor's sum is taken off in fp32, so the magnitudes that
+  fp32's roundings are relative to are those of u, at most |code| + 128: reach grows by
+  128 max ks sum |q|, and for the sums (not for the weights' rounding, which is the
+  same in both) spread by 128 sum p sv.
 * a token is the definition's, exactly; its share is rounded to fp32 once.
 """
 import numpy as np
@@ -333,9 +337,15 @@ def check_attention(c, q_heads, lens, seed=0, window=0, softcap=0.0, scale=None,
         K, V = c.tokens("k", slots), c.tokens("v", slots)
         ref, mag, reach = O.attend(q[r].reshape(q_heads, D), K, V, scale, softcap)
         m = len(slots)
+        sums = mag
+        if c.int8 and m:
+            ks, sv = (s[slots // c.page, :, slots % c.page].astype(np.float64) for s in (c.ks, c.vs))
+            of = np.arange(q_heads) // (q_heads // c.heads)
+            reach = reach + 128 * abs(scale) * (ks.max(0)[of] * np.abs(q[r].astype(float)).reshape(q_heads, D).sum(1))[:, None]
+            sums = mag + O.attend(q[r].reshape(q_heads, D), K, np.repeat(128 * sv[..., None], D, 2), scale, softcap)[0]
         dz = reach * (D + 8) * U
-        rel = H + 3 * dz + 2.0 ** -19 + 2 * (m / 16 + 96) * U + softcap * 2.0 ** -21
-        tol = mag * rel + np.abs(ref) * H + SUB + (m * 2.0 ** -40 * np.abs(V).max() if m else 0)
+        rel = H + 3 * dz + 2.0 ** -19 + softcap * 2.0 ** -21
+        tol = mag * rel + sums * 2 * (m / 16 + 96) * U + np.abs(ref) * H + SUB + (m * 2.0 ** -40 * np.abs(V).max() if m else 0)
         within(got[r].reshape(q_heads, D), ref, tol, ("row", r, "of", b, "len", int(lens[r])))
     return got
 

@@ -15,10 +15,29 @@ namespace {
 using namespace woqk;
 
 constexpr int WAVES = 4, T = 64 * WAVES;
-constexpr float LOG2E = 1.4426950408889634f;
 constexpr float NONE = -__builtin_huge_valf();
-constexpr float LEAST = 0x1p-60f;   // a smaller scale of values counts as this: its values are zero in fp16 either way
-constexpr float TOP = 15.0f;        // the largest weight is 2^15, so that fp16 holds weights 2^-40 of it
+constexpr int TOP = 15;             // weights are at most 2^15, so that fp16 holds weights 2^-40 of that
+
+// A cache's bytes u = code + 128 enter the matrix instructions as they are: u in the
+// low byte of an fp16 number is the subnormal u 2^-24, exactly, which one v_perm_b32
+// makes of two bytes, anywhere in two words.  The 128 leaves as a product of the same
+// operand with HALF in its place: once a segment for the keys, and with the weights as
+// one more row of sixteen channels for the values.
+constexpr uint32_t HALF = 0x00800080u;                        // 128 2^-24, twice
+constexpr float STEP = 0x1p24f;
+
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// The largest of the four lanes m, m + 16, m + 32 and m + 48, in all of them.
+__device__ __forceinline__ float max_over_rows(float v) {
+    const uint32_t x = __float_as_uint(v);
+    const auto p = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    const float a = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    const uint32_t y = __float_as_uint(a);
+    const auto s = __builtin_amdgcn_permlane32_swap(y, y, false, false);
+    return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
 
 struct AttnArgs {
     const uint8_t* k;
@@ -34,7 +53,7 @@ struct AttnArgs {
     float* sums;              // [2 * workgroups][heads of a tile][dim]
     float* stats;             // [2 * workgroups][16][2]: the reference of the weights, their sum
     int64_t ldq, ldpages, ldy, n_pages, capacity;
-    float scale, softcap;
+    float factor, cap;        // of the scores in powers of two, see the launch
     int heads, group, page, dim, window, b, tiles, per_tile;
 };
 
@@ -125,7 +144,13 @@ __device__ __forceinline__ void store_lane(uint16_t* out, const f4 (&acc)[E], fl
 // it does not hold whole goes through LDS to its neighbours, and of a span that the
 // workgroup does not hold whole through the workspace to the joining launch.
 template <int DP, bool INT8, bool EXACT, int WAVES, bool FLAT>
-__global__ __launch_bounds__(64 * WAVES) void attn_split_kernel(AttnArgs a) {
+#ifndef OCC
+#define OCC 2
+#endif
+#ifndef PERCU
+#define PERCU 2
+#endif
+__global__ __launch_bounds__(64 * WAVES, DP == 256 && !INT8 ? 1 : DP == 256 ? 2 : OCC) void attn_split_kernel(AttnArgs a) {
     using Mem = Tile<DP, INT8>;
     constexpr int T = 64 * WAVES, E = Mem::E, NK = Mem::NK, WV = Mem::WV, SIZE = INT8 ? 1 : 2;
     constexpr int PARTS = FLAT ? 2 * WAVES : WAVES;
@@ -133,8 +158,8 @@ __global__ __launch_bounds__(64 * WAVES) void attn_split_kernel(AttnArgs a) {
     extern __shared__ __align__(16) float join[];              // [PARTS][per_tile][ROW]
     __shared__ Parts<PARTS> parts;
     __shared__ int64_t scan[WAVES], found[WAVES][2];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
-    const int HH = a.heads * a.tiles;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int m = lane & 15, g = lane >> 4, HH = a.heads * a.tiles;
 
     int64_t pos, end, base, per = 0;          // this wave's positions; where its row's begin
     int r, hh = 0, ub = 0;                    // its row, key head and tile, and first unit there
@@ -185,8 +210,8 @@ __global__ __launch_bounds__(64 * WAVES) void attn_split_kernel(AttnArgs a) {
         base = pos < end ? found[wave][1] * HH : 0;
         sp = span_of(a, r);
         if (pos < end) {
-            hh = (int)((pos - base) / sp.units);
-            ub = (int)(pos - base - (int64_t)hh * sp.units);
+            hh = __builtin_amdgcn_readfirstlane((int)((pos - base) / sp.units));
+            ub = __builtin_amdgcn_readfirstlane((int)(pos - base - (int64_t)hh * sp.units));
         }
     } else {
         r = blockIdx.x / HH;
@@ -219,6 +244,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_split_kernel(AttnArgs a) {
     }
 #pragma unroll
     for (int t = 0; t < 4; ++t) vo[t] = (uint32_t)((4 * g + t) * dim + (EXACT || E * m < dim ? E * m : 0)) * SIZE;
+    const uint32_t so = 4 * g;                // scales
     const int spp = a.page >> 4;              // sixteens of a page
 
     int part = 0;
@@ -239,10 +265,17 @@ __global__ __launch_bounds__(64 * WAVES) void attn_split_kernel(AttnArgs a) {
                 q[i] = __builtin_bit_cast(h8, w);
             }
         }
-        f4 acc[E];
+        f4 acc[E], offset = {0, 0, 0, 0}, start = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < E; ++i) acc[i] = f4{0, 0, 0, 0};
+        const h8 half = __builtin_bit_cast(h8, make_uint4(HALF, HALF, HALF, HALF));
+        if constexpr (INT8) {
+#pragma unroll
+            for (int i = 0; i < DP / 32; ++i) start = __builtin_amdgcn_mfma_f32_16x16x32_f16(half, q[i], start, 0, 0, 0);
+            start = -start;
+        }
         float top = NONE, sum = 0.0f;
+        int power = -90;                      // INT8: scales of values are below 2^power
 
         // page of the sixteen sb + lane and its place there; -1 where it is not
         int sb = sp.s0 + 2 * ub, pg = -1, po = 0;
@@ -278,7 +311,8 @@ __global__ __launch_bounds__(64 * WAVES) void attn_split_kernel(AttnArgs a) {
                 const uint8_t* p = a.k + at[j] * dim * SIZE;
 #pragma unroll
                 for (int i = 0; i < NK; ++i) t.k[j][i] = gload_nt(reinterpret_cast<const uint4*>(p + ko[i]));
-                if constexpr (INT8) t.ks[j] = *(__attribute__((address_space(1))) const f4*)(a.ks + at[j] + 4 * g);
+                if constexpr (INT8)
+                    t.ks[j] = *reinterpret_cast<__attribute__((address_space(1))) const f4*>(gptr(a.ks + at[j]) + so);
             }
         };
         auto load_v = [&] {
@@ -287,77 +321,71 @@ __global__ __launch_bounds__(64 * WAVES) void attn_split_kernel(AttnArgs a) {
                 const uint8_t* p = a.v + at[j] * dim * SIZE;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) load_words<WV>(p + vo[i], t.v[4 * j + i]);
-                if constexpr (INT8) t.vs[j] = *(__attribute__((address_space(1))) const f4*)(a.vs + at[j] + 4 * g);
+                if constexpr (INT8)
+                    t.vs[j] = *reinterpret_cast<__attribute__((address_space(1))) const f4*>(gptr(a.vs + at[j]) + so);
             }
         };
 
-        if (ub < ue) {
-            fetch(sb + lane, pg, po);
-            place(ub);
-            load_k();
-            load_v();
-        }
+        fetch(sb + lane, pg, po);
+        place(ub);
+        load_k();
+        load_v();
         for (int u = ub; u < ue; ++u) {
             const int t0 = 16 * (sp.s0 + 2 * u);
             const bool whole = there[0] && there[1] && t0 >= sp.first && t0 + 32 <= sp.len;
+            const bool seen0 = there[0], seen1 = there[1];
             // scores: lane (g, m) gets tokens 4 g .. 4 g + 3 of both sixteens for head m
             float z[8];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                f4 s = {0, 0, 0, 0};
+                f4 s = start;
 #pragma unroll
                 for (int i = 0; i < NK; ++i) {
+                    const uint32_t w[4] = {t.k[j][i].x, t.k[j][i].y, t.k[j][i].z, t.k[j][i].w};
                     if constexpr (INT8) {
-                        const uint32_t w[4] = {t.k[j][i].x, t.k[j][i].y, t.k[j][i].z, t.k[j][i].w};
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            h2 c[4];
-                            int8_pairs(w[2 * e], c[0], c[1]);
-                            int8_pairs(w[2 * e + 1], c[2], c[3]);
-                            s = __builtin_amdgcn_mfma_f32_16x16x32_f16(pack8(c[0], c[1], c[2], c[3]), q[2 * i + e], s, 0, 0, 0);
+                            uint4 c;
+                            c.x = __builtin_amdgcn_perm(w[2 * e], w[2 * e], 0x0c010c00u);
+                            c.y = __builtin_amdgcn_perm(w[2 * e], w[2 * e], 0x0c030c02u);
+                            c.z = __builtin_amdgcn_perm(w[2 * e + 1], w[2 * e + 1], 0x0c010c00u);
+                            c.w = __builtin_amdgcn_perm(w[2 * e + 1], w[2 * e + 1], 0x0c030c02u);
+                            s = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, c), q[2 * i + e], s, 0, 0, 0);
                         }
                     } else {
-                        uint4 w = t.k[j][i];
-                        if (!EXACT && !kin[i]) w = make_uint4(0, 0, 0, 0);
-                        s = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, w), q[i], s, 0, 0, 0);
+                        uint4 c = t.k[j][i];
+                        if (!EXACT && !kin[i]) c = make_uint4(0, 0, 0, 0);
+                        s = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, c), q[i], s, 0, 0, 0);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float x = s[i] * a.scale;
-                    if constexpr (INT8) x *= t.ks[j][i];
-                    if (a.softcap > 0.0f) {
-                        // tanh(x) = 1 - 2 / (1 + e^2x)
-                        const float e2 = __builtin_amdgcn_exp2f(2.0f * LOG2E * x / a.softcap);
-                        x = a.softcap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e2));
-                    }
-                    z[4 * j + i] = x * LOG2E;
+                    z[4 * j + i] = s[i] * a.factor;
+                    if constexpr (INT8) z[4 * j + i] *= t.ks[j][i];
                 }
             }
-            float inv[8];                     // of the values' scales
+            if (a.cap > 0.0f) {
+                // cap tanh(x / cap) = cap (1 - 2 / (1 + e^(2 x / cap))); factor holds 2 log2(e) / cap
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                inv[i] = 1.0f;
-                if constexpr (INT8) {
-                    const float s = fmaxf(t.vs[i >> 2][i & 3], LEAST);
-                    // a scale that is NaN stays one
-                    const float sv = t.vs[i >> 2][i & 3] != t.vs[i >> 2][i & 3] ? t.vs[i >> 2][i & 3] : s;
-                    z[i] += __builtin_amdgcn_logf(sv);
-                    inv[i] = __builtin_amdgcn_rcpf(sv);
-                }
+                for (int i = 0; i < 8; ++i)
+                    z[i] = a.cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z[i])));
+            }
+            float vs[8];                      // of the values' scales
+            if constexpr (INT8) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) vs[i] = t.vs[i >> 2][i & 3];
             }
             if (!whole) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
-                    const bool seen = there[i >> 2] && tok >= sp.first && tok < sp.len;
-                    if (!seen) {
-                        z[i] = NONE;
-                        inv[i] = 0.0f;
-                        if constexpr (!INT8) {
+                    if ((i < 4 ? seen0 : seen1) && tok >= sp.first && tok < sp.len) continue;
+                    z[i] = NONE;
+                    if constexpr (INT8) {
+                        vs[i] = 0.0f;
+                    } else {
 #pragma unroll
-                            for (int w = 0; w < WV; ++w) t.v[i][w] = 0;
-                        }
+                        for (int w = 0; w < WV; ++w) t.v[i][w] = 0;
                     }
                 }
             }
@@ -368,57 +396,62 @@ __global__ __launch_bounds__(64 * WAVES) void attn_split_kernel(AttnArgs a) {
             float most = z[0];
 #pragma unroll
             for (int i = 1; i < 8; ++i) most = fmaxf(most, z[i]);
-            most = fmaxf(most, __shfl_xor(most, 16));
-            most = fmaxf(most, __shfl_xor(most, 32));
+            most = max_over_rows(most);
             if (__any(most > top)) {
                 const float next = fmaxf(top, most), keep = __builtin_amdgcn_exp2f(top - (next == NONE ? 0.0f : next));
                 top = next;
                 sum *= keep;
+                offset *= keep;
 #pragma unroll
                 for (int i = 0; i < E; ++i) acc[i] *= keep;
             }
-            const float ref = (top == NONE ? 0.0f : top) - TOP;
+            if constexpr (INT8) {
+                float large = vs[0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) large = fmaxf(large, vs[i]);
+                if (__any(large >= pow2i(power))) {
+                    large = max_over_rows(large);
+                    const int next = min(110, (int)(__builtin_amdgcn_readfirstlane(__float_as_uint(large)) >> 23) - 126);
+                    const float keep = pow2i(max(-126, power - next));
+                    power = next;
+                    offset *= keep;
+#pragma unroll
+                    for (int i = 0; i < E; ++i) acc[i] *= keep;
+                }
+            }
+            const float ref = (top == NONE ? 0.0f : top) - (INT8 ? 0 : TOP), raise = pow2i(TOP - power);
             f16 w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float e = __builtin_amdgcn_exp2f(z[i] - ref);
-                sum = fmaf(e, inv[i], sum);
-                w[i] = (f16)e;
+                sum += e;
+                w[i] = (f16)(INT8 ? e * (vs[i] * raise) : e);
             }
             const h8 weights = {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
             // sums: rows of the product are the channels E (lane % 16) + i
-            if constexpr (INT8) {
 #pragma unroll
-                for (int c = 0; c < WV; ++c) {
-                    h2 p[4][4];
+            for (int c = 0; c < WV; ++c) {
+                constexpr int N = INT8 ? 4 : 2;               // channels of a word
+                constexpr uint32_t SEL[4] = {INT8 ? 0x0c040c00u : 0x05040100u, INT8 ? 0x0c050c01u : 0x07060302u, 0x0c060c02u,
+                                             0x0c070c03u};
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint32_t e = t.v[2 * x][c], o = t.v[2 * x + 1][c];
-                        int8_pairs(__builtin_amdgcn_perm(o, e, 0x05010400u), p[0][x], p[1][x]);
-                        int8_pairs(__builtin_amdgcn_perm(o, e, 0x07030602u), p[2][x], p[3][x]);
-                    }
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        acc[4 * c + x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pack8(p[x][0], p[x][1], p[x][2], p[x][3]),
-                                                                                weights, acc[4 * c + x], 0, 0, 0);
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < WV; ++c) {
-                    h2 p[2][4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint32_t e = t.v[2 * x][c], o = t.v[2 * x + 1][c];
-                        p[0][x] = as_h2(__builtin_amdgcn_perm(o, e, 0x05040100u));
-                        p[1][x] = as_h2(__builtin_amdgcn_perm(o, e, 0x07060302u));
-                    }
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        acc[2 * c + x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pack8(p[x][0], p[x][1], p[x][2], p[x][3]),
-                                                                                weights, acc[2 * c + x], 0, 0, 0);
+                for (int x = 0; x < N; ++x) {
+                    uint4 v;
+                    v.x = __builtin_amdgcn_perm(t.v[1][c], t.v[0][c], SEL[x]);
+                    v.y = __builtin_amdgcn_perm(t.v[3][c], t.v[2][c], SEL[x]);
+                    v.z = __builtin_amdgcn_perm(t.v[5][c], t.v[4][c], SEL[x]);
+                    v.w = __builtin_amdgcn_perm(t.v[7][c], t.v[6][c], SEL[x]);
+                    acc[N * c + x] =
+                        __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, v), weights, acc[N * c + x], 0, 0, 0);
                 }
             }
+            if constexpr (INT8) offset = __builtin_amdgcn_mfma_f32_16x16x32_f16(half, weights, offset, 0, 0, 0);
             if (u + 1 < ue) load_v();
+        }
+        if constexpr (INT8) {
+            const float unit = pow2i(power - TOP);
+#pragma unroll
+            for (int i = 0; i < E; ++i) acc[i] = (acc[i] - offset) * STEP * unit;
         }
 
         sum += __shfl_xor(sum, 16);
@@ -558,7 +591,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 }
 
 // Workgroups of a split: as many as keep two on a compute unit.
-int workgroups() { return 2 * woq::compute_units(); }
+int workgroups() { return PERCU * woq::compute_units(); }
 
 // Where the capacity is no more than this, a workgroup takes a span whole and there is nothing to join.
 constexpr int64_t DIRECT = 512;
@@ -586,7 +619,8 @@ template <int DP, bool INT8>
 Kernel split_kernel(int dim, bool flat) {
 #define WOQ_ATTN(E, W, F) Kernel{reinterpret_cast<const void*>(&attn_split_kernel<DP, INT8, E, W, F>), W, DP}
     if (flat) return dim == DP ? WOQ_ATTN(true, 4, true) : WOQ_ATTN(false, 4, true);
-    return dim == DP ? WOQ_ATTN(true, 8, false) : WOQ_ATTN(false, 8, false);
+    constexpr int W = DP == 256 ? 4 : 8;
+    return dim == DP ? WOQ_ATTN(true, W, false) : WOQ_ATTN(false, W, false);
 #undef WOQ_ATTN
 }
 template <bool INT8>
@@ -656,8 +690,10 @@ extern "C" int woq_attn_decode(const woq_cache* c, const uint16_t* q, int64_t ld
     a.ldy = ldy;
     a.n_pages = c->n_pages;
     a.capacity = max_pages * c->page;
-    a.scale = scale;
-    a.softcap = softcap;
+    // scores are in units of log2: cap (1 - 2 / (1 + 2^(factor s))) or factor s
+    const double log2e = 1.4426950408889634, step = c->fmt == WOQ_CACHE_INT8 ? STEP : 1.0;
+    a.factor = (float)(step * log2e * scale * (softcap > 0.0f ? 2.0 / softcap : 1.0));
+    a.cap = (float)(log2e * softcap);
     a.heads = c->heads;
     a.group = q_heads / c->heads;
     a.page = c->page;
