@@ -595,8 +595,8 @@ int woq_cache_read(const woq_cache* c, const int32_t* slots, int64_t n, uint16_t
  * stands at offset t % page of page pages[r * ldpages + t / page] (int32 in
  * device memory, max_pages entries used of a row).  A page index outside [0,
  * n_pages) is a page that is not there: its tokens are not seen.  Entries of
- * pages without a visible token are not read, and what stands at tokens that are
- * not seen does not matter (NaN or infinity).  A row that sees nothing gives zeros.
+ * pages without a visible token may hold anything, and so may tokens that are not
+ * seen (NaN or infinity).  A row that sees nothing gives zeros.
  * Several new tokens of one sequence are rows with the same pages and rising
  * lens.  q fp16 [b, ldq] and y fp16 [b, ldy] with q_heads * dim values, 16-byte
  * aligned, leading dimensions multiples of 8; q_heads is a multiple of heads.

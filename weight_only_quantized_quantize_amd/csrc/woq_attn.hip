@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "woq_gemv.h"
 #include "woq_internal.h"
@@ -54,7 +55,7 @@ struct AttnArgs {
     float* stats;             // [2 * workgroups][16][2]: the reference of the weights, their sum
     int64_t ldq, ldpages, ldy, n_pages, capacity;
     float factor, cap;        // of the scores in powers of two, see the launch
-    int heads, group, page, dim, window, b, tiles, per_tile;
+    int heads, group, page, dim, window, b, tiles, per_tile, groups, spread;
 };
 
 // What row r sees: tokens first .. len - 1, in sixteens s0 .. s1 - 1 and units of
@@ -144,13 +145,7 @@ __device__ __forceinline__ void store_lane(uint16_t* out, const f4 (&acc)[E], fl
 // it does not hold whole goes through LDS to its neighbours, and of a span that the
 // workgroup does not hold whole through the workspace to the joining launch.
 template <int DP, bool INT8, bool EXACT, int WAVES, bool FLAT>
-#ifndef OCC
-#define OCC 2
-#endif
-#ifndef PERCU
-#define PERCU 2
-#endif
-__global__ __launch_bounds__(64 * WAVES, DP == 256 && !INT8 ? 1 : DP == 256 ? 2 : OCC) void attn_split_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) void attn_split_kernel(AttnArgs a) {
     using Mem = Tile<DP, INT8>;
     constexpr int T = 64 * WAVES, E = Mem::E, NK = Mem::NK, WV = Mem::WV, SIZE = INT8 ? 1 : 2;
     constexpr int PARTS = FLAT ? 2 * WAVES : WAVES;
@@ -215,19 +210,8 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !INT8 ? 1 : DP == 256 ? 2 
         }
     } else {
         r = blockIdx.x / HH;
-        sp = span_of(a, r);
         hh = blockIdx.x - r * HH;
-        const int share = (sp.units + WAVES - 1) / WAVES;
-        if (sp.units == 0) {
-            const int h = hh / a.tiles, tile = hh - h * a.tiles, n = min(16, a.group - 16 * tile) * a.dim;
-            uint16_t* out = a.y + r * a.ldy + (int64_t)(h * a.group + 16 * tile) * a.dim;
-            for (int d = tid; d < n; d += T) *gptr(out + d) = 0;
-            return;
-        }
-        base = 0;
-        ub = min(sp.units, wave * share);
-        pos = ub;
-        end = min(sp.units, ub + share);
+        base = pos = 0;
     }
     if (lane < PARTS / WAVES) parts.row[PARTS / WAVES * wave + lane] = -1;
 
@@ -246,10 +230,41 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !INT8 ? 1 : DP == 256 ? 2 
     for (int t = 0; t < 4; ++t) vo[t] = (uint32_t)((4 * g + t) * dim + (EXACT || E * m < dim ? E * m : 0)) * SIZE;
     const uint32_t so = 4 * g;                // scales
     const int spp = a.page >> 4;              // sixteens of a page
+    // page of a lane's sixteen s and its place there; -1 where it is not
+    int pg = -1, po = 0;
+    auto fetch = [&](int s, int stop) {
+        pg = -1;
+        po = 0;
+        if (s < stop) {
+            const int p = (int)((uint32_t)s / (uint32_t)spp);
+            pg = *gptr(a.pages + r * a.ldpages + p);
+            po = s - p * spp;
+            if (pg < 0 || pg >= a.n_pages) pg = -1;
+        }
+    };
+    if constexpr (!FLAT) {
+        // unit wave + WAVES i of the span: without a window its pages are asked for before the length is there
+        const int s = 2 * (wave + WAVES * (lane >> 1)) + (lane & 1), stop = (int)(a.capacity >> 4);
+        if (a.window > 0) {
+            sp = span_of(a, r);
+            fetch(sp.s0 + s, stop);
+        } else {
+            fetch(s, stop);
+            sp = span_of(a, r);
+        }
+        if (sp.units == 0) {
+            const int h = hh / a.tiles, tile = hh - h * a.tiles, n = min(16, a.group - 16 * tile) * a.dim;
+            uint16_t* out = a.y + r * a.ldy + (int64_t)(h * a.group + 16 * tile) * a.dim;
+            for (int d = tid; d < n; d += T) *gptr(out + d) = 0;
+            return;
+        }
+        end = wave < sp.units;                // one turn of the loop, or none
+    }
 
     int part = 0;
     for (; pos < end; ++hh, ub = 0) {
-        const int ue = (int)min((int64_t)sp.units, ub + (end - pos));
+        const int ue = FLAT ? (int)min((int64_t)sp.units, ub + (end - pos)) : 0;
+        const int n = FLAT ? ue - ub : (sp.units - wave + WAVES - 1) / WAVES;      // units of this wave here
         const int h = hh / a.tiles, tile = hh - h * a.tiles;
         const int heads = min(16, a.group - 16 * tile);          // query heads of this tile
         const int q0 = h * a.group + 16 * tile;
@@ -277,32 +292,26 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !INT8 ? 1 : DP == 256 ? 2 
         float top = NONE, sum = 0.0f;
         int power = -90;                      // INT8: scales of values are below 2^power
 
-        // page of the sixteen sb + lane and its place there; -1 where it is not
-        int sb = sp.s0 + 2 * ub, pg = -1, po = 0;
-        auto fetch = [&](int s, int& page, int& off) {
-            page = -1;
-            off = 0;
-            if (s < sp.s1) {
-                const int p = (int)((uint32_t)s / (uint32_t)spp);
-                page = *gptr(a.pages + r * a.ldpages + p);
-                off = s - p * spp;
-                if (page < 0 || page >= a.n_pages) page = -1;
-            }
-        };
         Mem t;
         bool there[2];
         int64_t at[2];                        // first token of the two sixteens
-        auto place = [&](int u) {
-            const int s = sp.s0 + 2 * u;
-            if (s - sb >= 64) {
-                sb += 64;
-                fetch(sb + lane, pg, po);
+        int sb = sp.s0 + 2 * ub;              // FLAT: pg and po are of sixteens sb ..
+        if constexpr (FLAT) fetch(sb + lane, sp.s1);
+        auto place = [&](int i) {
+            int l = 2 * i;                    // the lane that holds it
+            if constexpr (FLAT) {
+                l = sp.s0 + 2 * (ub + i) - sb;
+                if (l >= 64) {
+                    sb += 64;
+                    fetch(sb + lane, sp.s1);
+                    l = 0;
+                }
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int p = __builtin_amdgcn_readlane(pg, s - sb + j), o = __builtin_amdgcn_readlane(po, s - sb + j);
+                const int p = __builtin_amdgcn_readlane(pg, l + j), o = __builtin_amdgcn_readlane(po, l + j);
                 there[j] = p >= 0;
-                at[j] = (((int64_t)max(p, 0) * a.heads + h) * spp + (p >= 0 ? o : 0)) * 16;
+                at[j] = (((int64_t)max(p, 0) * a.heads + h) * spp + o) * 16;
             }
         };
         auto load_k = [&] {
@@ -326,14 +335,13 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !INT8 ? 1 : DP == 256 ? 2 
             }
         };
 
-        fetch(sb + lane, pg, po);
-        place(ub);
+        place(0);
         load_k();
         load_v();
-        for (int u = ub; u < ue; ++u) {
-            const int t0 = 16 * (sp.s0 + 2 * u);
-            const bool whole = there[0] && there[1] && t0 >= sp.first && t0 + 32 <= sp.len;
+        for (int it = 0; it < n; ++it) {
+            const int t0 = 16 * sp.s0 + 32 * (FLAT ? ub + it : wave + WAVES * it);
             const bool seen0 = there[0], seen1 = there[1];
+            const bool whole = seen0 && seen1 && t0 >= sp.first && t0 + 32 <= sp.len;
             // scores: lane (g, m) gets tokens 4 g .. 4 g + 3 of both sixteens for head m
             float z[8];
 #pragma unroll
@@ -389,8 +397,8 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !INT8 ? 1 : DP == 256 ? 2 
                     }
                 }
             }
-            if (u + 1 < ue) {
-                place(u + 1);
+            if (it + 1 < n) {
+                place(it + 1);
                 load_k();
             }
             float most = z[0];
@@ -420,14 +428,14 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !INT8 ? 1 : DP == 256 ? 2 
                 }
             }
             const float ref = (top == NONE ? 0.0f : top) - (INT8 ? 0 : TOP), raise = pow2i(TOP - power);
-            f16 w[8];
+            f16 p[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float e = __builtin_amdgcn_exp2f(z[i] - ref);
                 sum += e;
-                w[i] = (f16)(INT8 ? e * (vs[i] * raise) : e);
+                p[i] = (f16)(INT8 ? e * (vs[i] * raise) : e);
             }
-            const h8 weights = {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
+            const h8 weights = {p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]};
             // sums: rows of the product are the channels E (lane % 16) + i
 #pragma unroll
             for (int c = 0; c < WV; ++c) {
@@ -446,7 +454,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !INT8 ? 1 : DP == 256 ? 2 
                 }
             }
             if constexpr (INT8) offset = __builtin_amdgcn_mfma_f32_16x16x32_f16(half, weights, offset, 0, 0, 0);
-            if (u + 1 < ue) load_v();
+            if (it + 1 < n) load_v();
         }
         if constexpr (INT8) {
             const float unit = pow2i(power - TOP);
@@ -456,14 +464,15 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !INT8 ? 1 : DP == 256 ? 2 
 
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
-        if (ub == 0 && ue == sp.units) {
+        const bool begins = !FLAT || ub == 0, ends = !FLAT || ue == sp.units;
+        if (FLAT ? begins && ends : sp.units == 1) {
             if (m < heads)
                 store_lane<E>(a.y + r * a.ldy + (int64_t)(q0 + m) * dim, acc, sum == 0.0f ? 0.0f : 1.0f / sum, g, dim);
         } else {
             const int at = PARTS / WAVES * wave + part++;
             if (lane == 0) {
                 parts.row[at] = r, parts.head[at] = hh;
-                parts.begins[at] = ub == 0, parts.ends[at] = ue == sp.units;
+                parts.begins[at] = begins, parts.ends[at] = ends;
                 parts.stop[at] = base + (int64_t)(hh + 1) * sp.units;
             }
             if (g == 0) parts.ref[at][m] = top, parts.sum[at][m] = sum;
@@ -476,7 +485,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !INT8 ? 1 : DP == 256 ? 2 
                         *reinterpret_cast<f4*>(o + E * i + e) = f4{acc[e][i], acc[e + 1][i], acc[e + 2][i], acc[e + 3][i]};
             }
         }
-        pos += ue - ub;
+        pos += FLAT ? n : 1;
         if (FLAT && pos < end && hh == HH - 1) {
             base = pos;
             hh = -1;
@@ -539,61 +548,85 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !INT8 ? 1 : DP == 256 ? 2 
     if (FLAT && tid == 0) a.cuts[blockIdx.x] = cut;
 }
 
-// The span that workgroup x of the split began and others went on with, its head y:
-// their parts in order, each under the power of two of its own.  And the rows that see
+// The span that a workgroup of the split began and others went on with, one of its
+// heads: their parts in order, each under the power of two of its own.  And the rows that see
 // nothing, which are zeros.
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     __shared__ __align__(16) float red[16][WOQ_CACHE_MAX_DIM];
-    __shared__ float red_l[16];
-    const int tid = threadIdx.x;
-    if (blockIdx.y == 0) {
+    __shared__ float red_l[16], red_m[16];
+    // parts are read on the XCD that wrote the first of them, but of long rows, which
+    // begin at every 32nd or 64th workgroup, all would be read on one
+    const int tid = threadIdx.x, hq = blockIdx.x / a.groups, i = blockIdx.x - hq * a.groups;
+    const int wg = a.spread ? i ^ (i >> 6 & 63) : i;
+    if (hq == 0) {
         const int n = a.heads * a.group * a.dim;
-        for (int r = blockIdx.x; r < a.b; r += gridDim.x) {
+        for (int r = wg; r < a.b; r += a.groups) {
             if (span_of(a, r).units) continue;
             for (int d = tid; d < n; d += 256) *gptr(a.y + r * a.ldy + d) = 0;
         }
     }
-    const int4 cut = a.cuts[blockIdx.x];
+    const int4 cut = a.cuts[wg];
     if (cut.z == 0) return;
-    const int h = cut.y / a.tiles, tile = cut.y - h * a.tiles, hq = blockIdx.y;
+    const int h = cut.y / a.tiles, tile = cut.y - h * a.tiles;
     if (hq >= min(16, a.group - 16 * tile)) return;
-    // four channels to a thread, every 4th, 8th or 16th part to a wave or part of one
+    // four channels to a thread, every 4th, 8th or 16th part to a wave or part of one,
+    // eight parts in flight
     const int lanes = a.dim <= 64 ? 16 : a.dim <= 128 ? 32 : 64, parts = 256 / lanes;
     const int part = tid / lanes, d = 4 * (tid - part * lanes);
-    // the first workgroup's part is its second, the others' their first
-    auto slot = [&](int i) { return 2 * ((int64_t)blockIdx.x + i) + (i == 0); };
-    float ref = NONE;
-    for (int i = tid & 63; i < cut.z; i += 64) ref = fmaxf(ref, *gptr(a.stats + (slot(i) * 16 + hq) * 2));
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) ref = fmaxf(ref, __shfl_xor(ref, s));
-    if (ref == NONE) ref = 0.0f;
-    float l = 0.0f;
+    float ref = NONE, l = 0.0f;
     f4 o = {0, 0, 0, 0};
-    if (d < a.dim) {
-#pragma unroll 4
-        for (int i = part; i < cut.z; i += parts) {
-            const float* st = a.stats + (slot(i) * 16 + hq) * 2;
-            const float keep = __builtin_amdgcn_exp2f(*gptr(st) - ref);
-            l = fmaf(*gptr(st + 1), keep, l);
-            o += *(__attribute__((address_space(1))) const f4*)(a.sums + (slot(i) * a.per_tile + hq) * a.dim + d) * keep;
+    auto some = [&](auto count, int i0) {
+        constexpr int N = decltype(count)::value;
+        u32x2 st[N];
+        f4 v[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            // the first workgroup's part is its second, the others' their first
+            const int i = min(i0 + j * parts, cut.z - 1);
+            const int64_t slot = 2 * ((int64_t)wg + i) + (i == 0);
+            st[j] = *(g_u32x2*)(a.stats + (slot * 16 + hq) * 2);
+            v[j] = *(__attribute__((address_space(1))) const f4*)(a.sums + (slot * a.per_tile + hq) * a.dim + min(d, a.dim - 4));
         }
-        *reinterpret_cast<f4*>(&red[part][d]) = o;
-        if (d == 0) red_l[part] = l;
+        float next = ref;
+#pragma unroll
+        for (int j = 0; j < N; ++j) next = fmaxf(next, __uint_as_float(st[j][0]));
+        const float zero = next == NONE ? 0.0f : next, old = __builtin_amdgcn_exp2f(ref - zero);
+        l *= old;
+        o *= old;
+        ref = next;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if (i0 + j * parts >= cut.z) continue;
+            const float keep = __builtin_amdgcn_exp2f(__uint_as_float(st[j][0]) - zero);
+            l = fmaf(__uint_as_float(st[j][1]), keep, l);
+            o += v[j] * keep;
+        }
+    };
+    if (cut.z <= parts) {
+        if (part < cut.z) some(std::integral_constant<int, 1>{}, part);
+    } else {
+        for (int i0 = part; i0 < cut.z; i0 += 8 * parts) some(std::integral_constant<int, 8>{}, i0);
     }
+    if (d < a.dim) *reinterpret_cast<f4*>(&red[part][d]) = o;
+    if (d == 0) red_l[part] = l, red_m[part] = ref;
     __syncthreads();
     if (tid >= a.dim) return;
-    float s = 0.0f, t = 0.0f;
+    float all = NONE, s = 0.0f, t = 0.0f;
+    for (int i = 0; i < parts; ++i) all = fmaxf(all, red_m[i]);
+    if (all == NONE) all = 0.0f;
     for (int i = 0; i < parts; ++i) {
-        s += red[i][tid];
-        t += red_l[i];
+        const float keep = __builtin_amdgcn_exp2f(red_m[i] - all);
+        s = fmaf(red[i][tid], keep, s);
+        t = fmaf(red_l[i], keep, t);
     }
     *gptr(a.y + cut.x * a.ldy + (int64_t)(h * a.group + 16 * tile + hq) * a.dim + tid) = f_to_h(t == 0.0f ? 0.0f : s / t);
 }
 
 // Workgroups of a split: as many as keep two on a compute unit.
-int workgroups() { return PERCU * woq::compute_units(); }
+int workgroups() { return 2 * woq::compute_units(); }
 
-// Where the capacity is no more than this, a workgroup takes a span whole and there is nothing to join.
+// Where the capacity is no more than this and the spans are no more than the
+// workgroups, each takes one whole and there is nothing to join.
 constexpr int64_t DIRECT = 512;
 
 struct Layout {
@@ -707,17 +740,20 @@ extern "C" int woq_attn_decode(const woq_cache* c, const uint16_t* q, int64_t ld
     a.stats = reinterpret_cast<float*>(ws + l.stats);
     a.tiles = l.tiles;
     a.per_tile = l.per_tile;
+    a.groups = workgroups();
+    a.spread = b * c->heads * l.tiles * 8 <= a.groups && a.groups % 64 == 0;
     void* argv[] = {&a};
     hipStream_t s = (hipStream_t)stream;
-    const bool flat = a.capacity > DIRECT;
+    const int64_t spans = b * c->heads * l.tiles;
+    const bool flat = a.capacity > DIRECT || spans > workgroups();
     const Kernel k = c->fmt == WOQ_CACHE_INT8 ? split_kernel<true>(c->dim, flat) : split_kernel<false>(c->dim, flat);
     const size_t lds = (size_t)(flat ? 2 : 1) * k.waves * l.per_tile * (k.dim + 4) * 4;
-    const unsigned grid = flat ? (unsigned)workgroups() : (unsigned)(b * c->heads * l.tiles);
+    const unsigned grid = flat ? (unsigned)workgroups() : (unsigned)spans;
     hipError_t e = hipSuccess;
     if (lds > 64 << 10) e = hipFuncSetAttribute(k.f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e == hipSuccess) e = hipLaunchKernel(k.f, dim3(grid), dim3(64 * k.waves), argv, lds, s);
     if (e == hipSuccess && flat)
-        e = hipLaunchKernel(reinterpret_cast<const void*>(&attn_join_kernel), dim3(grid, l.per_tile),
+        e = hipLaunchKernel(reinterpret_cast<const void*>(&attn_join_kernel), dim3(grid * l.per_tile),
                             dim3(256), argv, 0, s);
     if (e != hipSuccess) {
         woq::set_hip_error((int)e);
