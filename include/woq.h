@@ -635,9 +635,10 @@ int64_t woq_attn_decode_workspace(const woq_cache* c, int32_t q_heads, int64_t b
  * are fp32 [b], top_k int32 [b], in device memory; temperature null: 1, top_k,
  * top_p, min_p null: off.  token int32 [b], prob fp32 [b] (may be null).  Weights
  * and their sums are 64-bit; what a row's draw gives depends on that row alone.
- * N <= WOQ_SAMPLE_MAX_N, b < 2^31; b = 0 is a no-op.
+ * N <= WOQ_SAMPLE_MAX_N, b <= WOQ_SAMPLE_MAX_ROWS; b = 0 is a no-op.
  */
 #define WOQ_SAMPLE_MAX_N (1 << 24)
+#define WOQ_SAMPLE_MAX_ROWS 4000000
 int woq_sample(const uint16_t* logits, int64_t ld, int64_t N, int64_t b, const float* temperature,
                const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* token,
                float* prob, void* stream);
