@@ -190,6 +190,11 @@ struct Weight {
     }
 };
 
+// What each value of a chunk weighs of the one before.
+__device__ __forceinline__ double step_of(const Weight& w, uint32_t chunk) {
+    return w.exp_of((value_of(chunk * CHUNK + 1) - value_of(chunk * CHUNK)) * w.inv);
+}
+
 // Weights of this lane's bins of a chunk.  Neighbouring values of a chunk are equally
 // far apart, so each weighs the same part of the one before; only the chunks up to
 // +infinity's have values one by one.
@@ -200,7 +205,7 @@ __device__ __forceinline__ void weights_of(const Weight& w, uint32_t chunk, doub
         for (int j = 0; j < B; ++j) v[j] = alive(e + j) ? w(e + j) : 0.0;
         return;
     }
-    const double step = w.exp_of((value_of(chunk * CHUNK + 1) - value_of(chunk * CHUNK)) * w.inv);
+    const double step = step_of(w, chunk);
     double next = w(max(e, w.first));         // bins before the first of all hold nothing
 #pragma unroll
     for (int j = 0; j < B; ++j) {
@@ -225,11 +230,21 @@ __device__ void weigh(Row& s, const uint16_t* x, uint32_t N, const Weight& w) {
             double m = 0.0;
             if (s.count[c] && c * CHUNK <= s.limit) {
                 uint32_t n[B];
-                double v[B];
                 counts_of(s, c, n);
-                weights_of(w, c, v);
+                if (c > FIRST / CHUNK && c * CHUNK > w.first && (c + 1) * CHUNK <= s.limit) {
+                    // all kept: the first weight times a polynomial in what each weighs of the one before
+                    // (61 rows of 128256 30.6 -> 28.0 us)
+                    const double step = step_of(w, c);
+                    m = (double)n[B - 1];
 #pragma unroll
-                for (int j = 0; j < B; ++j) m = fma((double)kept(s, c * CHUNK + B * lane + j, n[j]), v[j], m);
+                    for (int j = B - 2; j >= 0; --j) m = fma(m, step, (double)n[j]);
+                    m *= w(c * CHUNK + B * lane);
+                } else {
+                    double v[B];
+                    weights_of(w, c, v);
+#pragma unroll
+                    for (int j = 0; j < B; ++j) m = fma((double)kept(s, c * CHUNK + B * lane + j, n[j]), v[j], m);
+                }
                 m = wave_sum(m);
             }
             if (lane == 0) s.mass[c] = m;
