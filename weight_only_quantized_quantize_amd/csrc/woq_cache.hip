@@ -4,10 +4,14 @@
 //   rotation  (a, b) -> (a cos - b sin, b cos + a sin) for each pair of a head,
 //   INT8      scale = max|v| / 127, byte = rne(v / scale) + 128 per token and head.
 //
-// Bound by memory at many tokens and by one launch and two dependent round trips
-// (slot and position, then the row) at few.  A head is held by 4, 8 or 16 lanes,
-// 16 values each, so a wave takes several heads, its maximum is a reduction of two
-// to four steps inside the lanes that hold it, and no value passes through LDS.
+// Bound by memory at many tokens (2047 rows of 16 + 2 x 8 heads of 256 in 17 us, 3.5
+// TB/s; 16381 tokens of 8 heads of 128 read back in 20-24 us, 4.2-5.1 TB/s) and by one
+// launch and two dependent round trips (slot and position with the row, then the
+// angles) at few (one row of 64 + 2 x 8 heads of 128 3.3 us).  A head is held by 4, 8 or
+// 16 lanes, 16 values each, so a wave takes several heads, its maximum is a reduction
+// of two to four steps inside the lanes that hold it, and no value passes through LDS.
+// Four heads to a group of lanes, the angles read once for them, were no faster (17.1
+// us) and slower for few rows (4.9).
 #include <hip/hip_runtime.h>
 
 #include "woq_gemv.h"
@@ -62,12 +66,30 @@ __device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
     }
 }
 
-// The bytes of eight codes; the division decides every rounding, as on the host.
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float scale, bool zero) {
+// The bytes of eight codes, rne(v / scale) + 128, by a reciprocal: 1.5 2^23 + 128
+// added to v / scale leaves the byte in the sum's low bits.  v times the reciprocal is
+// off by less than 127 2^-22; near is set where that could decide the rounding.
+constexpr float MAGIC = 12583040.0f;
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv, bool& near) {
+    uint32_t u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float t = fmaf(v[j], inv, MAGIC);
+        near |= !(fabsf(fmaf(v[j], inv, MAGIC - t)) <= 0.4999f);
+        u[j] = __float_as_uint(t);
+    }
+    auto four = [&](int j) {
+        return __builtin_amdgcn_perm(__builtin_amdgcn_perm(u[j + 3], u[j + 2], 0x0c0c0400u),
+                                     __builtin_amdgcn_perm(u[j + 1], u[j], 0x0c0c0400u), 0x05040100u);
+    };
+    return make_uint2(four(0), four(4));
+}
+// The same by the division, bit for bit the host's.
+__device__ __forceinline__ uint2 codes8_exact(const float (&v)[8], float scale) {
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float d = zero ? 0.0f : fminf(fmaxf(rintf(v[j] / scale), -127.0f), 127.0f);
+        const float d = fminf(fmaxf(rintf(v[j] / scale), -127.0f), 127.0f);
         w[j >> 2] |= (uint32_t)((int)d + 128) << (8 * (j & 3));
     }
     return make_uint2(w[0], w[1]);
@@ -92,12 +114,9 @@ __global__ __launch_bounds__(256) void cache_write_kernel(WriteArgs a) {
     const bool apart = a.rope && kind != 1 && !a.interleaved && 16 * l < a.rot;
     const int o0 = apart ? 8 * l : 16 * l, o1 = apart ? a.rot / 2 + 8 * l : 16 * l + 8;
 
-    int64_t slot = 0;
-    if (kind != 2) {
-        slot = *gptr(a.slots + r);
-        if (slot < 0 || slot >= a.n_slots) return;
-    }
-    float x0[8] = {}, x1[8] = {};
+    // the row, its slot and its position are asked for together, then the angles
+    const int64_t slot = kind != 2 ? *gptr(a.slots + r) : 0, p = turn ? *gptr(a.pos + r) : 0;
+    float x0[8] = {}, x1[8] = {}, c[8], s[8];
     if (active) {
         const uint16_t* row = kind == 0   ? a.k + r * a.ldk + (int64_t)h * a.dim
                               : kind == 1 ? a.v + r * a.ldv + (int64_t)(h - a.heads) * a.dim
@@ -105,9 +124,8 @@ __global__ __launch_bounds__(256) void cache_write_kernel(WriteArgs a) {
         load8h(row + o0, x0);
         load8h(row + o1, x1);
     }
+    if (slot < 0 || slot >= a.n_slots) return;
     if (turn) {
-        const int64_t p = *gptr(a.pos + r);
-        float c[8], s[8];
         if (p >= 0 && p < a.n_pos) {
             load8f(a.rope + p * a.rot + 8 * l, c);
             load8f(a.rope + p * a.rot + a.rot / 2 + 8 * l, s);
@@ -142,8 +160,8 @@ __global__ __launch_bounds__(256) void cache_write_kernel(WriteArgs a) {
         return;
     }
     const int head = kind == 0 ? h : h - a.heads;
-    const int64_t page = slot / a.page;
-    const int64_t at = (page * a.heads + head) * a.page + (slot - page * a.page);     // token and head
+    const uint32_t page = (uint32_t)slot / (uint32_t)a.page;
+    const int64_t at = ((int64_t)page * a.heads + head) * a.page + ((uint32_t)slot - page * (uint32_t)a.page);
     if (!a.ks) {
         if (active) {
             uint16_t* out = reinterpret_cast<uint16_t*>(kind == 0 ? a.kc : a.vc) + at * a.dim;
@@ -166,8 +184,19 @@ __global__ __launch_bounds__(256) void cache_write_kernel(WriteArgs a) {
     const bool zero = bad || scale == 0.0f;
     if (active) {
         uint8_t* out = (kind == 0 ? a.kc : a.vc) + at * a.dim;
-        gstore_u2(out + o0, codes8(x0, scale, zero));
-        gstore_u2(out + o1, codes8(x1, scale, zero));
+        uint2 w0 = make_uint2(0x80808080u, 0x80808080u), w1 = w0;
+        if (!zero) {
+            const float inv = 1.0f / scale;
+            bool near = false;
+            w0 = codes8(x0, inv, near);
+            w1 = codes8(x1, inv, near);
+            if (near) {       // also where the reciprocal overflows
+                w0 = codes8_exact(x0, scale);
+                w1 = codes8_exact(x1, scale);
+            }
+        }
+        gstore_u2(out + o0, w0);
+        gstore_u2(out + o1, w1);
     }
     if (l == 0) *gptr((kind == 0 ? a.ks : a.vs) + at) = scale;
 }
@@ -194,8 +223,8 @@ __global__ __launch_bounds__(256) void cache_read_kernel(ReadArgs a) {
     const int64_t slot = *gptr(a.slots + r);
     uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
     if (slot >= 0 && slot < a.n_slots) {
-        const int64_t page = slot / a.page;
-        const int64_t at = (page * a.heads + head) * a.page + (slot - page * a.page);
+        const uint32_t page = (uint32_t)slot / (uint32_t)a.page;
+        const int64_t at = ((int64_t)page * a.heads + head) * a.page + ((uint32_t)slot - page * (uint32_t)a.page);
         const uint8_t* c = kind ? a.c[1] : a.c[0];
         const float* sp = kind ? a.s[1] : a.s[0];
         if (sp) {
