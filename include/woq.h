@@ -721,6 +721,42 @@ int woq_stack_run_lora(woq_stack* st, const uint16_t* const* inputs, uint16_t* c
 int64_t woq_stack_lora_workspace(const woq_stack* st, const woq_lora_w* const* adapters, int64_t b);
 
 /*
+ * The attention behind a step that writes q | k | v side by side: its rows hold
+ * (q_heads + 2 cache->heads) * cache->dim values.  y (fp16 [b, q_heads * dim])
+ * receives the result, as a rule the input buffer of the step that follows.  rope
+ * may be null (no rotation); rot, interleaved, n_pos, scale, softcap and window as
+ * for woq_cache_write and woq_attn_decode.
+ */
+typedef struct {
+    const woq_cache* cache;
+    const float* rope;
+    uint16_t* y;
+    int64_t n_pos;
+    float scale, softcap;
+    int32_t q_heads, rot, interleaved, window;
+} woq_stack_attn;
+
+/*
+ * woq_stack_run with attention between its steps: after step i has written
+ * outputs[out_slot], the rows' keys and values are written into the cache of
+ * attn[i] (null: no attention behind this step) at slots[r], q and k turned by
+ * pos[r] on the way (woq_cache_write; the turned q replaces the step's), and
+ * woq_attn_decode attends over the row's pages into attn[i]->y, before the next
+ * step runs.  slots, pos, pages and lens are of the batch: every layer's cache is
+ * paged alike, and lens count the new tokens.  attn holds an entry for every step.
+ * The two calls' limits hold for every such step (the output 16-byte aligned, N a
+ * multiple of 8), and everything is checked before the first launch.  workspace:
+ * woq_stack_attn_workspace bytes, owned by the caller; runs that share it, or the
+ * runner, must not overlap.
+ */
+int woq_stack_run_attn(woq_stack* st, const uint16_t* const* inputs, uint16_t* const* outputs, int64_t b,
+                       const woq_stack_attn* const* attn, const int32_t* slots, const int32_t* pos,
+                       const int32_t* pages, int64_t ldpages, int64_t max_pages, const int32_t* lens,
+                       void* workspace, int64_t workspace_bytes, void* stream);
+/* Bytes for batches of up to b rows, or a negative status. */
+int64_t woq_stack_attn_workspace(const woq_stack* st, const woq_stack_attn* const* attn, int64_t b);
+
+/*
  * Kernel launches of one woq_stack_run pass at batch b (a folded INT4O step
  * or an INT8 step is one launch, a permute-then-product INT4O step two, three
  * with the split-K reduction), assuming 16-byte aligned inputs.

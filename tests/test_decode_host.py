@@ -248,3 +248,9 @@ def test_binding_refuses_a_cache_of_another_device():
     pages, ws = on_gpu(torch.zeros(3, 5, dtype=i32), 0), on_gpu(torch.zeros(1 << 20, dtype=torch.uint8), 0)
     with pytest.raises(ValueError, match="woq_attn_decode: the cache"):
         woq.woq_attn_decode(c, rows, pages, slots, rows, ws)
+
+
+def test_stack_with_attention_refusals():
+    one = (ctypes.c_void_p * 1)(P)
+    assert call("woq_stack_run_attn", None, one, one, 1, one, P, P, P, 4, 4, P, P, 1 << 20, None) == EINVAL
+    assert call("woq_stack_attn_workspace", None, one, 1) == EINVAL

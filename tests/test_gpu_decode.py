@@ -646,3 +646,319 @@ def test_sample_rows_do_not_touch_each_other(gpu_lib):
     together = check_sample(x, u, p=0.9)
     for r in (0, 17, 299):
         assert check_sample(x[r:r + 1], u[r:r + 1], p=0.9)[0] == together[r]
+
+
+# ------------------------------------------------------- all of them in a row
+
+class Step:
+    """A decode step of one small layer and a head: the q|k|v product of an INT8
+    weight, the new tokens into the cache, attention, the o product, the head's
+    product and the choice of the token."""
+
+    def __init__(self, b, seed=0, heads=2, q_heads=4, dim=64, page=16, length=200, vocab=1000, int8=True):
+        import torch
+        rng = np.random.default_rng(seed)
+        self.b, self.K, self.n, self.m = b, 128, q_heads * dim, heads * dim
+        self.heads, self.q_heads, self.dim, self.page, self.vocab = heads, q_heads, dim, page, vocab
+
+        def weight(N, K):
+            return woq.DeviceInt8([woq.woq_quantize_int8((rng.standard_normal((N, K)) / np.sqrt(K)).astype(np.float32))])
+
+        self.qkv_w, self.o_w, self.head_w = weight(self.n + 2 * self.m, self.K), weight(self.K, self.n), weight(vocab, self.K)
+        W = -(-length // page) + 1
+        self.c = Cache(b * W + 1, heads, page, dim, int8, seed=seed)
+        self.pages = rng.permutation(b * W).reshape(b, W).astype(np.int32)
+        self.lens = rng.integers(1, length, b).astype(np.int32)
+        self.rope = rope_table(W * page, dim)
+        half = dict(dtype=torch.float16, device="cuda")
+        self.d = dict(x=dev(rng.standard_normal((b, self.K)).astype(np.float16)), pages=dev(self.pages), rope=dev(self.rope),
+                      u=dev(rng.random(b).astype(np.float32)), top_p=dev(np.full(b, 0.9, np.float32)))
+        self.qkv, self.y = torch.empty(b, self.n + 2 * self.m, **half), torch.empty(b, self.n, **half)
+        self.h, self.logits = torch.empty(b, self.K, **half), torch.empty(b, vocab, **half)
+        self.token = torch.empty(b, dtype=torch.int32, device="cuda")
+        self.ws = torch.empty(woq.woq_attn_decode_workspace(self.c.desc, q_heads, b), dtype=torch.uint8, device="cuda")
+        self.set_lens()
+
+    def set_lens(self):
+        at = self.lens - 1
+        slots = self.pages[np.arange(self.b), at // self.page] * self.page + at % self.page
+        self.d.update(lens=dev(self.lens), pos=dev(at.astype(np.int32)), slots=dev(slots.astype(np.int32)))
+
+    def run(self, stream=None):
+        d, n, m = self.d, self.n, self.m
+        woq.woq_qgemv_int8(self.qkv_w.desc, d["x"], self.qkv, stream=stream)
+        woq.woq_cache_write(self.c.desc, self.qkv[:, n:n + m], self.qkv[:, n + m:], d["slots"], q=self.qkv[:, :n],
+                            q_out=self.qkv[:, :n], rope=d["rope"], pos=d["pos"], stream=stream)
+        woq.woq_attn_decode(self.c.desc, self.qkv[:, :n], d["pages"], d["lens"], self.y, self.ws, stream=stream)
+        woq.woq_qgemv_int8(self.o_w.desc, self.y, self.h, stream=stream)
+        woq.woq_qgemv_int8(self.head_w.desc, self.h, self.logits, stream=stream)
+        woq.woq_sample(self.logits, d["u"], self.token, top_p=d["top_p"], stream=stream)
+
+    def results(self):
+        return [host(t).copy() for t in (self.qkv, self.y, self.logits, self.token)] + [a.copy() for a in self.c.now()
+                                                                                         if a is not None]
+
+
+def same(a, b):
+    for x, y in zip(a, b):
+        np.testing.assert_array_equal(x.view(np.uint8), y.view(np.uint8))
+
+
+@pytest.mark.parametrize("int8", [True, False])
+@pytest.mark.parametrize("b", [1, 5, 8])
+def test_decode_steps_in_a_row(gpu_lib, int8, b):
+    """Four tokens of every request: each operator's result is the definition's of
+    what the one before has left."""
+    import torch
+    case("steps", int8, b)
+    s = Step(b, seed=b, int8=int8)
+    for _ in range(4):
+        s.run()
+        qkv, y, x, token = (host(t) for t in (s.qkv, s.y, s.logits, s.token))
+        k, v, ks, vs = s.c.now()
+        s.c.k, s.c.v, s.c.ks, s.c.vs = k, v, ks, vs
+        plain = torch.empty_like(s.qkv)
+        woq.woq_qgemv_int8(s.qkv_w.desc, s.d["x"], plain)
+        new = host(plain).reshape(b, -1, s.dim)
+        turned = O.rotate(new[:, :s.q_heads + s.heads], s.rope, host(s.d["pos"]))
+        within(qkv[:, :s.n].reshape(b, s.q_heads, s.dim), turned[:, :s.q_heads],
+               np.abs(turned[:, :s.q_heads]) * H + 4 * U * 2 * np.abs(new).max() + SUB)
+        slots = host(s.d["slots"])
+        for which, ref in (("k", turned[:, s.q_heads:]), ("v", new[:, s.q_heads + s.heads:].astype(np.float64))):
+            top = np.abs(ref).max(-1, keepdims=True)
+            step = top / 127 * (0.5 + 2.0 ** -10) if int8 else np.abs(ref) * H + SUB
+            within(s.c.tokens(which, slots), ref, step + 4 * U * 2 * np.abs(new).max(), which)
+        check_attention(s.c, s.q_heads, s.lens, q=qkv[:, :s.n], pages=s.pages, got=y)
+        for r in range(b):
+            assert token[r] == O.sample(x[r], float(host(s.d["u"])[r]), top_p=float(np.float32(0.9)))[0]
+        s.lens += 1
+        s.set_lens()
+        s.d["u"].copy_(torch.rand(b))
+        s.d["x"].copy_(torch.randn(b, s.K))
+
+
+@pytest.mark.parametrize("length", [200, 1500])
+def test_decode_step_captured_and_replayed(gpu_lib, length):
+    """One graph replayed between eager runs on other inputs and other work gives
+    the eager bits every time; two graphs share a workspace in turn."""
+    import torch
+    s, t = Step(5, seed=1, length=length), Step(5, seed=2, length=length)
+    t.ws = s.ws
+    for x in (s, t):
+        x.run()
+    torch.cuda.synchronize()
+    graphs = []
+    for x in (s, t):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            x.run()
+        graphs.append(g)
+    for it in range(4):
+        for x, g in zip((s, t), graphs):
+            x.d["x"].copy_(torch.randn(5, x.K))
+            x.lens = 1 + (x.lens + 37) % (length - 1)
+            fresh = x.d.copy()
+            x.set_lens()
+            for name in ("lens", "pos", "slots"):               # into the graph's own buffers
+                fresh[name].copy_(x.d[name])
+            x.d = fresh
+            x.run()
+            want = x.results()
+            x.y.fill_(3)
+            x.token.fill_(-9)
+            x.ws.fill_(255)
+            g.replay()
+            same(x.results(), want)
+            torch.randn(1000, 1000, device="cuda").sum().item()  # the program's own work
+
+
+def test_two_streams_at_once(gpu_lib):
+    import torch
+    steps = [Step(4, seed=i, length=900) for i in range(4)]
+    alone = []
+    for s in steps:
+        s.run()
+        alone.append(s.results())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in steps]
+    for _ in range(8):
+        for s, st in zip(steps, streams):
+            s.run(stream=st)
+    torch.cuda.synchronize()
+    for s, want in zip(steps, alone):
+        same(s.results(), want)
+    # the stream of the caller, not the default one
+    for s, st, want in zip(steps, streams, alone):
+        s.y.fill_(0)
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            s.run()
+        st.synchronize()
+        same(s.results(), want)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "int4o"])
+def test_stack_with_attention_equals_its_steps(gpu_lib, fmt):
+    """q|k|v, attention, o of two layers through the runner: the bits of the calls
+    one by one, also from a graph; a step without attention between."""
+    import torch
+    case("stack attention", fmt)
+    rng = np.random.default_rng(3)
+    b, heads, q_heads, dim, page = 6, 2, 4, 64, 16
+    n, m, K = q_heads * dim, heads * dim, 128
+    dims = [(n + 2 * m, K), (K, n)] * 2
+    steps, keep = [], []
+    for i, (N, k) in enumerate(dims):
+        W = (rng.standard_normal((N, k)) / np.sqrt(k)).astype(np.float32)
+        if fmt == "int8":
+            d = woq.DeviceInt8([woq.woq_quantize_int8(W)])
+            steps.append(woq.step_int8(d, i, i))
+        else:
+            geom = woq.woq_int4o_geometry(k)
+            perm = O.global_perm(k, np.sort(rng.choice(k, geom.n_out, replace=False)))
+            d, pd = woq.DeviceInt4o([woq.woq_quantize_int4o(W, perm, geom.n_out)], geom), dev(perm)
+            keep.append(pd)
+            steps.append(woq.step_int4o(d, pd, i, i))
+        keep.append(d)
+    half = dict(dtype=torch.float16, device="cuda")
+    lens = np.array([1, 100, 33, 0, 16, 77], np.int32)
+    pages = rng.permutation(6 * 8)[:48].reshape(6, 8).astype(np.int32)
+    at = np.maximum(lens - 1, 0)
+    slots = np.where(lens > 0, pages[np.arange(6), at // page] * page + at % page, -1).astype(np.int32)
+    rope = dev(rope_table(128, 32))
+    sd, pd, ld, posd = dev(slots), dev(pages), dev(lens), dev(at.astype(np.int32))
+
+    def fresh():
+        caches = [Cache(48, heads, page, dim, i == 0, seed=20 + i) for i in range(2)]
+        outs = [torch.full((b, N), 7.0, **half) for N, _ in dims]
+        ys = [torch.full((b, n), 7.0, **half) for _ in range(2)]
+        return caches, outs, ys
+
+    x = dev(rng.standard_normal((b, K)).astype(np.float16))
+    caches, outs, ys = fresh()
+    st = woq.Stack(steps, 8)
+    st.bind([x, ys[0], outs[1], ys[1]], outs)
+    attn = [woq.StackAttention(caches[0].d, ys[0], rope=rope, interleaved=True), None,
+            woq.StackAttention(caches[1].d, ys[1], softcap=30.0, window=40), None]
+    ws = torch.empty(st.attn_workspace(attn, b), dtype=torch.uint8, device="cuda")
+    st.run_attn(b, attn, sd, pd, ld, ws, pos=posd)
+    got = [host(t).copy() for t in outs + ys] + [a for c in caches for a in c.now() if a is not None]
+
+    hc, ho, hy = fresh()
+    src = x
+    for layer in range(2):
+        for j in range(2):
+            i = 2 * layer + j
+            step = steps[i]
+            step.in_slot = step.out_slot = 0
+            one = woq.Stack([step], 8)
+            one.bind([src], [ho[i]])
+            one.run(b)
+            if j == 0:
+                q, kv = ho[i][:, :n], ho[i][:, n:]
+                kw = dict(q=q, q_out=q, rope=rope, pos=posd, interleaved=True) if layer == 0 else {}
+                woq.woq_cache_write(hc[layer].desc, kv[:, :m], kv[:, m:], sd, **kw)
+                woq.woq_attn_decode(hc[layer].desc, q, pd, ld, hy[layer], ws, softcap=30.0 * layer, window=40 * layer)
+                src = hy[layer]
+            else:
+                src = ho[i]
+    want = [host(t) for t in ho + hy] + [a for c in hc for a in c.now() if a is not None]
+    same(got, want)
+    assert not host(ys[0])[3].any()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        st.run_attn(b, attn, sd, pd, ld, ws, pos=posd)
+    for _ in range(3):
+        for t in outs + ys:
+            t.fill_(3)
+        g.replay()
+        same([host(t) for t in outs + ys] + [a for c in caches for a in c.now() if a is not None], want)
+    del keep
+
+
+def test_stack_with_attention_refuses_before_the_first_launch(gpu_lib):
+    import torch
+    rng = np.random.default_rng(0)
+    d = woq.DeviceInt8([woq.woq_quantize_int8(rng.standard_normal((256, 64)).astype(np.float32))])
+    st = woq.Stack([woq.step_int8(d, 0, 0)], 4)
+    half = dict(dtype=torch.float16, device="cuda")
+    x, out, y = torch.ones(4, 64, **half), torch.full((4, 256), 7.0, **half), torch.full((4, 128), 7.0, **half)
+    st.bind([x], [out])
+    c, idx, pages = Cache(4, 1, 16, 64), dev(np.zeros(4, np.int32)), dev(np.zeros((4, 1), np.int32))
+    good = woq.StackAttention(c.d, y, rope=torch.zeros(3, 16, device="cuda"))
+    ws = torch.empty(st.attn_workspace([good], 4), dtype=torch.uint8, device="cuda")
+    wide = Cache(4, 2, 16, 64)
+    for bad in (woq.StackAttention(wide.d, y), woq.StackAttention(c.d, torch.empty(4, 64, **half)),
+                woq.StackAttention(c.d, y, rope=torch.zeros(3, 24, device="cuda")),
+                woq.StackAttention(c.d, y, window=-1), woq.StackAttention(c.d, y, scale=float("nan"))):
+        with pytest.raises(woq.WoqError):
+            st.run_attn(4, [bad], idx, pages, idx, ws, pos=idx)
+    with pytest.raises(woq.WoqError):
+        st.run_attn(4, [good], idx, pages, idx, ws)                       # angles without positions
+    with pytest.raises(woq.WoqError):
+        st.run_attn(4, [good], idx, pages, idx, ws[:64], pos=idx)
+    for args in (([good, None], idx, pages, idx), ([good], idx[:3], pages, idx), ([good], idx, pages[:3], idx)):
+        with pytest.raises(ValueError):
+            st.run_attn(4, *args, ws, pos=idx)
+    with pytest.raises(ValueError):
+        st.run_attn(4, [woq.StackAttention(c.d, y[:3])], idx, pages, idx, ws)
+    assert np.all(host(out) == 7) and np.all(host(y) == 7)
+
+
+def test_empty_calls_are_no_ops(gpu_lib):
+    s = Step(2, seed=5)
+    s.run()
+    want = s.results()
+    d, n, m = s.d, s.n, s.m
+    woq.woq_cache_write(s.c.desc, s.qkv[:, n:n + m], s.qkv[:, n + m:], d["slots"], q=s.qkv[:, :n], q_out=s.qkv[:, :n],
+                        rope=d["rope"], pos=d["pos"], b=0)
+    woq.woq_cache_read(s.c.desc, d["slots"], s.qkv[:, :m], n=0)
+    woq.woq_attn_decode(s.c.desc, s.qkv[:, :n], d["pages"], d["lens"], s.y, s.ws, b=0)
+    woq.woq_sample(s.logits, d["u"], s.token, b=0)
+    same(s.results(), want)
+
+
+def test_offsets_past_32_bits(gpu_lib):
+    """A cache of more than 2^32 bytes of keys, its tokens at the far end, and
+    logits whose rows start past 2^31."""
+    import torch
+    heads, page, dim = 8, 64, 256
+    n_pages = (1 << 32) // (heads * page * dim) + 40
+    k, v = (torch.full((n_pages, heads, page, dim), 255, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((n_pages, heads, page), float("nan"), device="cuda") for _ in range(2))
+    c = woq.DeviceCache(k, v, ks, vs)
+    rng = np.random.default_rng(1)
+    b = 130
+    x = rng.standard_normal((b, 2 * heads * dim)).astype(np.float16)
+    last = np.arange(n_pages - 3, n_pages)
+    slots = (last[np.arange(b) // page] * page + np.arange(b) % page).astype(np.int32)
+    xd = dev(x)
+    woq.woq_cache_write(c.desc, xd[:, :heads * dim], xd[:, heads * dim:], dev(slots))
+    ko, vo = (torch.empty(b, heads * dim, dtype=torch.float16, device="cuda") for _ in range(2))
+    woq.woq_cache_read(c.desc, dev(slots), ko, vo)
+    for got, src in ((host(ko), x[:, :heads * dim]), (host(vo), x[:, heads * dim:])):
+        top = np.abs(src.astype(float)).reshape(b, heads, dim).max(-1).repeat(dim, 1)
+        within(got, src.astype(np.float64), top / 127 * (0.5 + 2.0 ** -10) + np.abs(src) * H)
+    q = rng.standard_normal((1, 16 * dim)).astype(np.float16)
+    y = torch.empty(1, 16 * dim, dtype=torch.float16, device="cuda")
+    ws = torch.empty(woq.woq_attn_decode_workspace(c.desc, 16, 1), dtype=torch.uint8, device="cuda")
+    for width in (3, 40):
+        pages = np.full((1, width), -1, np.int32)
+        pages[0, :3] = last
+        woq.woq_attn_decode(c.desc, dev(q), dev(pages), dev(np.array([b], np.int32)), y, ws)
+        small = Cache(3, heads, page, dim)
+        small.k, small.v, small.ks, small.vs = (host(t[-3:]) for t in (k, v, ks, vs))
+        check_attention(small, 16, [b], q=q, pages=np.arange(3, dtype=np.int32)[None], got=host(y))
+    del k, v, ks, vs, c
+    N, rows = 256000, 8500
+    logit = torch.zeros(rows, N, dtype=torch.float16, device="cuda")
+    far = torch.randn(3, N, device="cuda").half()
+    logit[-3:] = far
+    u = torch.rand(rows, device="cuda")
+    token = torch.empty(rows, dtype=torch.int32, device="cuda")
+    woq.woq_sample(logit, u, token, top_k=torch.full((rows,), 50, dtype=torch.int32, device="cuda"))
+    got, uh, fh = host(token), host(u), host(far)
+    for i in range(3):
+        assert got[rows - 3 + i] == O.sample(fh[i], float(uh[rows - 3 + i]), top_k=50)[0]
+    assert got[0] == O.sample(np.zeros(N), float(uh[0]), top_k=50)[0]

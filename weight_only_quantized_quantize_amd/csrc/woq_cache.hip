@@ -290,11 +290,13 @@ int cache_check(const woq_cache* c) {
 
 }  // namespace woq
 
-extern "C" int woq_cache_write(const woq_cache* c, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
-                               const int32_t* slots, int64_t b, const uint16_t* q, int64_t ldq, int32_t q_heads,
-                               uint16_t* q_out, int64_t ldq_out, const float* rope, int64_t n_pos, int32_t rot,
-                               int32_t interleaved, const int32_t* pos, void* stream) {
-    int rc = woq::cache_check(c);
+namespace woq {
+
+int cache_write_check(const woq_cache* c, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                      const int32_t* slots, int64_t b, const uint16_t* q, int64_t ldq, int32_t q_heads,
+                      const uint16_t* q_out, int64_t ldq_out, const float* rope, int64_t n_pos, int32_t rot,
+                      int32_t interleaved, const int32_t* pos) {
+    const int rc = cache_check(c);
     if (rc == WOQ_EINVAL || b < 0) return WOQ_EINVAL;
     const int64_t width = (int64_t)c->heads * c->dim;
     if (ldk < width || ldv < width) return WOQ_EINVAL;
@@ -307,10 +309,23 @@ extern "C" int woq_cache_write(const woq_cache* c, const uint16_t* k, int64_t ld
     if (b == 0) return WOQ_OK;
     if (!half_rows_ok(k, ldk) || !half_rows_ok(v, ldv) || ((uintptr_t)slots & 3u) ||
         (q && (!half_rows_ok(q, ldq) || !half_rows_ok(q_out, ldq_out))) ||
-        (rope && (!woq::aligned16(rope) || ((uintptr_t)pos & 3u))))
+        (rope && (!aligned16(rope) || ((uintptr_t)pos & 3u))))
         return WOQ_EALIGN;
-    const int64_t per_row = 2 * c->heads + (q ? q_heads : 0);
+    const int64_t per_row = 2 * (int64_t)c->heads + (q ? q_heads : 0);
     if ((rope && (rot & 15)) || b > INT32_MAX / per_row) return WOQ_EUNSUPPORTED;
+    return WOQ_OK;
+}
+
+}  // namespace woq
+
+extern "C" int woq_cache_write(const woq_cache* c, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                               const int32_t* slots, int64_t b, const uint16_t* q, int64_t ldq, int32_t q_heads,
+                               uint16_t* q_out, int64_t ldq_out, const float* rope, int64_t n_pos, int32_t rot,
+                               int32_t interleaved, const int32_t* pos, void* stream) {
+    const int rc = woq::cache_write_check(c, k, ldk, v, ldv, slots, b, q, ldq, q_heads, q_out, ldq_out, rope, n_pos,
+                                          rot, interleaved, pos);
+    if (rc || b == 0) return rc;
+    const int64_t per_row = 2 * (int64_t)c->heads + (q ? q_heads : 0);
     WriteArgs a;
     a.kc = static_cast<uint8_t*>(c->k);
     a.vc = static_cast<uint8_t*>(c->v);

@@ -33,7 +33,12 @@ int lora_check(const woq_lora_w* w, const uint16_t* x, int64_t ldx, const int32_
 // WOQ_EUNSUPPORTED in that order.
 int cache_check(const woq_cache* c);
 
-// The argument checks of woq_attn_decode, in its order; nothing is launched.
+// The argument checks of woq_cache_write and woq_attn_decode, in their order;
+// nothing is launched.
+int cache_write_check(const woq_cache* c, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                      const int32_t* slots, int64_t b, const uint16_t* q, int64_t ldq, int32_t q_heads,
+                      const uint16_t* q_out, int64_t ldq_out, const float* rope, int64_t n_pos, int32_t rot,
+                      int32_t interleaved, const int32_t* pos);
 int attn_check(const woq_cache* c, const uint16_t* q, int64_t ldq, int32_t q_heads, const int32_t* pages,
                int64_t ldpages, int64_t max_pages, const int32_t* lens, int64_t b, float scale, float softcap,
                int32_t window, const uint16_t* y, int64_t ldy, const void* workspace, int64_t workspace_bytes);

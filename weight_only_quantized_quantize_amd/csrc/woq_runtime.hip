@@ -268,6 +268,64 @@ int woq_stack_run_lora(woq_stack* st, const uint16_t* const* inputs, uint16_t* c
     return WOQ_OK;
 }
 
+int64_t woq_stack_attn_workspace(const woq_stack* st, const woq_stack_attn* const* attn, int64_t b) {
+    if (!st || !attn || b < 1 || b > st->max_b) return WOQ_EINVAL;
+    int64_t most = 16;
+    for (size_t i = 0; i < st->steps.size(); ++i) {
+        if (!attn[i]) continue;
+        const int64_t n = woq_attn_decode_workspace(attn[i]->cache, attn[i]->q_heads, b);
+        if (n < 0) return n;
+        most = std::max(most, n);
+    }
+    return most;
+}
+
+int woq_stack_run_attn(woq_stack* st, const uint16_t* const* inputs, uint16_t* const* outputs, int64_t b,
+                       const woq_stack_attn* const* attn, const int32_t* slots, const int32_t* pos,
+                       const int32_t* pages, int64_t ldpages, int64_t max_pages, const int32_t* lens,
+                       void* workspace, int64_t workspace_bytes, void* stream) {
+    if (!st || !inputs || !outputs || !attn || b < 1 || b > st->max_b) return WOQ_EINVAL;
+    // the step's rows hold q | k | v; q is turned in place
+    auto write = [&](const woq_stack_attn& t, uint16_t* y, int64_t N, bool check) {
+        const int64_t n = (int64_t)t.q_heads * t.cache->dim, m = (int64_t)t.cache->heads * t.cache->dim;
+        uint16_t* q = t.rope ? y : nullptr;
+        return check ? woq::cache_write_check(t.cache, y + n, N, y + n + m, N, slots, b, q, N, t.q_heads, q, N, t.rope,
+                                              t.n_pos, t.rot, t.interleaved, pos)
+                     : woq_cache_write(t.cache, y + n, N, y + n + m, N, slots, b, q, N, t.q_heads, q, N, t.rope, t.n_pos,
+                                       t.rot, t.interleaved, pos, stream);
+    };
+    for (size_t i = 0; i < st->steps.size(); ++i) {        // everything before the first launch
+        if (!attn[i]) continue;
+        const woq_stack_step& s = st->steps[i];
+        const woq_stack_attn& t = *attn[i];
+        const int64_t N = s.fmt == WOQ_FMT_INT4O ? s.w4.N : s.w8.N;
+        uint16_t* y = outputs[s.out_slot];
+        if (!t.cache || t.q_heads < 1 || !y || y == t.y || y == inputs[s.in_slot]) return WOQ_EINVAL;
+        if (((int64_t)t.q_heads + 2 * (int64_t)t.cache->heads) * t.cache->dim != N) return WOQ_EINVAL;
+        int rc = write(t, y, N, true);
+        if (rc == WOQ_OK)
+            rc = woq::attn_check(t.cache, y, N, t.q_heads, pages, ldpages, max_pages, lens, b, t.scale, t.softcap,
+                                 t.window, t.y, (int64_t)t.q_heads * t.cache->dim, workspace, workspace_bytes);
+        if (rc) return rc;
+    }
+    for (size_t i = 0; i < st->steps.size(); ++i) {
+        const woq_stack_step& s = st->steps[i];
+        uint16_t* y = outputs[s.out_slot];
+        int rc = run_step(st, i, s, inputs[s.in_slot], y, b, stream, nullptr);
+        if (rc == WOQ_OK && attn[i]) {
+            const woq_stack_attn& t = *attn[i];
+            const int64_t N = s.fmt == WOQ_FMT_INT4O ? s.w4.N : s.w8.N;
+            rc = write(t, y, N, false);
+            if (rc == WOQ_OK)
+                rc = woq_attn_decode(t.cache, y, N, t.q_heads, pages, ldpages, max_pages, lens, b, t.scale, t.softcap,
+                                     t.window, t.y, (int64_t)t.q_heads * t.cache->dim, workspace, workspace_bytes,
+                                     stream);
+        }
+        if (rc) return rc;
+    }
+    return WOQ_OK;
+}
+
 int woq_stack_time(woq_stack* st, const uint16_t* const* inputs, uint16_t* const* outputs, int64_t b, void* stream,
                    int32_t iters, float* step_ms, float* pass_ms) {
     if (!st || !inputs || !outputs || b < 1 || b > st->max_b || iters < 1 || !pass_ms ||

@@ -74,6 +74,12 @@ class Cache(ctypes.Structure):
     device = None       # index of the GPU that holds the cache, where it is known
 
 
+class StackAttn(ctypes.Structure):
+    _fields_ = [("cache", POINTER(Cache)), ("rope", c_void_p), ("y", c_void_p), ("n_pos", c_int64), ("scale", c_float),
+                ("softcap", c_float), ("q_heads", c_int32), ("rot", c_int32), ("interleaved", c_int32),
+                ("window", c_int32)]
+
+
 FMT_INT8, FMT_INT4O = 1, 2
 CACHE_FP16, CACHE_INT8 = 1, 2
 
@@ -134,6 +140,9 @@ _SIGS = {
     "woq_stack_run_lora": (c_int, [c_void_p, POINTER(c_void_p), POINTER(c_void_p), c_int64, POINTER(c_void_p),
                                    c_void_p, c_void_p, c_int64, c_void_p]),
     "woq_stack_lora_workspace": (c_int64, [c_void_p, POINTER(c_void_p), c_int64]),
+    "woq_stack_run_attn": (c_int, [c_void_p, POINTER(c_void_p), POINTER(c_void_p), c_int64, POINTER(c_void_p), c_void_p,
+                                   c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_int64, c_void_p]),
+    "woq_stack_attn_workspace": (c_int64, [c_void_p, POINTER(c_void_p), c_int64]),
     "woq_stack_launches": (c_int, [c_void_p, c_int64, POINTER(c_int32)]),
     "woq_stack_time": (c_int, [c_void_p, POINTER(c_void_p), POINTER(c_void_p), c_int64, c_void_p, c_int32,
                                POINTER(c_float), POINTER(c_float)]),
@@ -866,6 +875,30 @@ class DeviceCache:
         return cls(k, v, *(_torch.empty(shape[:3], dtype=f32, device=device) for _ in range(2)))
 
 
+class StackAttention:
+    """The attention behind a step of a Stack (woq_stack_attn), which keeps its
+    tensors: a DeviceCache, the result's rows y (fp16 [>= b, q_heads * dim],
+    contiguous) and, optionally, the angles ``rope`` (fp32 [positions, rot])."""
+
+    def __init__(self, cache, y, rope=None, interleaved: bool = False, scale: float | None = None,
+                 softcap: float = 0.0, window: int = 0):
+        _lib()
+        self.cache, self.y, self.rope = cache, y, rope
+        dim = cache.desc.dim
+        if y.dim() != 2 or y.shape[1] % dim or rope is not None and rope.dim() != 2:
+            raise ValueError(f"y is [rows, heads of {dim}], rope [positions, rot]")
+        if y.device != cache.k.device or rope is not None and rope.device != y.device:
+            raise ValueError("the cache, y and rope have to be on one GPU")
+        d = self.desc = StackAttn()
+        d.cache = ctypes.pointer(cache.desc)
+        d.y = _vector(y, "y", _torch.float16, 0)
+        if rope is not None:
+            d.rope = _vector(rope, "rope", _torch.float32, 0)
+            d.n_pos, d.rot = rope.shape
+        d.q_heads, d.interleaved = y.shape[1] // dim, int(interleaved)
+        d.scale, d.softcap, d.window = dim ** -0.5 if scale is None else scale, softcap, window
+
+
 # ------------------------------------------------------------- stack runner
 
 class Stack:
@@ -918,6 +951,35 @@ class Stack:
               b, self._pools(adapters), _vector(ids, "ids", _torch.int32, b), workspace.data_ptr(),
               workspace.numel() * workspace.element_size(),
               held=[(f"the pool of step {i}", p.desc.device) for i, p in enumerate(adapters) if p is not None])
+
+    def _attentions(self, attn):
+        if len(attn) != self.n:
+            raise ValueError(f"{len(attn)} attentions for {self.n} steps")
+        return (c_void_p * max(1, self.n))(*[None if a is None else ctypes.addressof(a.desc) for a in attn])
+
+    def attn_workspace(self, attn, b: int) -> int:
+        """Bytes of the workspace of run_attn for batches of up to b rows."""
+        n = _lib().woq_stack_attn_workspace(self.handle, self._attentions(attn), b)
+        if n < 0:
+            _check(n, "woq_stack_attn_workspace")
+        return n
+
+    def run_attn(self, b: int, attn, slots, pages, lens, workspace, pos=None, stream=None):
+        """run with the attention of a decode step between its steps: ``attn``
+        holds a StackAttention, or None, for every step, applied to the rows
+        that step has written; slots, lens and pos (int32 [b]) and pages (int32
+        [b, W]) as for woq_cache_write and woq_attn_decode."""
+        need_rows(b, *self._in, *self._out, *[a.y for a in attn if a is not None])
+        if not workspace.is_contiguous():
+            raise ValueError("workspace: must be contiguous")
+        i32, W = _torch.int32, pages.shape[1]
+        tp, ldt = _rows(pages, "pages", i32, b, W)
+        held = [(f"the cache of step {i}", a.cache.desc.device) for i, a in enumerate(attn) if a is not None]
+        held += [(f"the attention of step {i}", a.y.get_device()) for i, a in enumerate(attn) if a is not None]
+        _call("woq_stack_run_attn", stream, (*self._in, *self._out, slots, pos, pages, lens, workspace), self.handle,
+              self._pin, self._pout, b, self._attentions(attn), _vector(slots, "slots", i32, b),
+              _optional(pos, "pos", i32, b), tp, ldt, W, _vector(lens, "lens", i32, b), workspace.data_ptr(),
+              workspace.numel() * workspace.element_size(), held=held)
 
     def launches(self, b: int) -> int:
         n = c_int32()
