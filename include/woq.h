@@ -606,8 +606,9 @@ int woq_cache_read(const woq_cache* c, const int32_t* slots, int64_t n, uint16_t
  * same leading dimension.  workspace: at least woq_attn_decode_workspace bytes of device memory,
  * 16-byte aligned, owned by the caller, its contents on return unspecified;
  * calls that share it must not overlap.  Deterministic for given inputs on one
- * device model.  q_heads <= WOQ_ATTN_MAX_HEADS, b <= WOQ_ATTN_MAX_ROWS, b *
- * q_heads < 2^24, max_pages * page < 2^31; b = 0 is a no-op.
+ * device model.  q_heads <= WOQ_ATTN_MAX_HEADS, b <= WOQ_ATTN_MAX_ROWS,
+ * max_pages * page < 2^31, and b * heads * ceil(q_heads / heads / 16) * (max_pages *
+ * page / 32 + 1) < 2^31; b = 0 is a no-op.
  */
 #define WOQ_ATTN_MAX_HEADS 4096
 #define WOQ_ATTN_MAX_ROWS 65536

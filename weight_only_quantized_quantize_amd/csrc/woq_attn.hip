@@ -58,21 +58,32 @@ struct AttnArgs {
     int heads, group, page, dim, window, b, tiles, per_tile, groups, spread;
 };
 
+// Sum over the lanes up to this one: in rows of 16, then from row to row.
+__device__ __forceinline__ int wave_upto(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, true);
+    return v;
+}
+
 // What row r sees: tokens first .. len - 1, in sixteens s0 .. s1 - 1 and units of
 // two of them.
 struct Span {
     int len, first, s0, s1, units;
 };
-__device__ __forceinline__ Span span_of(const AttnArgs& a, int r) {
+__device__ __forceinline__ Span span_from(const AttnArgs& a, int len) {
     Span s;
-    const int64_t len = min((int64_t)max(*gptr(a.lens + r), 0), a.capacity);
-    s.len = (int)len;
+    s.len = (int)min((int64_t)max(len, 0), a.capacity);
     s.first = a.window > 0 ? max(0, s.len - a.window) : 0;
     s.s0 = s.first >> 4;
-    s.s1 = (int)((len + 15) >> 4);
+    s.s1 = (int)(((uint32_t)s.len + 15) >> 4);
     s.units = (s.s1 - s.s0 + 1) >> 1;
     return s;
 }
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int r) { return span_from(a, *gptr(a.lens + r)); }
 
 // The bytes that a lane loads of a sixteen of tokens: of the keys 16 bytes of one
 // token's row at a time (token lane % 16), of the values its E = DP / 16 channels of
@@ -113,7 +124,7 @@ template <int N>
 struct Parts {
     int row[N], head[N];                      // row -1: none; key head and tile
     int begins[N], ends[N];                   // whether the part holds the span's first and last unit
-    int64_t stop[N];                          // the position behind the span
+    int stop[N];                              // the position behind the span
     float ref[N][16], sum[N][16];
 };
 
@@ -152,61 +163,73 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
     constexpr int ROW = DP + 4;               // floats of a head in LDS: 16 heads in different banks
     extern __shared__ __align__(16) float join[];              // [PARTS][per_tile][ROW]
     __shared__ Parts<PARTS> parts;
-    __shared__ int64_t scan[WAVES], found[WAVES][2];
+    __shared__ int scan[WAVES], found[WAVES][2];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m = lane & 15, g = lane >> 4, HH = a.heads * a.tiles;
 
-    int64_t pos, end, base, per = 0;          // this wave's positions; where its row's begin
+    int pos, end, base, per = 0;              // this wave's positions (fewer than 2^31); where its row's begin
     int r, hh = 0, ub = 0;                    // its row, key head and tile, and first unit there
     Span sp;
+    // lengths of up to 64 rows stay in the wave's lanes
+    const int lane_len = FLAT && a.b <= 64 ? *gptr(a.lens + min(lane, a.b - 1)) : 0;
+    auto span = [&](int r) {
+        return span_from(a, a.b <= 64 ? __builtin_amdgcn_readlane(lane_len, r)
+                                      : __builtin_amdgcn_readfirstlane(*gptr(a.lens + r)));
+    };
     if constexpr (FLAT) {
-        int64_t mine = 0, before = 0, total = 0;
-        const int each = (a.b + T - 1) / T, lo = min(a.b, tid * each), hi = min(a.b, lo + each);
-        for (int i = lo; i < hi; ++i) mine += span_of(a, i).units;
-        int64_t s = mine;
+        const int groups = (int)gridDim.x;
+        int first, last, share;
+        auto divide = [&](int total) {        // false: nothing is left for this workgroup
+            const int positions = total * HH;
+            per = max(WAVES, (int)(((uint32_t)positions + groups - 1) / (uint32_t)groups));
+            first = (int)min((int64_t)positions, (int64_t)blockIdx.x * per);
+            last = min(positions - first, per) + first;
+            share = (last - first + WAVES - 1) / WAVES;
+            pos = min(last, first + wave * share);
+            end = min(last, pos + share);
+            if (first == last && tid == 0) a.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+            return first < last;
+        };
+        if (a.b <= 64) {                      // a row to a lane: nothing to exchange between waves
+            const int n = lane < a.b ? span_from(a, lane_len).units : 0, upto = wave_upto(n);
+            if (!divide(__builtin_amdgcn_readlane(upto, 63))) return;
+            r = pos < end ? (int)__builtin_popcountll(__ballot(upto * HH <= pos)) : 0;
+            base = r ? __builtin_amdgcn_readlane(upto, r - 1) * HH : 0;
+        } else {
+            int mine = 0, total = 0;
+            const int each = (a.b + T - 1) / T, lo = min(a.b, tid * each), hi = min(a.b, lo + each);
+            for (int i = lo; i < hi; ++i) mine += span_of(a, i).units;
+            const int upto = wave_upto(mine);
+            if (lane == 63) scan[wave] = upto;
+            __syncthreads();
+            int before = upto - mine;
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int64_t o = __shfl_up(s, d);
-            if (lane >= d) s += o;
-        }
-        if (lane == 63) scan[wave] = s;
-        __syncthreads();
-        before = s - mine;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-            if (w < wave) before += scan[w];
-            total += scan[w];
-        }
-        const int64_t positions = total * HH;
-        per = max((int64_t)WAVES, (positions + gridDim.x - 1) / gridDim.x);
-        const int64_t first = blockIdx.x * per, last = min(positions, first + per);
-        if (first >= last) {
-            if (tid == 0) a.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
-            return;
-        }
-        const int64_t share = (last - first + WAVES - 1) / WAVES;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-            const int64_t p = first + w * share;
-            if (p >= last || p < before * HH || p >= (before + mine) * HH) continue;
-            int64_t at = before;
-            int i = lo;
-            for (; i < hi - 1; ++i) {
-                const int n = span_of(a, i).units;
-                if (p < (at + n) * HH) break;
-                at += n;
+            for (int w = 0; w < WAVES; ++w) {
+                if (w < wave) before += scan[w];
+                total += scan[w];
             }
-            found[w][0] = i, found[w][1] = at;
+            if (!divide(total)) return;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) {
+                const int p = first + w * share;
+                if (p >= last || p < before * HH || p >= (before + mine) * HH) continue;
+                int at = before, i = lo;
+                for (; i < hi - 1; ++i) {
+                    const int n = span_of(a, i).units;
+                    if (p < (at + n) * HH) break;
+                    at += n;
+                }
+                found[w][0] = i, found[w][1] = at;
+            }
+            __syncthreads();
+            r = pos < end ? __builtin_amdgcn_readfirstlane(found[wave][0]) : 0;
+            base = pos < end ? __builtin_amdgcn_readfirstlane(found[wave][1]) * HH : 0;
         }
-        __syncthreads();
-        pos = first + wave * share;
-        end = min(last, pos + share);
-        r = pos < end ? __builtin_amdgcn_readfirstlane((int)found[wave][0]) : 0;
-        base = pos < end ? found[wave][1] * HH : 0;
-        sp = span_of(a, r);
+        sp = span(r);
         if (pos < end) {
-            hh = __builtin_amdgcn_readfirstlane((int)((pos - base) / sp.units));
-            ub = __builtin_amdgcn_readfirstlane((int)(pos - base - (int64_t)hh * sp.units));
+            const int rel = pos - base;
+            hh = __builtin_amdgcn_readfirstlane((int)((uint32_t)rel / (uint32_t)sp.units));
+            ub = rel - hh * sp.units;
         }
     } else {
         r = blockIdx.x / HH;
@@ -263,7 +286,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
 
     int part = 0;
     for (; pos < end; ++hh, ub = 0) {
-        const int ue = FLAT ? (int)min((int64_t)sp.units, ub + (end - pos)) : 0;
+        const int ue = FLAT ? min(sp.units, ub + (end - pos)) : 0;
         const int n = FLAT ? ue - ub : (sp.units - wave + WAVES - 1) / WAVES;      // units of this wave here
         const int h = hh / a.tiles, tile = hh - h * a.tiles;
         const int heads = min(16, a.group - 16 * tile);          // query heads of this tile
@@ -473,7 +496,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
             if (lane == 0) {
                 parts.row[at] = r, parts.head[at] = hh;
                 parts.begins[at] = begins, parts.ends[at] = ends;
-                parts.stop[at] = base + (int64_t)(hh + 1) * sp.units;
+                parts.stop[at] = base + (hh + 1) * sp.units;
             }
             if (g == 0) parts.ref[at][m] = top, parts.sum[at][m] = sum;
             if (m < heads) {
@@ -491,7 +514,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
             hh = -1;
             do {
                 ++r;
-                sp = span_of(a, r);
+                sp = span(r);
             } while (sp.units == 0);
         }
     }
@@ -511,7 +534,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
         const bool begins = parts.begins[k0], ends = parts.ends[63 - __builtin_clzll(these)];
         const int64_t slot = 2 * (int64_t)blockIdx.x + begins;
         if (FLAT && begins && !ends)
-            cut = make_int4(row, hh, (int)((parts.stop[k0] - 1) / per - blockIdx.x) + 1, 0);
+            cut = make_int4(row, hh, (parts.stop[k0] - 1) / per - (int)blockIdx.x + 1, 0);
         for (int i = tid; i < heads * (DP / 4); i += T) {
             const int hq = i / (DP / 4), d = 4 * (i - hq * (DP / 4));
             if (!EXACT && d >= dim) continue;
@@ -625,9 +648,13 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 // Workgroups of a split: as many as keep two on a compute unit.
 int workgroups() { return 2 * woq::compute_units(); }
 
-// Where the capacity is no more than this and the spans are no more than the
-// workgroups, each takes one whole and there is nothing to join.
-constexpr int64_t DIRECT = 512;
+// Where the capacity is no more than this (twice as much from a quarter as many spans as
+// workgroups) and the spans are no more than the workgroups, each takes one whole and
+// there is nothing to join.  Rows of up to 1024 tokens, 8 heads of 128, 64 queries:
+// 1 row 12 us against 8 + 4 for two launches, 32 rows 14.5 against 16 + 5; of up to 2048
+// 8 rows 20 against 11.5 + 6, 32 rows 23 against 22 + 6; 256 rows of up to 512 (2048
+// spans) 54 against 42 + 5.
+constexpr int64_t DIRECT = 1024;
 
 struct Layout {
     int64_t sums, stats, bytes;
@@ -684,10 +711,11 @@ int attn_check(const woq_cache* c, const uint16_t* q, int64_t ldq, int32_t q_hea
     if (!half_rows_ok(q, ldq) || !half_rows_ok(y, ldy) || ((uintptr_t)pages & 3u) || ((uintptr_t)lens & 3u) ||
         !aligned16(workspace))
         return WOQ_EALIGN;
-    // the launch that joins has 256 threads for every row and head, fewer than 2^32
-    if (q_heads > WOQ_ATTN_MAX_HEADS || b > WOQ_ATTN_MAX_ROWS || b * q_heads >= 1 << 24 ||
-        max_pages > INT32_MAX / c->page)
+    if (q_heads > WOQ_ATTN_MAX_HEADS || b > WOQ_ATTN_MAX_ROWS || max_pages > INT32_MAX / c->page)
         return WOQ_EUNSUPPORTED;
+    // positions are 32 bits wide
+    const int64_t units = max_pages * c->page / 32 + 1, spans = (int64_t)c->heads * ceil_div(q_heads / c->heads, 16);
+    if (units > INT32_MAX / (b * spans)) return WOQ_EUNSUPPORTED;
     if (workspace_bytes < woq_attn_decode_workspace(c, q_heads, b)) return WOQ_EINVAL;
     return WOQ_OK;
 }
@@ -698,7 +726,7 @@ extern "C" int64_t woq_attn_decode_workspace(const woq_cache* c, int32_t q_heads
     const int rc = woq::cache_check(c);
     if (rc == WOQ_EINVAL || b < 0 || q_heads < 1 || q_heads % c->heads) return WOQ_EINVAL;
     if (rc) return rc;
-    if (q_heads > WOQ_ATTN_MAX_HEADS || b > WOQ_ATTN_MAX_ROWS || b * q_heads >= 1 << 24) return WOQ_EUNSUPPORTED;
+    if (q_heads > WOQ_ATTN_MAX_HEADS || b > WOQ_ATTN_MAX_ROWS) return WOQ_EUNSUPPORTED;
     return layout(c, q_heads).bytes;
 }
 
@@ -745,7 +773,7 @@ extern "C" int woq_attn_decode(const woq_cache* c, const uint16_t* q, int64_t ld
     void* argv[] = {&a};
     hipStream_t s = (hipStream_t)stream;
     const int64_t spans = b * c->heads * l.tiles;
-    const bool flat = a.capacity > DIRECT || spans > workgroups();
+    const bool flat = spans > workgroups() || a.capacity > (spans * 4 > workgroups() ? 2 * DIRECT : DIRECT);
     const Kernel k = c->fmt == WOQ_CACHE_INT8 ? split_kernel<true>(c->dim, flat) : split_kernel<false>(c->dim, flat);
     const size_t lds = (size_t)(flat ? 2 : 1) * k.waves * l.per_tile * (k.dim + 4) * 4;
     const unsigned grid = flat ? (unsigned)workgroups() : (unsigned)spans;
