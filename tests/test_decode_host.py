@@ -158,7 +158,9 @@ def test_read_refusals(change, status):
     (dict(y=P + 4096, ldy=260), EALIGN), (dict(y=P + 4096, ldq=260), EALIGN), (dict(pages=P + 2), EALIGN),
     (dict(lens=P + 1), EALIGN), (dict(ws=P + 8), EALIGN), (dict(b=65537), EUNSUPPORTED),
     (dict(b=1 << 40), EUNSUPPORTED), (dict(q_heads=4098, ldq=1 << 20, ldy=1 << 20), EUNSUPPORTED),
-    (dict(max_pages=1 << 27, ldpages=1 << 27), EUNSUPPORTED), (dict(b=0, q=None, lens=None, y=None, ws=None), OK),
+    (dict(max_pages=1 << 27, ldpages=1 << 27), EUNSUPPORTED), (dict(max_pages=(1 << 26) + 1, ldpages=1 << 27), EUNSUPPORTED),
+    (dict(max_pages=1 << 24, ldpages=1 << 24, b=65536), EUNSUPPORTED), (dict(scale=1e32), EUNSUPPORTED),
+    (dict(scale=1.0, softcap=1e-38), EUNSUPPORTED), (dict(b=0, q=None, lens=None, y=None, ws=None), OK),
 ])
 def test_attention_refusals(change, status):
     a = dict(c=cache(), q=P, ldq=256, q_heads=4, pages=P, ldpages=5, max_pages=5, lens=P, b=3, scale=0.1, softcap=0.0,

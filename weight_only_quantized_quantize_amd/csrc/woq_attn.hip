@@ -55,7 +55,7 @@ struct AttnArgs {
     float* stats;             // [2 * workgroups][16][2]: the reference of the weights, their sum
     int64_t ldq, ldpages, ldy, n_pages, capacity;
     float factor, cap;        // of the scores in powers of two, see the launch
-    int heads, group, page, dim, window, b, tiles, per_tile, groups, spread;
+    int heads, group, page, dim, window, b, tiles, per_tile, groups;
 };
 
 // Sum over the lanes up to this one: in rows of 16, then from row to row.
@@ -84,6 +84,13 @@ __device__ __forceinline__ Span span_from(const AttnArgs& a, int len) {
     return s;
 }
 __device__ __forceinline__ Span span_of(const AttnArgs& a, int r) { return span_from(a, *gptr(a.lens + r)); }
+
+// Positions of a workgroup of the split: an equal share, a unit to each of four waves at
+// least.
+constexpr int FLAT_WAVES = 4;
+__device__ __forceinline__ int per_group(int positions, int groups) {
+    return max(FLAT_WAVES, (int)(((uint32_t)positions + groups - 1) / (uint32_t)groups));
+}
 
 // The bytes that a lane loads of a sixteen of tokens: of the keys 16 bytes of one
 // token's row at a time (token lane % 16), of the values its E = DP / 16 channels of
@@ -181,7 +188,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
         int first, last, share;
         auto divide = [&](int total) {        // false: nothing is left for this workgroup
             const int positions = total * HH;
-            per = max(WAVES, (int)(((uint32_t)positions + groups - 1) / (uint32_t)groups));
+            per = per_group(positions, groups);
             first = (int)min((int64_t)positions, (int64_t)blockIdx.x * per);
             last = min(positions - first, per) + first;
             share = (last - first + WAVES - 1) / WAVES;
@@ -571,41 +578,60 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
     if (FLAT && tid == 0) a.cuts[blockIdx.x] = cut;
 }
 
-// The span that a workgroup of the split began and others went on with, one of its
-// heads: their parts in order, each under the power of two of its own.  And the rows that see
-// nothing, which are zeros.
+// Joins the parts of the spans that were cut, in order, each under the power of two of
+// its own, and writes the zeros of rows that see nothing.  Few spans (FEW) are long and
+// have many parts: a workgroup for every span and head.  Otherwise a workgroup for every
+// one of the split: it joins the span that that one began and others went on with, all
+// heads at once as far as the threads go.  (A workgroup for every cut and head: 6 us
+// where this takes 4, and 16 where it takes 6, most of it for those that find nothing.)
+template <bool FEW>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     __shared__ __align__(16) float red[16][WOQ_CACHE_MAX_DIM];
     __shared__ float red_l[16], red_m[16];
-    // parts are read on the XCD that wrote the first of them, but of long rows, which
-    // begin at every 32nd or 64th workgroup, all would be read on one
-    const int tid = threadIdx.x, hq = blockIdx.x / a.groups, i = blockIdx.x - hq * a.groups;
-    const int wg = a.spread ? i ^ (i >> 6 & 63) : i;
-    if (hq == 0) {
-        const int n = a.heads * a.group * a.dim;
+    const int tid = threadIdx.x, lane = tid & 63, q_heads = a.heads * a.group, HH = a.heads * a.tiles;
+    int wg = blockIdx.x, only = -1;           // whose cut this is, and the one head of it
+    if constexpr (FEW) {
+        const int span = blockIdx.x / a.per_tile, r = span / HH, hh = span - r * HH;
+        const int tile = hh % a.tiles, h = hh / a.tiles;
+        only = blockIdx.x - span * a.per_tile;
+        if (only >= min(16, a.group - 16 * tile)) return;
+        // as the split divides: at most 64 rows
+        const int len = *gptr(a.lens + min(lane, a.b - 1));
+        const int n = lane < a.b ? span_from(a, len).units : 0, upto = wave_upto(n);
+        const int positions = __builtin_amdgcn_readlane(upto, 63) * HH, units = __builtin_amdgcn_readlane(n, r);
+        if (units == 0) {
+            for (int d = tid; d < a.dim; d += 256)
+                *gptr(a.y + r * a.ldy + (int64_t)(h * a.group + 16 * tile + only) * a.dim + d) = 0;
+            return;
+        }
+        const int per = per_group(positions, a.groups);
+        const int p0 = (__builtin_amdgcn_readlane(upto, r) - units) * HH + hh * units;
+        wg = p0 / per;
+        if (wg == (p0 + units - 1) / per) return;
+    } else {
         for (int r = wg; r < a.b; r += a.groups) {
             if (span_of(a, r).units) continue;
-            for (int d = tid; d < n; d += 256) *gptr(a.y + r * a.ldy + d) = 0;
+            for (int d = tid; d < q_heads * a.dim; d += 256) *gptr(a.y + r * a.ldy + d) = 0;
         }
     }
     const int4 cut = a.cuts[wg];
     if (cut.z == 0) return;
-    const int h = cut.y / a.tiles, tile = cut.y - h * a.tiles;
-    if (hq >= min(16, a.group - 16 * tile)) return;
-    // four channels to a thread, every 4th, 8th or 16th part to a wave or part of one,
-    // eight parts in flight
+    const int h = cut.y / a.tiles, tile = cut.y - h * a.tiles, heads = min(16, a.group - 16 * tile);
+    uint16_t* out = a.y + cut.x * a.ldy + (int64_t)(h * a.group + 16 * tile) * a.dim;
+    // four channels to a thread
     const int lanes = a.dim <= 64 ? 16 : a.dim <= 128 ? 32 : 64, parts = 256 / lanes;
     const int part = tid / lanes, d = 4 * (tid - part * lanes);
-    float ref = NONE, l = 0.0f;
-    f4 o = {0, 0, 0, 0};
-    auto some = [&](auto count, int i0) {
+    float ref, l;
+    f4 o;
+    // N parts of head hq in flight: i0, i0 + step, ...
+    auto some = [&](auto count, int hq, int i0, int step) {
         constexpr int N = decltype(count)::value;
         u32x2 st[N];
         f4 v[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             // the first workgroup's part is its second, the others' their first
-            const int i = min(i0 + j * parts, cut.z - 1);
+            const int i = min(i0 + j * step, cut.z - 1);
             const int64_t slot = 2 * ((int64_t)wg + i) + (i == 0);
             st[j] = *(g_u32x2*)(a.stats + (slot * 16 + hq) * 2);
             v[j] = *(__attribute__((address_space(1))) const f4*)(a.sums + (slot * a.per_tile + hq) * a.dim + min(d, a.dim - 4));
@@ -619,41 +645,55 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
         ref = next;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            if (i0 + j * parts >= cut.z) continue;
+            if (i0 + j * step >= cut.z) continue;
             const float keep = __builtin_amdgcn_exp2f(__uint_as_float(st[j][0]) - zero);
             l = fmaf(__uint_as_float(st[j][1]), keep, l);
             o += v[j] * keep;
         }
     };
-    if (cut.z <= parts) {
-        if (part < cut.z) some(std::integral_constant<int, 1>{}, part);
-    } else {
-        for (int i0 = part; i0 < cut.z; i0 += 8 * parts) some(std::integral_constant<int, 8>{}, i0);
+    if (!FEW && cut.z <= 16) {
+        for (int hq = part; hq < heads; hq += parts) {
+            ref = NONE, l = 0.0f, o = f4{0, 0, 0, 0};
+            for (int i = 0; i < cut.z; i += 4) some(std::integral_constant<int, 4>{}, hq, i, 1);
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            if (d < a.dim)
+                *(__attribute__((address_space(1))) u32x2*)(out + hq * a.dim + d) =
+                    u32x2{(uint32_t)f_to_h(o[0] * inv) | (uint32_t)f_to_h(o[1] * inv) << 16,
+                          (uint32_t)f_to_h(o[2] * inv) | (uint32_t)f_to_h(o[3] * inv) << 16};
+        }
+        return;
     }
-    if (d < a.dim) *reinterpret_cast<f4*>(&red[part][d]) = o;
-    if (d == 0) red_l[part] = l, red_m[part] = ref;
-    __syncthreads();
-    if (tid >= a.dim) return;
-    float all = NONE, s = 0.0f, t = 0.0f;
-    for (int i = 0; i < parts; ++i) all = fmaxf(all, red_m[i]);
-    if (all == NONE) all = 0.0f;
-    for (int i = 0; i < parts; ++i) {
-        const float keep = __builtin_amdgcn_exp2f(red_m[i] - all);
-        s = fmaf(red[i][tid], keep, s);
-        t = fmaf(red_l[i], keep, t);
+    for (int hq = FEW ? only : 0; hq < (FEW ? only + 1 : heads); ++hq) {
+        ref = NONE, l = 0.0f, o = f4{0, 0, 0, 0};
+        for (int i = part; i < cut.z; i += 8 * parts) some(std::integral_constant<int, 8>{}, hq, i, parts);
+        if (d < a.dim) *reinterpret_cast<f4*>(&red[part][d]) = o;
+        if (d == 0) red_l[part] = l, red_m[part] = ref;
+        __syncthreads();
+        if (tid < a.dim) {
+            float all = NONE, s = 0.0f, t = 0.0f;
+            for (int i = 0; i < parts; ++i) all = fmaxf(all, red_m[i]);
+            if (all == NONE) all = 0.0f;
+            for (int i = 0; i < parts; ++i) {
+                const float keep = __builtin_amdgcn_exp2f(red_m[i] - all);
+                s = fmaf(red[i][tid], keep, s);
+                t = fmaf(red_l[i], keep, t);
+            }
+            *gptr(out + hq * a.dim + tid) = f_to_h(t == 0.0f ? 0.0f : s / t);
+        }
+        if (!FEW) __syncthreads();
     }
-    *gptr(a.y + cut.x * a.ldy + (int64_t)(h * a.group + 16 * tile + hq) * a.dim + tid) = f_to_h(t == 0.0f ? 0.0f : s / t);
 }
 
 // Workgroups of a split: as many as keep two on a compute unit.
 int workgroups() { return 2 * woq::compute_units(); }
 
-// Where the capacity is no more than this (twice as much from a quarter as many spans as
-// workgroups) and the spans are no more than the workgroups, each takes one whole and
-// there is nothing to join.  Rows of up to 1024 tokens, 8 heads of 128, 64 queries:
-// 1 row 12 us against 8 + 4 for two launches, 32 rows 14.5 against 16 + 5; of up to 2048
-// 8 rows 20 against 11.5 + 6, 32 rows 23 against 22 + 6; 256 rows of up to 512 (2048
-// spans) 54 against 42 + 5.
+// Where the capacity is no more than this and the spans are no more than the
+// workgroups, each takes one whole and there is nothing to join; twice as much where
+// the spans are a quarter to a half of the workgroups.  64 queries over 8 heads of 128,
+// rows of up to 1024: 4 rows 12.8 us against 7.3 + 4.2 and a launch between them, 32
+// rows 14.1 against 15.1 + 4.2, 64 rows 25.6 against 23.0 + 4.2; of up to 2048: 16 rows
+// 21.3 against 14.2 + 4.2, 32 rows 23.0 against 20.7 + 4.2, 64 rows 40.8 against 33.9 +
+// 4.2; 256 rows of up to 512 (2048 spans) 54 against 42 + 4.8.
 constexpr int64_t DIRECT = 1024;
 
 struct Layout {
@@ -678,7 +718,7 @@ struct Kernel {
 template <int DP, bool INT8>
 Kernel split_kernel(int dim, bool flat) {
 #define WOQ_ATTN(E, W, F) Kernel{reinterpret_cast<const void*>(&attn_split_kernel<DP, INT8, E, W, F>), W, DP}
-    if (flat) return dim == DP ? WOQ_ATTN(true, 4, true) : WOQ_ATTN(false, 4, true);
+    if (flat) return dim == DP ? WOQ_ATTN(true, FLAT_WAVES, true) : WOQ_ATTN(false, FLAT_WAVES, true);
     constexpr int W = DP == 256 ? 4 : 8;
     return dim == DP ? WOQ_ATTN(true, W, false) : WOQ_ATTN(false, W, false);
 #undef WOQ_ATTN
@@ -688,6 +728,14 @@ Kernel split_kernel(int dim, bool flat) {
     return dim <= 64    ? split_kernel<64, INT8>(dim, flat)
            : dim <= 128 ? split_kernel<128, INT8>(dim, flat)
                         : split_kernel<256, INT8>(dim, flat);
+}
+
+// Scores are in units of log2: factor s, or cap (1 - 2 / (1 + 2^(factor s))), with s the
+// product of a query and a key's bytes as they are.
+constexpr double LOG2E = 1.4426950408889634;
+float score_factor(const woq_cache* c, float scale, float softcap) {
+    const double step = c->fmt == WOQ_CACHE_INT8 ? STEP : 1.0;
+    return (float)(step * LOG2E * scale * (softcap > 0.0f ? 2.0 / softcap : 1.0));
 }
 
 bool half_rows_ok(const void* p, int64_t ld) { return woq::aligned16(p) && (ld & 7) == 0; }
@@ -711,11 +759,12 @@ int attn_check(const woq_cache* c, const uint16_t* q, int64_t ldq, int32_t q_hea
     if (!half_rows_ok(q, ldq) || !half_rows_ok(y, ldy) || ((uintptr_t)pages & 3u) || ((uintptr_t)lens & 3u) ||
         !aligned16(workspace))
         return WOQ_EALIGN;
-    if (q_heads > WOQ_ATTN_MAX_HEADS || b > WOQ_ATTN_MAX_ROWS || max_pages > INT32_MAX / c->page)
+    // tokens and positions are 32 bits wide, with room for sums of two
+    if (q_heads > WOQ_ATTN_MAX_HEADS || b > WOQ_ATTN_MAX_ROWS || max_pages > WOQ_ATTN_MAX_TOKENS / c->page)
         return WOQ_EUNSUPPORTED;
-    // positions are 32 bits wide
     const int64_t units = max_pages * c->page / 32 + 1, spans = (int64_t)c->heads * ceil_div(q_heads / c->heads, 16);
-    if (units > INT32_MAX / (b * spans)) return WOQ_EUNSUPPORTED;
+    if (units > WOQ_ATTN_MAX_TOKENS / (b * spans)) return WOQ_EUNSUPPORTED;
+    if (!std::isfinite(score_factor(c, scale, softcap))) return WOQ_EUNSUPPORTED;
     if (workspace_bytes < woq_attn_decode_workspace(c, q_heads, b)) return WOQ_EINVAL;
     return WOQ_OK;
 }
@@ -751,10 +800,8 @@ extern "C" int woq_attn_decode(const woq_cache* c, const uint16_t* q, int64_t ld
     a.ldy = ldy;
     a.n_pages = c->n_pages;
     a.capacity = max_pages * c->page;
-    // scores are in units of log2: cap (1 - 2 / (1 + 2^(factor s))) or factor s
-    const double log2e = 1.4426950408889634, step = c->fmt == WOQ_CACHE_INT8 ? STEP : 1.0;
-    a.factor = (float)(step * log2e * scale * (softcap > 0.0f ? 2.0 / softcap : 1.0));
-    a.cap = (float)(log2e * softcap);
+    a.factor = score_factor(c, scale, softcap);
+    a.cap = (float)(LOG2E * softcap);
     a.heads = c->heads;
     a.group = q_heads / c->heads;
     a.page = c->page;
@@ -769,20 +816,22 @@ extern "C" int woq_attn_decode(const woq_cache* c, const uint16_t* q, int64_t ld
     a.tiles = l.tiles;
     a.per_tile = l.per_tile;
     a.groups = workgroups();
-    a.spread = b * c->heads * l.tiles * 8 <= a.groups && a.groups % 64 == 0;
     void* argv[] = {&a};
     hipStream_t s = (hipStream_t)stream;
     const int64_t spans = b * c->heads * l.tiles;
-    const bool flat = spans > workgroups() || a.capacity > (spans * 4 > workgroups() ? 2 * DIRECT : DIRECT);
+    const bool flat = spans > workgroups() || a.capacity > (spans * 4 > workgroups() && spans * 2 <= workgroups() ? 2 * DIRECT : DIRECT);
     const Kernel k = c->fmt == WOQ_CACHE_INT8 ? split_kernel<true>(c->dim, flat) : split_kernel<false>(c->dim, flat);
     const size_t lds = (size_t)(flat ? 2 : 1) * k.waves * l.per_tile * (k.dim + 4) * 4;
     const unsigned grid = flat ? (unsigned)workgroups() : (unsigned)spans;
     hipError_t e = hipSuccess;
     if (lds > 64 << 10) e = hipFuncSetAttribute(k.f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e == hipSuccess) e = hipLaunchKernel(k.f, dim3(grid), dim3(64 * k.waves), argv, lds, s);
-    if (e == hipSuccess && flat)
-        e = hipLaunchKernel(reinterpret_cast<const void*>(&attn_join_kernel), dim3(grid * l.per_tile),
-                            dim3(256), argv, 0, s);
+    if (e == hipSuccess && flat) {
+        const bool few = b <= 64 && spans * 8 <= workgroups();
+        e = hipLaunchKernel(few ? reinterpret_cast<const void*>(&attn_join_kernel<true>)
+                                : reinterpret_cast<const void*>(&attn_join_kernel<false>),
+                            dim3(few ? (unsigned)(spans * l.per_tile) : grid), dim3(256), argv, 0, s);
+    }
     if (e != hipSuccess) {
         woq::set_hip_error((int)e);
         return WOQ_EHIP;

@@ -515,10 +515,12 @@ def woq_qgemm_int4o(w: Int4oW, xp, y, stream=None, b: int | None = None):
 def _rows(t, what: str, dtype, b: int, width: int):
     """(address, leading dimension) of a row-major device buffer that must
     hold b rows of ``width`` values; rows may be apart (t.stride(0))."""
-    if t.dtype is not dtype or t.dim() != 2:
+    try:
+        (rows, cols), (ld, step) = t.shape, t.stride()
+    except ValueError:
+        rows = -1
+    if t.dtype is not dtype or rows < 0:
         raise ValueError(f"{what}: expected a 2-D {dtype} tensor, got {t.dim()}-D {t.dtype}")
-    rows, cols = t.shape
-    ld, step = t.stride()
     if rows < b or cols < width or (step != 1 and cols > 1):
         raise ValueError(f"{what}: needs {b} rows of {width} adjacent values, got {tuple(t.shape)} with strides "
                          f"{(ld, step)}")
@@ -539,7 +541,7 @@ def _call(name: str, stream, tensors, *args, held=()):
     current.  ``held``: pairs of a name and the device of what the call reads
     through a descriptor (None: not known)."""
     dev = tensors[0].get_device()
-    for t in tensors:
+    for t in tensors[1:]:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{name}: tensors on {tensors[0].device} and {t.device}")
     if dev < 0:
@@ -652,23 +654,26 @@ def woq_cache_write(c: Cache, k, v, slots, q=None, q_out=None, rope=None, pos=No
     half, i32 = _torch.float16, _torch.int32
     if b is None:
         b = k.shape[0]
-    width = c.heads * c.dim
+    dim = c.dim
+    width = c.heads * dim
     kp, ldk = _rows(k, "k", half, b, width)
     vp, ldv = _rows(v, "v", half, b, width)
     if (q is None) != (q_out is None) or (rope is None) != (pos is None):
         raise ValueError("q goes with q_out, rope with pos")
     qp, ldq, q_heads, op, ldo = None, 0, 0, None, 0
     if q is not None:
-        q_heads, rest = divmod(q.shape[1], c.dim)
+        cols = q.shape[1]
+        q_heads, rest = divmod(cols, dim)
         if rest or not q_heads:
-            raise ValueError(f"q: {q.shape[1]} values a row are not heads of {c.dim}")
-        qp, ldq = _rows(q, "q", half, b, q.shape[1])
-        op, ldo = _rows(q_out, "q_out", half, b, q.shape[1])
+            raise ValueError(f"q: {cols} values a row are not heads of {dim}")
+        qp, ldq = _rows(q, "q", half, b, cols)
+        op, ldo = _rows(q_out, "q_out", half, b, cols)
     rp, n_pos, rot, pp = None, 0, 0, None
     if rope is not None:
-        if rope.dim() != 2:
-            raise ValueError("rope: expected [positions, rot]")
-        n_pos, rot = rope.shape
+        try:
+            n_pos, rot = rope.shape
+        except ValueError:
+            raise ValueError("rope: expected [positions, rot]") from None
         rp, pp = _vector(rope, "rope", _torch.float32, 0), _vector(pos, "pos", i32, b)
     _call("woq_cache_write", stream, (k, v, slots, q, q_out, rope, pos), c, kp, ldk, vp, ldv,
           _vector(slots, "slots", i32, b), b, qp, ldq, q_heads, op, ldo, rp, n_pos, rot, int(interleaved), pp,
@@ -706,10 +711,10 @@ def woq_attn_decode(c: Cache, q, pages, lens, y, workspace, scale: float | None 
     half = _torch.float16
     if b is None:
         b = q.shape[0]
-    width = q.shape[1]
-    q_heads, rest = divmod(width, c.dim)
+    width, dim = q.shape[1], c.dim
+    q_heads, rest = divmod(width, dim)
     if rest:
-        raise ValueError(f"q: {width} values a row are not heads of {c.dim}")
+        raise ValueError(f"q: {width} values a row are not heads of {dim}")
     qp, ldq = _rows(q, "q", half, b, width)
     yp, ldy = _rows(y, "y", half, b, width)
     W = pages.shape[1]
@@ -717,7 +722,7 @@ def woq_attn_decode(c: Cache, q, pages, lens, y, workspace, scale: float | None 
     if not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous")
     _call("woq_attn_decode", stream, (q, pages, lens, y, workspace), c, qp, ldq, q_heads, tp, ldt, W,
-          _vector(lens, "lens", _torch.int32, b), b, c.dim ** -0.5 if scale is None else scale, softcap, window, yp, ldy,
+          _vector(lens, "lens", _torch.int32, b), b, dim ** -0.5 if scale is None else scale, softcap, window, yp, ldy,
           workspace.data_ptr(), workspace.numel() * workspace.element_size(), held=(("the cache", c.device),))
     return y
 
