@@ -527,6 +527,50 @@ def test_attention_over_its_queries_and_rows_of_a_sequence(gpu_lib):
     check_attention(c, 4, lens, q=q, pages=pages, got=host(qd))
 
 
+@pytest.mark.parametrize("b", [63, 64, 65, 130])
+def test_attention_many_rows_of_every_length(gpu_lib, b):
+    """Ragged rows around the number that a wave holds, some empty, with a window
+    and without; one long row among short ones."""
+    rng = np.random.default_rng(b)
+    lens = rng.integers(0, 60, b)
+    lens[rng.random(b) < 0.2] = 0
+    lens[b // 2] = 4000
+    case("attention ragged", b)
+    c = Cache(int(sum(-(-lens // 32))) + 1, 3, 32, 64, True, seed=b)
+    check_attention(c, 6, lens, seed=b)
+    check_attention(c, 6, lens, seed=b, window=33)
+    lens[:] = 0
+    assert not check_attention(c, 6, lens, seed=b, width=200).any()
+
+
+@pytest.mark.parametrize("int8", [True, False])
+def test_attention_captured_where_it_takes_much_shared_memory(gpu_lib, int8):
+    """Sixteen heads of 256 to a key head: more than 64 KB a workgroup, short
+    tables and long; one graph of both, replayed."""
+    import torch
+    c = Cache(300, 1, 16, 256, int8, seed=3)
+    rng = np.random.default_rng(2)
+    lens = np.array([500, 0, 77], np.int32)
+    q = rng.standard_normal((3, 16 * 256)).astype(np.float16)
+    short = tables(rng, c, lens)
+    wide = np.full((3, 280), -1, np.int32)
+    wide[:, :short.shape[1]] = short
+    qd, ld, pages = dev(q), dev(lens), (dev(short), dev(wide))
+    y = [torch.empty(3, 16 * 256, dtype=torch.float16, device="cuda") for _ in pages]
+    ws = torch.empty(woq.woq_attn_decode_workspace(c.desc, 16, 3), dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        for p, out in zip(pages, y):
+            woq.woq_attn_decode(c.desc, qd, p, ld, out, ws)
+    for _ in range(3):
+        for out in y:
+            out.fill_(9)
+        g.replay()
+        for out in y:
+            check_attention(c, 16, lens, q=q, pages=short, got=host(out))
+
+
 # ----------------------------------------------------------------- sampling
 
 def check_sample(x, u, T=None, k=None, p=None, m=None, pad=0):
