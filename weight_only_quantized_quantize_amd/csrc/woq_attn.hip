@@ -3,6 +3,22 @@
 //   z[t] = scale (q . k[t]), or softcap tanh(scale (q . k[t]) / softcap),
 //   y = sum_t e^(z[t] - m) v[t] / sum_t e^(z[t] - m),   m = max_t z[t].
 //
+// Bound by the cache's bytes at many tokens (64 rows of up to 8192, 64 queries over 8
+// heads of 128, INT8: 96.5 us, 5.7 TB/s of 6.84 that a bare read reaches; 37 rows of a
+// window of 4096 over fp16 heads of 256: 129.5 us, 5.8 TB/s; one row of 131072: 50.6 us,
+// 5.5 TB/s) and by dependent round trips at few (lengths, pages, keys; one row of 509:
+// 8.4 us).  One pass over the tokens, a wave 32 of them at a time with the running
+// maximum and sum of the softmax, every query head of a key head at once: the scores of
+// 16 tokens are one tile of the fp16 matrix cores, tokens as rows, and leave each lane
+// with eight tokens of one head, the operand of the values' product as it stands.
+// Nothing passes through LDS but the joining of waves.  The keys of the next 32 tokens
+// are asked for behind the scores, their values behind the sums; with two workgroups a
+// compute unit about 50 KB are in flight there (three workgroups were slower, 102 us
+// for 97 above).
+//
+// Roundings: scores, maxima and sums are fp32.  Weights are rounded to fp16, to
+// nearest, for the matrix cores: 2^-12 of a weight on average, as many bits as the
+// fp16 result has, and the range is kept by the powers of two below.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -15,15 +31,17 @@ namespace {
 
 using namespace woqk;
 
-constexpr int WAVES = 4, T = 64 * WAVES;
 constexpr float NONE = -__builtin_huge_valf();
 constexpr int TOP = 15;             // weights are at most 2^15, so that fp16 holds weights 2^-40 of that
 
 // A cache's bytes u = code + 128 enter the matrix instructions as they are: u in the
 // low byte of an fp16 number is the subnormal u 2^-24, exactly, which one v_perm_b32
 // makes of two bytes, anywhere in two words.  The 128 leaves as a product of the same
-// operand with HALF in its place: once a segment for the keys, and with the weights as
-// one more row of sixteen channels for the values.
+// operand with HALF in its place: once a span for the keys, and with the weights as
+// one more tile of channels for the values.  Against conversion to the codes' own fp16
+// values (1 and 1.25 instructions a byte) this takes 0.5, and a wave's 32 tokens of 128
+// channels 305 vector instructions in all for 480; sums are of u instead of the code,
+// so fp32's roundings weigh up to |code| + 128 in place of |code|.
 constexpr uint32_t HALF = 0x00800080u;                        // 128 2^-24, twice
 constexpr float STEP = 0x1p24f;
 
@@ -121,10 +139,6 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&v)[W]) {
     }
 }
 
-__device__ __forceinline__ h8 pack8(h2 a, h2 b, h2 c, h2 d) {
-    return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
 // The parts that the waves of a workgroup leave of spans they do not hold whole: the
 // first and the last of each, in order.
 template <int N>
@@ -157,8 +171,8 @@ __device__ __forceinline__ void store_lane(uint16_t* out, const f4 (&acc)[E], fl
     }
 }
 
-// All positions (row, key head, tile of 16 query heads, unit) in order, an equal
-// count of them to every workgroup and in it to every wave (FLAT); or a span, all
+// All positions (row, key head, tile of 16 query heads, unit of 32 tokens) in order, an
+// equal count of them to every workgroup and in it to every wave (FLAT); or a span, all
 // units of a row, head and tile, to every workgroup.  What a wave holds of a span that
 // it does not hold whole goes through LDS to its neighbours, and of a span that the
 // workgroup does not hold whole through the workspace to the joining launch.

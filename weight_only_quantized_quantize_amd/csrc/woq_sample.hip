@@ -8,6 +8,12 @@
 // number of its tokens, and the draw falls on a bin and a number in it.  Only then
 // are the logits read again, for the index of that many-th token of that value.
 //
+// Bound by one compute unit's phases for few rows (one row of 128256 23.6 us: the
+// histogram 8, sums of its bins 2.5, limits 2.8, masses 2.5 to 6, searches 2.9, the
+// place 2.8), by HBM and those in turn for many (256 rows of 256000 56 us, the
+// histogram 26 of them at 5.2 TB/s).  A sort would move the row several times, a
+// threshold found in rounds read it several times.
+//
 // One workgroup per row.  The counts are 16 bits wide (65536 of them are 128 KB of
 // LDS, a value and its negative's neighbour to a word); one that passes 65535 loses
 // 65535 or 65536 of the sum of all, so a sum that is not the number of logits tells
