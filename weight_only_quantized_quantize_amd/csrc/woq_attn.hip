@@ -43,7 +43,7 @@ constexpr int TOP = 15;             // weights are at most 2^15, so that fp16 ho
 // channels 305 vector instructions in all for 480; sums are of u instead of the code,
 // so fp32's roundings weigh up to |code| + 128 in place of |code|.
 constexpr uint32_t HALF = 0x00800080u;                        // 128 2^-24, twice
-constexpr float STEP = 0x1p24f;
+constexpr double STEP = 0x1p24;
 
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
@@ -501,9 +501,9 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
             if (it + 1 < n) load_v();
         }
         if constexpr (INT8) {
-            const float unit = pow2i(power - TOP);
+            const float unit = pow2i(power - TOP + 24);       // bytes count 2^-24
 #pragma unroll
-            for (int i = 0; i < E; ++i) acc[i] = (acc[i] - offset) * STEP * unit;
+            for (int i = 0; i < E; ++i) acc[i] = (acc[i] - offset) * unit;
         }
 
         sum += __shfl_xor(sum, 16);
@@ -554,25 +554,30 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
         const int h = hh / a.tiles, tile = hh - h * a.tiles, heads = min(16, a.group - 16 * tile);
         const bool begins = parts.begins[k0], ends = parts.ends[63 - __builtin_clzll(these)];
         const int64_t slot = 2 * (int64_t)blockIdx.x + begins;
-        if (FLAT && begins && !ends)
-            cut = make_int4(row, hh, (parts.stop[k0] - 1) / per - (int)blockIdx.x + 1, 0);
+        if (FLAT && begins && !ends) cut = make_int4(row, hh, parts.stop[k0], 0);
         for (int i = tid; i < heads * (DP / 4); i += T) {
             const int hq = i / (DP / 4), d = 4 * (i - hq * (DP / 4));
             if (!EXACT && d >= dim) continue;
-            float ref = NONE, l = 0.0f, refs[PARTS];
+            // every place is read, whether or not a part of this span is there: the reads then wait for each other
+            // once, not one by one
+            float ref = NONE, l = 0.0f, refs[PARTS], sums[PARTS];
+            f4 v[PARTS], o = {0, 0, 0, 0};
 #pragma unroll
             for (int k = 0; k < PARTS; ++k) {
-                refs[k] = these >> k & 1 ? parts.ref[k][hq] : NONE;
-                ref = fmaxf(ref, refs[k]);
+                refs[k] = parts.ref[k][hq];
+                sums[k] = parts.sum[k][hq];
+                v[k] = *reinterpret_cast<const f4*>(join + (k * a.per_tile + hq) * ROW + d);
             }
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) ref = these >> k & 1 ? fmaxf(ref, refs[k]) : ref;
             const float zero = ref == NONE ? 0.0f : ref;
-            f4 o = {0, 0, 0, 0};
 #pragma unroll
             for (int k = 0; k < PARTS; ++k) {
-                if (!(these >> k & 1)) continue;
                 const float keep = __builtin_amdgcn_exp2f(refs[k] - zero);
-                l = fmaf(parts.sum[k][hq], keep, l);
-                o += *reinterpret_cast<const f4*>(join + (k * a.per_tile + hq) * ROW + d) * keep;
+                const bool in = these >> k & 1;
+                l += in ? sums[k] * keep : 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] += in ? v[k][e] * keep : 0.0f;
             }
             if (begins && ends) {
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -589,7 +594,10 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
             }
         }
     }
-    if (FLAT && tid == 0) a.cuts[blockIdx.x] = cut;
+    if (FLAT && tid == 0) {
+        if (cut.z) cut.z = (cut.z - 1) / per - (int)blockIdx.x + 1;       // workgroups up to the one that ends it
+        a.cuts[blockIdx.x] = cut;
+    }
 }
 
 // Joins the parts of the spans that were cut, in order, each under the power of two of
