@@ -70,7 +70,7 @@ struct Row {
     double mass[CHUNKS];
     uint32_t count[CHUNKS];
     uint32_t wave[WAVES], list[LIST];
-    uint32_t all, dead, wide, half;   // counts of 32 bits, of which half
+    uint32_t all, dead, places, wide, half;       // counts of 32 bits, of which half
     uint32_t chunk, bin, rank, limit, left;
     double before, kept;
 };
@@ -341,7 +341,7 @@ __global__ __launch_bounds__(T) void sample_kernel(SampleArgs a) {
     if (!(temp > 0.0f)) temp = 1.0f, k = 1;
 
     for (int i = tid; i < 32768 / 4; i += T) reinterpret_cast<uint4*>(s.hist)[i] = make_uint4(0, 0, 0, 0);
-    if (tid == 0) s.all = 0, s.dead = 0, s.wide = 0, s.half = 2, s.limit = 65536, s.left = 0;
+    if (tid == 0) s.all = 0, s.dead = 0, s.places = 0, s.wide = 0, s.half = 2, s.limit = 65536, s.left = 0;
     __syncthreads();
     // -infinity, which a mask may have put in most places, goes to a bin of the lane's
     // own behind DEAD, not to one word for all
@@ -459,83 +459,86 @@ __global__ __launch_bounds__(T) void sample_kernel(SampleArgs a) {
             if (n[j]) e = c * CHUNK + B * lane + j;
         first = (uint32_t)__builtin_amdgcn_readlane((int)e, __builtin_ctzll(__ballot(e < DEAD)));
     }
-    const Weight w{value_of(first), 1.0 / (double)temp, first};
-    // top-k: the bin at which the count reaches k
-    if (k > 0 && k < live) {
-        if (wave == 0) {
-            const uint32_t mine = all_counts();
-            uint32_t before = wave_upto(mine) - mine;
+    uint32_t bin = first, rank = 0;
+    if (k == 1) {             // the largest logit, the first of several
+        if (tid == 0 && a.prob) *gptr(a.prob + r) = 1.0f;
+    } else {
+        const Weight w{value_of(first), 1.0 / (double)temp, first};
+        // top-k: the bin at which the count reaches k
+        if (k > 0 && k < live) {
+            if (wave == 0) {
+                const uint32_t mine = all_counts();
+                uint32_t before = wave_upto(mine) - mine;
 #pragma unroll
-            for (int j = 0; j < CHUNKS / 64; ++j) {
-                const uint32_t n = s.count[CHUNKS / 64 * lane + j];
-                if (before < k && k <= before + n) s.chunk = CHUNKS / 64 * lane + j, s.left = before;
-                before += n;
+                for (int j = 0; j < CHUNKS / 64; ++j) {
+                    const uint32_t n = s.count[CHUNKS / 64 * lane + j];
+                    if (before < k && k <= before + n) s.chunk = CHUNKS / 64 * lane + j, s.left = before;
+                    before += n;
+                }
             }
+            __syncthreads();
+            need(s, x, a.N, s.chunk);
+            if (wave == 0) {
+                uint32_t n[B], mine = 0;
+                counts_of(s, s.chunk, n);
+#pragma unroll
+                for (int j = 0; j < B; ++j) mine += n[j];
+                uint32_t before = s.left + wave_upto(mine) - mine;
+#pragma unroll
+                for (int j = 0; j < B; ++j) {
+                    if (before < k && k <= before + n[j])
+                        s.limit = s.chunk * CHUNK + B * lane + j, s.left = (uint32_t)k - before;
+                    before += n[j];
+                }
+            }
+            __syncthreads();
+        }
+        // min-p: weights fall from bin to bin, so the first that is too small ends the rest
+        if (min_p > 0.0f && wave == 0) {
+            uint32_t lo = first, hi = 65536;     // the weight of bin lo suffices, that of hi does not
+            while (hi - lo > 1) {
+                const uint32_t step = (hi - lo + 63) / 64, e = lo + (lane + 1) * step;
+                const bool ok = e < hi && e < DEAD && w(e) >= (double)min_p;
+                const uint32_t n = (uint32_t)__popcll(__ballot(ok));
+                const uint32_t up = lo + (n + 1) * step;
+                lo += n * step;
+                hi = min(hi, up);
+            }
+            if (lane == 0 && hi <= s.limit) s.limit = hi, s.left = 0;
         }
         __syncthreads();
-        need(s, x, a.N, s.chunk);
-        if (wave == 0) {
-            uint32_t n[B], mine = 0;
-            counts_of(s, s.chunk, n);
-#pragma unroll
-            for (int j = 0; j < B; ++j) mine += n[j];
-            uint32_t before = s.left + wave_upto(mine) - mine;
-#pragma unroll
-            for (int j = 0; j < B; ++j) {
-                if (before < k && k <= before + n[j])
-                    s.limit = s.chunk * CHUNK + B * lane + j, s.left = (uint32_t)k - before;
-                before += n[j];
-            }
+        weigh(s, x, a.N, w);
+        // top-p, then the draw
+        if (p < 1.0f) {
+            double t = 0.0;
+            if (wave == 0)
+                find_chunk<true>(s, [&](double total) {
+                    t = (double)p * total;
+                    return t;
+                });
+            __syncthreads();
+            need(s, x, a.N, s.chunk);
+            if (wave == 0) find_bin<true>(s, w, t);
+            __syncthreads();
+            if (tid == 0) s.limit = s.bin, s.left = s.rank;
+            __syncthreads();
         }
-        __syncthreads();
-    }
-    // min-p: weights fall from bin to bin, so the first that is too small ends the rest
-    if (min_p > 0.0f && wave == 0) {
-        uint32_t lo = first, hi = 65536;     // the weight of bin lo suffices, that of hi does not
-        while (hi - lo > 1) {
-            const uint32_t step = (hi - lo + 63) / 64, e = lo + (lane + 1) * step;
-            const bool ok = e < hi && e < DEAD && w(e) >= (double)min_p;
-            const uint32_t n = (uint32_t)__popcll(__ballot(ok));
-            const uint32_t up = lo + (n + 1) * step;
-            lo += n * step;
-            hi = min(hi, up);
-        }
-        if (lane == 0 && hi <= s.limit) s.limit = hi, s.left = 0;
-    }
-    __syncthreads();
-    weigh(s, x, a.N, w);
-    // top-p, then the draw
-    if (p < 1.0f) {
         double t = 0.0;
-        if (wave == 0)
-            find_chunk<true>(s, [&](double total) {
-                t = (double)p * total;
+        if (wave == 0) {
+            const double kept = p < 1.0f ? s.kept : 0.0;       // top-p leaves less than the chunks' masses
+            find_chunk<false>(s, [&](double total) {
+                t = (double)u * (p < 1.0f ? kept : total);
                 return t;
             });
+            if (p < 1.0f && lane == 0) s.kept = kept;
+        }
         __syncthreads();
         need(s, x, a.N, s.chunk);
-        if (wave == 0) find_bin<true>(s, w, t);
+        if (wave == 0) find_bin<false>(s, w, t);
         __syncthreads();
-        if (tid == 0) s.limit = s.bin, s.left = s.rank;
-        __syncthreads();
-    } else if (wave == 0) {
-        find_chunk<false>(s, [&](double total) { return total; });
+        bin = s.bin, rank = s.rank;
+        if (tid == 0 && a.prob) *gptr(a.prob + r) = (float)((double)w(bin) / s.kept);
     }
-    __syncthreads();
-    double t = 0.0;
-    if (wave == 0) {
-        const double total = s.kept;
-        t = (double)u * total;
-        find_chunk<false>(s, [&](double) { return t; });
-        if (lane == 0) s.kept = total;
-    }
-    __syncthreads();
-    need(s, x, a.N, s.chunk);
-    if (wave == 0) find_bin<false>(s, w, t);
-    if (tid == 0) s.dead = 0;
-    __syncthreads();
-    const uint32_t bin = s.bin, rank = s.rank;
-    if (tid == 0 && a.prob) *gptr(a.prob + r) = (float)((double)w(bin) / s.kept);
     // the rank-th token of that bin.  A zero's sign does not matter.
     const uint32_t mask = bin == ZERO ? 0x7FFF7FFFu : 0xFFFFFFFFu;
     const uint32_t value = bin == ZERO ? 0 : (bin & 0x8000u ? bin : 0x7FFFu - bin) * 0x10001u;
@@ -545,7 +548,7 @@ __global__ __launch_bounds__(T) void sample_kernel(SampleArgs a) {
                            : bin & 0x8000u ? s.hist[bin & 0x7FFFu] >> 16 : s.hist[bin] & 0xFFFFu;
     if (there <= LIST) {
         // all of their places, in any order; each then looks how many lie before it
-        auto put = [&](uint32_t i) { s.list[atomicAdd(&s.dead, 1u)] = i; };
+        auto put = [&](uint32_t i) { s.list[atomicAdd(&s.places, 1u)] = i; };
         each(x, a.N, [&](uint4 q, uint32_t i) {
             const us2 d[4] = {differ(q.x), differ(q.y), differ(q.z), differ(q.w)};
             const us2 least = __builtin_elementwise_min(__builtin_elementwise_min(d[0], d[1]),
