@@ -353,7 +353,9 @@ def check_attention(c, q_heads, lens, seed=0, window=0, softcap=0.0, scale=None,
 @pytest.mark.parametrize("int8", [True, False])
 @pytest.mark.parametrize("heads,q_heads,dim,page", [
     (8, 64, 128, 16), (8, 16, 256, 64), (8, 32, 128, 48), (12, 12, 64, 16), (5, 20, 96, 32), (1, 16, 128, 128),
-    (1, 40, 64, 16), (2, 6, 80, 16), (1, 1, 16, 16), (1, 17, 256, 16), (3, 3, 240, 32), (2, 66, 48, 16), (4, 28, 128, 256)])
+    (1, 40, 64, 16), (2, 6, 80, 16), (1, 1, 16, 16), (1, 17, 256, 16), (3, 3, 240, 32), (2, 66, 48, 16), (4, 28, 128, 256),
+    (1, 32, 64, 16), (1, 32, 128, 16), (1, 48, 128, 32), (2, 128, 64, 16), (1, 71, 64, 16), (1, 33, 80, 16), (2, 40, 96, 48),
+    (1, 17, 16, 16)])
 def test_attention_head_layouts(gpu_lib, int8, heads, q_heads, dim, page):
     """Over tables of just the pages needed and over wide ones: a short table's
     rows are a workgroup's whole, a long one's are divided."""
@@ -380,7 +382,8 @@ def test_attention_batches(gpu_lib, int8, b):
     (True, 8, 64, 128, 64, [5000]), (False, 2, 4, 256, 48, [6001, 3]), (True, 1, 8, 128, 16, [30001]),
     (True, 2, 16, 64, 256, [9000, 0, 1, 12000, 77]), (False, 1, 3, 80, 32, [20011]),
     (True, 2, 2, 64, 16, [0] * 40 + [700] + [0] * 300 + [3, 40] * 60 + [0] * 40),
-    (False, 3, 60, 16, 16, [2000, 1, 0, 5000]), (True, 8, 128, 256, 16, [1000, 3000])])
+    (False, 3, 60, 16, 16, [2000, 1, 0, 5000]), (True, 8, 128, 256, 16, [1000, 3000]),
+    (True, 1, 40, 64, 64, [30000, 7, 900]), (False, 1, 32, 128, 16, [9000]), (True, 2, 96, 128, 16, [4000, 0, 2100])])
 def test_attention_long(gpu_lib, int8, heads, q_heads, dim, page, lens):
     case("attention long", int8, heads, q_heads, dim, page, lens)
     c = Cache(sum(-(-n // page) for n in lens) + 1, heads, page, dim, int8, seed=7)
