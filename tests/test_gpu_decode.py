@@ -546,6 +546,30 @@ def test_attention_many_rows_of_every_length(gpu_lib, b):
     assert not check_attention(c, 6, lens, seed=b, width=200).any()
 
 
+@pytest.mark.parametrize("width", [20, 90])
+def test_attention_of_views(gpu_lib, width):
+    """Tables, lengths and rows that are pieces of larger tensors, at addresses of
+    any 4 (int32) or 16 (rows) bytes; rows behind the batch stay."""
+    import torch
+    c = Cache(60, 2, 16, 64, True, seed=21)
+    rng = np.random.default_rng(width)
+    lens = np.array([300, 17, 0, 211], np.int32)
+    pages = tables(rng, c, lens, width=width)
+    q = rng.standard_normal((4, 4 * 64)).astype(np.float16)
+    big = dev(np.full((6, width + 5), 2 ** 30, np.int32))
+    big[1:5, 3:3 + width] = dev(pages)
+    ld = dev(np.full(9, 777, np.int32))
+    ld[3:7] = dev(lens)
+    rows = torch.full((6, 3 * 256), 5.0, dtype=torch.float16, device="cuda")
+    rows[1:5, 256:512] = dev(q)
+    ws = torch.empty(woq.woq_attn_decode_workspace(c.desc, 4, 4) + 16, dtype=torch.uint8, device="cuda")
+    woq.woq_attn_decode(c.desc, rows[1:, 256:512], big[1:, 3:3 + width], ld[3:], rows[1:, 512:], ws[16:], b=4)
+    got = host(rows)
+    check_attention(c, 4, lens, q=q, pages=pages, got=got[1:5, 512:])
+    assert np.all(got[[0, 5]] == 5) and np.all(got[:, :256] == 5)
+    np.testing.assert_array_equal(got[1:5, 256:512], q)
+
+
 @pytest.mark.parametrize("int8", [True, False])
 def test_attention_captured_where_it_takes_much_shared_memory(gpu_lib, int8):
     """Sixteen heads of 256 to a key head: more than 64 KB a workgroup, short
@@ -685,6 +709,23 @@ def test_sample_more_equal_logits_than_16_bits_count(gpu_lib, N):
     check_sample(x, u, T=0.8, p=0.9, m=0.01)
     check_sample(x, u, k=[1, 70000, N, N - 1, 1000, 66000, 60000, 65536, 30000])
     check_sample(x, u, k=66000, p=0.999)
+
+
+def test_sample_of_views(gpu_lib):
+    """Rows inside wider ones, parameters from the middle of vectors."""
+    import torch
+    x, rng = logits(6, 2000, 4)
+    wide = dev(np.full((8, 2400), 60000, np.float16))
+    wide[1:7, 200:2200] = dev(x)
+    u, top_p = rng.random(6).astype(np.float32), np.array([0.3, 0.9, 1.0, 0.5, 0.99, 0.7], np.float32)
+    ud, pd = dev(np.full(9, 0.5, np.float32)), dev(np.full(9, 0.0, np.float32))
+    ud[3:], pd[2:8] = dev(u), dev(top_p)
+    token = torch.full((8,), -5, dtype=torch.int32, device="cuda")
+    woq.woq_sample(wide[1:, 200:2200], ud[3:], token[1:7], top_p=pd[2:], b=6)
+    got = host(token)
+    assert got[0] == got[7] == -5
+    for r in range(6):
+        assert got[1 + r] == O.sample(x[r], float(u[r]), top_p=float(top_p[r]))[0]
 
 
 def test_sample_rows_do_not_touch_each_other(gpu_lib):
