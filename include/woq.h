@@ -601,8 +601,8 @@ int woq_cache_read(const woq_cache* c, const int32_t* slots, int64_t n, uint16_t
  * lens.  q fp16 [b, ldq] and y fp16 [b, ldy] with q_heads * dim values, 16-byte
  * aligned, leading dimensions multiples of 8; q_heads is a multiple of heads.
  * Scores, softmax and sums are fp32; the weights of the values (the softmax's
- * numerators, times the token's scale where there is one) are rounded to fp16
- * under a power of two of their own for the matrix cores.  y may be q with the
+ * numerators, times the token's scale where there is one) meet them as two fp16
+ * halves under a common power of two.  y may be q with the
  * same leading dimension.  workspace: at least woq_attn_decode_workspace bytes of device memory,
  * 16-byte aligned, owned by the caller, its contents on return unspecified;
  * calls that share it must not overlap.  Deterministic for given inputs on one

@@ -11,15 +11,14 @@ SUB = 2^-25 half the spacing of fp16's subnormals.
   encoder's.
 * attention: a score is a sum of dim exact products in fp32, then at most 8
   roundings (its factors, the exponential's argument): (dim + 8) U of its terms'
-  magnitudes (reach), and as much again for the row's largest score; a weight's
-  rounding to fp16 is H of it, exponential, logarithm and reciprocal 2^-20, its
-  argument 2^-22 for the token's scale; the sums of n tokens are at most n / 16 + 96
-  roundings long, twice (values and weights): all of them relative to spread =
-  sum p |v|.  Weights below 2^-40 of the largest may be lost: n 2^-40 max |v|.
+  magnitudes (reach), and as much again for the row's largest score; two fp16
+  halves of a weight lose 2^-22 of it, its exponential, its argument and the token's
+  scale 2^-19; the sums of n tokens are at most n / 16 + 96 roundings long, twice
+  (values and weights): all of them relative to spread = sum p |v|.  Weights below 2^-40 of the largest may be lost: n 2^-40 max |v|.
   The result is rounded to fp16.  INT8 bytes u = code + 128 are multiplied as they
   are and 128 times the factor's sum is taken off in fp32, so the magnitudes that
   fp32's roundings are relative to are those of u, at most |code| + 128: reach grows by
-  128 max ks sum |q|, and for the sums (not for the weights' rounding, which is the
+  128 max ks sum |q|, and for the sums (not for the weights' halves, which are the
   same in both) spread by 128 sum p sv.
 * a token is the definition's, exactly; its share is rounded to fp32 once.
 """
@@ -344,7 +343,7 @@ def check_attention(c, q_heads, lens, seed=0, window=0, softcap=0.0, scale=None,
             reach = reach + 128 * abs(scale) * (ks.max(0)[of] * np.abs(q[r].astype(float)).reshape(q_heads, D).sum(1))[:, None]
             sums = mag + O.attend(q[r].reshape(q_heads, D), K, np.repeat(128 * sv[..., None], D, 2), scale, softcap)[0]
         dz = reach * (D + 8) * U
-        rel = H + 3 * dz + 2.0 ** -19 + softcap * 2.0 ** -21
+        rel = 2.0 ** -22 + 3 * dz + 2.0 ** -19 + softcap * 2.0 ** -21
         tol = mag * rel + sums * 2 * (m / 16 + 96) * U + np.abs(ref) * H + SUB + (m * 2.0 ** -40 * np.abs(V).max() if m else 0)
         within(got[r].reshape(q_heads, D), ref, tol, ("row", r, "of", b, "len", int(lens[r])))
     return got

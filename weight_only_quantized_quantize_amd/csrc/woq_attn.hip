@@ -4,21 +4,23 @@
 //   y = sum_t e^(z[t] - m) v[t] / sum_t e^(z[t] - m),   m = max_t z[t].
 //
 // Bound by the cache's bytes at many tokens (64 rows of up to 8192, 64 queries over 8
-// heads of 128, INT8: 96.5 us, 5.7 TB/s of 6.84 that a bare read reaches; 37 rows of a
-// window of 4096 over fp16 heads of 256: 129.5 us, 5.8 TB/s; one row of 131072: 50.6 us,
-// 5.5 TB/s) and by dependent round trips at few (lengths, pages, keys; one row of 509:
-// 8.4 us).  One pass over the tokens, a wave 32 of them at a time with the running
+// heads of 128, INT8: 98 us, 5.6 TB/s of 6.84 that a bare read reaches; 37 rows of a
+// window of 4096 over fp16 heads of 256: 131 us, 5.9 TB/s; one row of 131072: 51 us,
+// 5.4 TB/s) and by dependent round trips at few (lengths, pages, keys; one row of 509:
+// 8.5 us).  One pass over the tokens, a wave 32 of them at a time with the running
 // maximum and sum of the softmax, every query head of a key head at once: the scores of
 // 16 tokens are one tile of the fp16 matrix cores, tokens as rows, and leave each lane
 // with eight tokens of one head, the operand of the values' product as it stands.
 // Nothing passes through LDS but the joining of waves.  The keys of the next 32 tokens
 // are asked for behind the scores, their values behind the sums; with two workgroups a
 // compute unit about 50 KB are in flight there (three workgroups were slower, 102 us
-// for 97 above).
+// for 97 with one fp16 number a weight).
 //
-// Roundings: scores, maxima and sums are fp32.  Weights are rounded to fp16, to
-// nearest, for the matrix cores: 2^-12 of a weight on average, as many bits as the
-// fp16 result has, and the range is kept by the powers of two below.
+// Roundings: scores, maxima and sums are fp32.  Weights meet the values as two fp16
+// numbers, the nearest and what it leaves, 22 bits of a weight together (2^-40 of the
+// largest at least): one more product of an operand that is there, for 0.7% of the time
+// at 128 channels and 4% at 64 and 256, and results as near to the exact ones as fp32
+// throughout would give, where one fp16 number alone was 1.4 times as far.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -32,7 +34,7 @@ namespace {
 using namespace woqk;
 
 constexpr float NONE = -__builtin_huge_valf();
-constexpr int TOP = 15;             // weights are at most 2^15, so that fp16 holds weights 2^-40 of that
+constexpr int TOP = 15;             // weights are at most 2^15, so that fp16 holds what is 2^-40 of that
 
 // A cache's bytes u = code + 128 enter the matrix instructions as they are: u in the
 // low byte of an fp16 number is the subnormal u 2^-24, exactly, which one v_perm_b32
@@ -40,7 +42,8 @@ constexpr int TOP = 15;             // weights are at most 2^15, so that fp16 ho
 // operand with HALF in its place: once a span for the keys, and with the weights as
 // one more tile of channels for the values.  Against conversion to the codes' own fp16
 // values (1 and 1.25 instructions a byte) this takes 0.5, and a wave's 32 tokens of 128
-// channels 305 vector instructions in all for 480; sums are of u instead of the code,
+// channels 305 vector instructions in all for 480 (325 with the second product of the
+// weights); sums are of u instead of the code,
 // so fp32's roundings weigh up to |code| + 128 in place of |code|.
 constexpr uint32_t HALF = 0x00800080u;                        // 128 2^-24, twice
 constexpr double STEP = 0x1p24;
@@ -472,14 +475,14 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
                 }
             }
             const float ref = (top == NONE ? 0.0f : top) - (INT8 ? 0 : TOP), raise = pow2i(TOP - power);
-            f16 p[8];
+            h8 weights, rests;                // a weight's fp16 and what that leaves of it
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float e = __builtin_amdgcn_exp2f(z[i] - ref);
+                const float e = __builtin_amdgcn_exp2f(z[i] - ref), x = INT8 ? e * (vs[i] * raise) : e;
                 sum += e;
-                p[i] = (f16)(INT8 ? e * (vs[i] * raise) : e);
+                weights[i] = (f16)x;
+                rests[i] = (f16)(x - (float)weights[i]);
             }
-            const h8 weights = {p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]};
             // sums: rows of the product are the channels E (lane % 16) + i
 #pragma unroll
             for (int c = 0; c < WV; ++c) {
@@ -493,11 +496,15 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
                     v.y = __builtin_amdgcn_perm(t.v[3][c], t.v[2][c], SEL[x]);
                     v.z = __builtin_amdgcn_perm(t.v[5][c], t.v[4][c], SEL[x]);
                     v.w = __builtin_amdgcn_perm(t.v[7][c], t.v[6][c], SEL[x]);
-                    acc[N * c + x] =
-                        __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, v), weights, acc[N * c + x], 0, 0, 0);
+                    f4& o = acc[N * c + x];
+                    o = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, v), weights, o, 0, 0, 0);
+                    o = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, v), rests, o, 0, 0, 0);
                 }
             }
-            if constexpr (INT8) offset = __builtin_amdgcn_mfma_f32_16x16x32_f16(half, weights, offset, 0, 0, 0);
+            if constexpr (INT8) {
+                offset = __builtin_amdgcn_mfma_f32_16x16x32_f16(half, weights, offset, 0, 0, 0);
+                offset = __builtin_amdgcn_mfma_f32_16x16x32_f16(half, rests, offset, 0, 0, 0);
+            }
             if (it + 1 < n) load_v();
         }
         if constexpr (INT8) {
