@@ -4,10 +4,10 @@
 //   y = sum_t e^(z[t] - m) v[t] / sum_t e^(z[t] - m),   m = max_t z[t].
 //
 // Bound by the cache's bytes at many tokens (64 rows of up to 8192, 64 queries over 8
-// heads of 128, INT8: 98 us, 5.6 TB/s of 6.84 that a bare read reaches; 37 rows of a
+// heads of 128, INT8: 98 us, 5.7 TB/s of 6.84 that a bare read reaches; 37 rows of a
 // window of 4096 over fp16 heads of 256: 131 us, 5.9 TB/s; one row of 131072: 51 us,
-// 5.4 TB/s) and by dependent round trips at few (lengths, pages, keys; one row of 509:
-// 8.5 us).  One pass over the tokens, a wave 32 of them at a time with the running
+// 5.5 TB/s) and by dependent round trips at few (lengths, pages, keys; one row of 509:
+// 8.6 us).  One pass over the tokens, a wave 32 of them at a time with the running
 // maximum and sum of the softmax, every query head of a key head at once: the scores of
 // 16 tokens are one tile of the fp16 matrix cores, tokens as rows, and leave each lane
 // with eight tokens of one head, the operand of the values' product as it stands.
@@ -42,7 +42,7 @@ constexpr int TOP = 15;             // weights are at most 2^15, so that fp16 ho
 // operand with HALF in its place: once a span for the keys, and with the weights as
 // one more tile of channels for the values.  Against conversion to the codes' own fp16
 // values (1 and 1.25 instructions a byte) this takes 0.5, and a wave's 32 tokens of 128
-// channels 305 vector instructions in all for 480 (325 with the second product of the
+// channels 305 vector instructions in all for 480 (330 with the second product of the
 // weights); sums are of u instead of the code,
 // so fp32's roundings weigh up to |code| + 128 in place of |code|.
 constexpr uint32_t HALF = 0x00800080u;                        // 128 2^-24, twice
