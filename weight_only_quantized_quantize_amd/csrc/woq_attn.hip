@@ -36,17 +36,21 @@ using namespace woqk;
 constexpr float NONE = -__builtin_huge_valf();
 constexpr int TOP = 15;             // weights are at most 2^15, so that fp16 holds what is 2^-40 of that
 
-// A cache's bytes u = code + 128 enter the matrix instructions as they are: u in the
-// low byte of an fp16 number is the subnormal u 2^-24, exactly, which one v_perm_b32
-// makes of two bytes, anywhere in two words.  The 128 leaves as a product of the same
-// operand with HALF in its place: once a span for the keys, and with the weights as
-// one more tile of channels for the values.  Against conversion to the codes' own fp16
-// values (1 and 1.25 instructions a byte) this takes 0.5, and a wave's 32 tokens of 128
-// channels 305 vector instructions in all for 480 (330 with the second product of the
-// weights); sums are of u instead of the code,
-// so fp32's roundings weigh up to |code| + 128 in place of |code|.
-constexpr uint32_t HALF = 0x00800080u;                        // 128 2^-24, twice
-constexpr double STEP = 0x1p24;
+// A cache's bytes u = code + 128 become the fp16 numbers code 2^-9, exactly: v_perm_b32
+// puts two bytes, from anywhere in two words, into the low bytes of two fp16 numbers,
+// the subnormals u 2^-24, and one packed fused multiply-add makes u 2^-9 - 128 2^-9 of
+// them.  The bytes as they are would do for the matrix instructions too, with the 128
+// taken off the sums (one row of 131072 50.8 us for 51.3, 64 rows of up to 8192 98.0 for
+// 99.4, one row of 509 8.7 for 9.0), but sums of u are three and more times as large as
+// what is left of them, and the matrix cores keep fewer bits of a sum whose operands are
+// subnormal: over 131072 tokens 8.6% of the results then were not the nearest fp16 number
+// to the exact ones, 1.6% with subnormal codes, and 0.25% as it is, where fp32 throughout
+// has 0.28%.
+constexpr int STEP = 9;
+__device__ __forceinline__ uint32_t codes2(uint32_t u) {
+    const h2 up = {(f16)0x1p15f, (f16)0x1p15f}, offset = {(f16)-0.25f, (f16)-0.25f};
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(as_h2(u), up, offset));
+}
 
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
@@ -327,15 +331,9 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
                 q[i] = __builtin_bit_cast(h8, w);
             }
         }
-        f4 acc[E], offset = {0, 0, 0, 0}, start = {0, 0, 0, 0};
+        f4 acc[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) acc[i] = f4{0, 0, 0, 0};
-        const h8 half = __builtin_bit_cast(h8, make_uint4(HALF, HALF, HALF, HALF));
-        if constexpr (INT8) {
-#pragma unroll
-            for (int i = 0; i < DP / 32; ++i) start = __builtin_amdgcn_mfma_f32_16x16x32_f16(half, q[i], start, 0, 0, 0);
-            start = -start;
-        }
         float top = NONE, sum = 0.0f;
         int power = -90;                      // INT8: scales of values are below 2^power
 
@@ -393,7 +391,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
             float z[8];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                f4 s = start;
+                f4 s = {0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < NK; ++i) {
                     const uint32_t w[4] = {t.k[j][i].x, t.k[j][i].y, t.k[j][i].z, t.k[j][i].w};
@@ -401,10 +399,10 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             uint4 c;
-                            c.x = __builtin_amdgcn_perm(w[2 * e], w[2 * e], 0x0c010c00u);
-                            c.y = __builtin_amdgcn_perm(w[2 * e], w[2 * e], 0x0c030c02u);
-                            c.z = __builtin_amdgcn_perm(w[2 * e + 1], w[2 * e + 1], 0x0c010c00u);
-                            c.w = __builtin_amdgcn_perm(w[2 * e + 1], w[2 * e + 1], 0x0c030c02u);
+                            c.x = codes2(__builtin_amdgcn_perm(w[2 * e], w[2 * e], 0x0c010c00u));
+                            c.y = codes2(__builtin_amdgcn_perm(w[2 * e], w[2 * e], 0x0c030c02u));
+                            c.z = codes2(__builtin_amdgcn_perm(w[2 * e + 1], w[2 * e + 1], 0x0c010c00u));
+                            c.w = codes2(__builtin_amdgcn_perm(w[2 * e + 1], w[2 * e + 1], 0x0c030c02u));
                             s = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, c), q[2 * i + e], s, 0, 0, 0);
                         }
                     } else {
@@ -456,7 +454,6 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
                 const float next = fmaxf(top, most), keep = __builtin_amdgcn_exp2f(top - (next == NONE ? 0.0f : next));
                 top = next;
                 sum *= keep;
-                offset *= keep;
 #pragma unroll
                 for (int i = 0; i < E; ++i) acc[i] *= keep;
             }
@@ -469,7 +466,6 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
                     const int next = min(110, (int)(__builtin_amdgcn_readfirstlane(__float_as_uint(large)) >> 23) - 126);
                     const float keep = pow2i(max(-126, power - next));
                     power = next;
-                    offset *= keep;
 #pragma unroll
                     for (int i = 0; i < E; ++i) acc[i] *= keep;
                 }
@@ -496,21 +492,18 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
                     v.y = __builtin_amdgcn_perm(t.v[3][c], t.v[2][c], SEL[x]);
                     v.z = __builtin_amdgcn_perm(t.v[5][c], t.v[4][c], SEL[x]);
                     v.w = __builtin_amdgcn_perm(t.v[7][c], t.v[6][c], SEL[x]);
+                    if constexpr (INT8) v = make_uint4(codes2(v.x), codes2(v.y), codes2(v.z), codes2(v.w));
                     f4& o = acc[N * c + x];
                     o = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, v), weights, o, 0, 0, 0);
                     o = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, v), rests, o, 0, 0, 0);
                 }
             }
-            if constexpr (INT8) {
-                offset = __builtin_amdgcn_mfma_f32_16x16x32_f16(half, weights, offset, 0, 0, 0);
-                offset = __builtin_amdgcn_mfma_f32_16x16x32_f16(half, rests, offset, 0, 0, 0);
-            }
             if (it + 1 < n) load_v();
         }
         if constexpr (INT8) {
-            const float unit = pow2i(power - TOP + 24);       // bytes count 2^-24
+            const float unit = pow2i(power - TOP + STEP);
 #pragma unroll
-            for (int i = 0; i < E; ++i) acc[i] = (acc[i] - offset) * unit;
+            for (int i = 0; i < E; ++i) acc[i] *= unit;
         }
 
         sum += __shfl_xor(sum, 16);
@@ -760,11 +753,10 @@ Kernel split_kernel(int dim, bool flat) {
 }
 
 // Scores are in units of log2: factor s, or cap (1 - 2 / (1 + 2^(factor s))), with s the
-// product of a query and a key's bytes as they are.
+// product of a query and a key's numbers as they enter the matrix instructions.
 constexpr double LOG2E = 1.4426950408889634;
-float score_factor(const woq_cache* c, float scale, float softcap) {
-    const double step = c->fmt == WOQ_CACHE_INT8 ? STEP : 1.0;
-    return (float)(step * LOG2E * scale * (softcap > 0.0f ? 2.0 / softcap : 1.0));
+float score_factor(const woq_cache* c, float scale, float softcap, int step = STEP) {
+    return (float)(std::ldexp(1.0, c->fmt == WOQ_CACHE_INT8 ? step : 0) * LOG2E * scale * (softcap > 0.0f ? 2.0 / softcap : 1.0));
 }
 
 bool half_rows_ok(const void* p, int64_t ld) { return woq::aligned16(p) && (ld & 7) == 0; }
@@ -793,7 +785,7 @@ int attn_check(const woq_cache* c, const uint16_t* q, int64_t ldq, int32_t q_hea
         return WOQ_EUNSUPPORTED;
     const int64_t units = max_pages * c->page / 32 + 1, spans = (int64_t)c->heads * ceil_div(q_heads / c->heads, 16);
     if (units > WOQ_ATTN_MAX_TOKENS / (b * spans)) return WOQ_EUNSUPPORTED;
-    if (!std::isfinite(score_factor(c, scale, softcap))) return WOQ_EUNSUPPORTED;
+    if (!std::isfinite(score_factor(c, scale, softcap, 24))) return WOQ_EUNSUPPORTED;      // with room above what is used
     if (workspace_bytes < woq_attn_decode_workspace(c, q_heads, b)) return WOQ_EINVAL;
     return WOQ_OK;
 }
