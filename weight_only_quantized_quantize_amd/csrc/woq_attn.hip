@@ -40,12 +40,12 @@ constexpr int TOP = 15;             // weights are at most 2^15, so that fp16 ho
 // puts two bytes, from anywhere in two words, into the low bytes of two fp16 numbers,
 // the subnormals u 2^-24, and one packed fused multiply-add makes u 2^-9 - 128 2^-9 of
 // them.  The bytes as they are would do for the matrix instructions too, with the 128
-// taken off the sums (one row of 131072 50.8 us for 51.3, 64 rows of up to 8192 98.0 for
-// 99.4, one row of 509 8.7 for 9.0), but sums of u are three and more times as large as
-// what is left of them, and the matrix cores keep fewer bits of a sum whose operands are
-// subnormal: over 131072 tokens 8.6% of the results then were not the nearest fp16 number
-// to the exact ones, 1.6% with subnormal codes, and 0.25% as it is, where fp32 throughout
-// has 0.28%.
+// taken off the sums (64 rows of up to 8192 97.7 us for 98.3, one row of 131072 51.0 for
+// 51.2, one row of 509 8.7 for 9.0, but 64 rows of up to 8000 of heads of 256 199 for 180),
+// but sums of u are three and more times as large as what is left of them, and the matrix
+// cores keep fewer bits of a sum whose operands are subnormal: over 131072 tokens 8.6% of
+// the results then were not the nearest fp16 number to the exact ones, 1.6% with
+// subnormal codes, and 0.25% as it is, where fp32 throughout has 0.28%.
 constexpr int STEP = 9;
 __device__ __forceinline__ uint32_t codes2(uint32_t u) {
     const h2 up = {(f16)0x1p15f, (f16)0x1p15f}, offset = {(f16)-0.25f, (f16)-0.25f};
