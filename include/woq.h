@@ -608,12 +608,14 @@ int woq_cache_read(const woq_cache* c, const int32_t* slots, int64_t n, uint16_t
  * calls that share it must not overlap.  Deterministic for given inputs on one
  * device model.  q_heads <= WOQ_ATTN_MAX_HEADS, b <= WOQ_ATTN_MAX_ROWS,
  * max_pages * page <= WOQ_ATTN_MAX_TOKENS, and b * heads * ceil(q_heads / heads / 16)
- * * (max_pages * page / 32 + 1) too; 2^24 log2(e) scale, times 2 / softcap where there
- * is one, has to be finite in fp32; b = 0 is a no-op.
+ * * (max_pages * page / 32 + 1) too; softcap <= WOQ_ATTN_MAX_SOFTCAP, below which no
+ * score is too small for fp32 when it is divided by it; 2^24 log2(e) scale, times 2 /
+ * softcap where there is one, has to be finite in fp32; b = 0 is a no-op.
  */
 #define WOQ_ATTN_MAX_HEADS 4096
 #define WOQ_ATTN_MAX_ROWS 65536
 #define WOQ_ATTN_MAX_TOKENS (1 << 30)
+#define WOQ_ATTN_MAX_SOFTCAP 18446744073709551616.0f      /* 2^64 */
 int woq_attn_decode(const woq_cache* c, const uint16_t* q, int64_t ldq, int32_t q_heads, const int32_t* pages,
                     int64_t ldpages, int64_t max_pages, const int32_t* lens, int64_t b, float scale, float softcap,
                     int32_t window, uint16_t* y, int64_t ldy, void* workspace, int64_t workspace_bytes, void* stream);

@@ -118,3 +118,26 @@ def test_scores_of_whole_numbers(gpu_lib, int8):
     y, (ref, spread) = attend(c, q_heads, q, pages, [n], scale=0.25), exact(c, q_heads, q, pages, [n], 0.25)
     rel = 2 * 3 * 64 * U + 2.0 ** -19 + 200 * U
     within(y, ref, spread * rel + np.abs(ref) * H + SUB)
+
+
+@pytest.mark.parametrize("int8", [True, False])
+@pytest.mark.parametrize("softcap", [1.0, 8.0, 50.0, 1e3, 1e4, 1e6, 1e8, 1e12, 2.0 ** 64])
+def test_bounded_scores_of_any_bound(gpu_lib, int8, softcap):
+    """Scores of up to some 40 under bounds from far below to far above them.  A score
+    is off by a sum's roundings as in the sharp scores' test, which the bound never
+    raises (tanh's slope is at most 1), and by 2^-22 of itself for tanh and eight
+    roundings, all relative to it however large the bound."""
+    case("softcap", int8, softcap)
+    D, q_heads, lens = 128, 6, [700, 33, 2, 150]
+    c = Cache(80, 2, 16, D, int8, seed=60)
+    rng = np.random.default_rng(61)
+    q = (rng.standard_normal((4, q_heads * D)) * 4).astype(np.float16)
+    pages = tables(rng, c, lens)
+    y = attend(c, q_heads, q, pages, lens, softcap=softcap)
+    ref, spread = exact(c, q_heads, q, pages, lens, D ** -0.5, softcap)
+    kn = np.linalg.norm(c.values("k"), axis=-1).max()
+    for r in range(4):
+        reach = D ** -0.5 * np.linalg.norm(q[r].reshape(q_heads, D).astype(float), axis=-1).max() * kn
+        rel = 2 * ((4 * np.sqrt(D) + 8) * U + 2.0 ** -22) * reach + 2.0 ** -19 + 200 * U
+        assert rel < 1e-2
+        within(y[r], ref[r], spread[r] * rel + np.abs(ref[r]) * H + SUB, ("row", r))

@@ -55,6 +55,19 @@ __device__ __forceinline__ uint32_t codes2(uint32_t u) {
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+// tanh(t ln 2 / 2).  1 - 2 / (1 + 2^t) is off by 2^-24 of 1, which near 0 is not little of
+// the result; up to 1.5 there is the odd polynomial that is nearest in relative terms
+// (2^-25.6).  Both are within 2^-22.5 of the result with their roundings.
+__device__ __forceinline__ float tanh_of(float t) {
+    const float u = t * t;
+    float p = fmaf(u, 0x1.458fecp-20f, -0x1.0a33f4p-15f);
+    p = fmaf(u, p, 0x1.5d40cap-11f);
+    p = fmaf(u, p, -0x1.c6af52p-7f);
+    p = fmaf(u, p, 0x1.62e43p-2f);
+    const float far = fmaf(-2.0f, __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t)), 1.0f);
+    return fabsf(t) <= 1.5f ? t * p : far;
+}
+
 // The largest of the four lanes m, m + 16, m + 32 and m + 48, in all of them.
 __device__ __forceinline__ float max_over_rows(float v) {
     const uint32_t x = __float_as_uint(v);
@@ -418,10 +431,9 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
                 }
             }
             if (a.cap > 0.0f) {
-                // cap tanh(x / cap) = cap (1 - 2 / (1 + e^(2 x / cap))); factor holds 2 log2(e) / cap
+                // factor holds 2 log2(e) / cap
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    z[i] = a.cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z[i])));
+                for (int i = 0; i < 8; ++i) z[i] = a.cap * tanh_of(z[i]);
             }
             float vs[8];                      // of the values' scales
             if constexpr (INT8) {
@@ -752,7 +764,7 @@ Kernel split_kernel(int dim, bool flat) {
                         : split_kernel<256, INT8>(dim, flat);
 }
 
-// Scores are in units of log2: factor s, or cap (1 - 2 / (1 + 2^(factor s))), with s the
+// Scores are in units of log2: factor s, or cap tanh(factor s ln 2 / 2), with s the
 // product of a query and a key's numbers as they enter the matrix instructions.
 constexpr double LOG2E = 1.4426950408889634;
 float score_factor(const woq_cache* c, float scale, float softcap, int step = STEP) {
@@ -785,6 +797,7 @@ int attn_check(const woq_cache* c, const uint16_t* q, int64_t ldq, int32_t q_hea
         return WOQ_EUNSUPPORTED;
     const int64_t units = max_pages * c->page / 32 + 1, spans = (int64_t)c->heads * ceil_div(q_heads / c->heads, 16);
     if (units > WOQ_ATTN_MAX_TOKENS / (b * spans)) return WOQ_EUNSUPPORTED;
+    if (softcap > WOQ_ATTN_MAX_SOFTCAP) return WOQ_EUNSUPPORTED;
     if (!std::isfinite(score_factor(c, scale, softcap, 24))) return WOQ_EUNSUPPORTED;      // with room above what is used
     if (workspace_bytes < woq_attn_decode_workspace(c, q_heads, b)) return WOQ_EINVAL;
     return WOQ_OK;
