@@ -141,3 +141,37 @@ def test_bounded_scores_of_any_bound(gpu_lib, int8, softcap):
         rel = 2 * ((4 * np.sqrt(D) + 8) * U + 2.0 ** -22) * reach + 2.0 ** -19 + 200 * U
         assert rel < 1e-2
         within(y[r], ref[r], spread[r] * rel + np.abs(ref[r]) * H + SUB, ("row", r))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lens,width", [([1], None), ([40], None), ([300, 1, 77], None), ([300, 1, 77], 150), ([9000], None)])
+def test_values_that_are_infinite(gpu_lib, dim, lens, width):
+    """An infinity among the visible values of an fp16 cache gives infinity, as it
+    does times any weight and in any sum; two of different signs, or a NaN, give NaN;
+    other channels are what they are without it."""
+    case("infinite values", dim, lens)
+    q_heads, page = 4, 16
+    c = Cache(sum(-(-n // page) for n in lens) + 1, 2, page, dim, False, seed=70)
+    rng = np.random.default_rng(71)
+    q = (rng.standard_normal((len(lens), q_heads * dim)) * 0.5).astype(np.float16)
+    pages = tables(rng, c, lens, width=width)
+    plain = attend(c, q_heads, q, pages, lens)
+    want = plain.copy()
+
+    def put(r, t, h, d, x):
+        c.v[pages[r, t // page], h, t % page, d] = x
+
+    for r, n in enumerate(lens):
+        at = rng.permutation(n)
+        put(r, at[0], 0, 3, np.inf)
+        put(r, at[0], 1, 5, -np.inf)
+        put(r, at[-1], 0, 17, np.nan)
+        for t in at[:5]:
+            put(r, t, 1, 40, np.inf)
+        want[r, :2, 3], want[r, 2:, 5], want[r, :2, 17], want[r, 2:, 40] = np.inf, -np.inf, np.nan, np.inf
+        if n > 1:
+            put(r, at[0], 0, dim - 1, np.inf)
+            put(r, at[1], 0, dim - 1, -np.inf)
+            want[r, :2, dim - 1] = np.nan
+    c.upload()
+    np.testing.assert_array_equal(attend(c, q_heads, q, pages, lens), want)

@@ -52,6 +52,19 @@ __device__ __forceinline__ uint32_t codes2(uint32_t u) {
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(as_h2(u), up, offset));
 }
 
+// Two fp16 numbers with +-65504 in place of infinities and NaN, for the product with the
+// second half of a weight: that half may be 0 or negative, and infinity times it would
+// make NaN of what the first half's product has right.  37 rows of up to 6001 over a window
+// of 4096 of fp16 heads of 256 133.7 us without, 134.9 with it.
+__device__ __forceinline__ uint32_t finite2(uint32_t v) {
+    typedef short s2 __attribute__((ext_vector_type(2)));
+    typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+    const s2 most = {0x7BFF, 0x7BFF};
+    const us2 least = {0xFBFF, 0xFBFF};
+    const s2 w = __builtin_elementwise_min(__builtin_bit_cast(s2, v), most);
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(us2, w), least));
+}
+
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
@@ -507,6 +520,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
                     if constexpr (INT8) v = make_uint4(codes2(v.x), codes2(v.y), codes2(v.z), codes2(v.w));
                     f4& o = acc[N * c + x];
                     o = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, v), weights, o, 0, 0, 0);
+                    if constexpr (!INT8) v = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
                     o = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, v), rests, o, 0, 0, 0);
                 }
             }
