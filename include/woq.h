@@ -602,7 +602,7 @@ int woq_cache_read(const woq_cache* c, const int32_t* slots, int64_t n, uint16_t
  * aligned, leading dimensions multiples of 8; q_heads is a multiple of heads.
  * Scores, softmax and sums are fp32; the weights of the values (the softmax's
  * numerators, times the token's scale where there is one) meet them as two fp16
- * halves under a common power of two.  A visible value of an fp16 cache that is
+ * halves under a power of two that goes by the largest of them.  A visible value of an fp16 cache that is
  * infinite makes its channel infinite (NaN where infinities of both signs meet, or where
  * its weight is below 2^-40 of the largest and counts as none), one that is NaN makes it
  * NaN.  y may be q with the

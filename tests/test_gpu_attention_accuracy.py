@@ -175,3 +175,43 @@ def test_values_that_are_infinite(gpu_lib, dim, lens, width):
             want[r, :2, dim - 1] = np.nan
     c.upload()
     np.testing.assert_array_equal(attend(c, q_heads, q, pages, lens), want)
+
+
+@pytest.mark.parametrize("dim,n,width", [(64, 60, None), (128, 700, None), (128, 700, 100), (256, 5000, None)])
+@pytest.mark.parametrize("large,small", [(2.0 ** 9, 2.0 ** -20), (2.0 ** 15, 2.0 ** -15), (2.0 ** 30, 2.0 ** -8),
+                                         (2.0 ** 30, 2.0 ** 8), (2.0 ** -10, 2.0 ** -20)])
+def test_scales_of_values_that_hardly_count(gpu_lib, dim, n, width, large, small):
+    """INT8 values of which the largest by far have next to no weight: what counts are
+    the others, and they keep their bits.  Weights times their scales below 2^-40 of the
+    largest such product may be lost, the rest is as in the sharp scores' test."""
+    case("scales apart", dim, n, width, large, small)
+    q_heads = 8
+    rng = np.random.default_rng(80)
+    c = Cache(-(-n // 16) + 1, 2, 16, dim, True, seed=81)
+    q = rng.standard_normal((1, q_heads, dim)).astype(np.float16)
+    q[0, :, 0] = 8
+    pages = tables(rng, c, [n], width=width)
+    c.vs = (small * rng.uniform(0.5, 1, c.vs.shape)).astype(np.float32)
+    c.k = (128 + np.rint((c.k.astype(float) - 128) / 8)).astype(np.uint8)
+    c.k[..., 0] = 128 + 100                 # all keys share a component along the queries,
+    c.ks[...] = 0.04
+    far = rng.permutation(n)[:max(3, n // 20)]
+    for t in far:                           # but for those, whose weights are 2^-80 and less
+        c.k[pages[0, t // 16], :, t % 16, 0] = 1
+        c.vs[pages[0, t // 16], :, t % 16] = large * rng.uniform(0.5, 1, 2)
+    c.upload()
+    flat, scale = q.reshape(1, -1), 1.0
+    y = attend(c, q_heads, flat, pages, [n], scale=scale)[0]
+    ref, spread = (a[0] for a in exact(c, q_heads, flat, pages, [n], scale))
+    slots = pages[0, np.arange(n) // 16].astype(np.int64) * 16 + np.arange(n) % 16
+    K, sv = c.tokens("k", slots), c.vs[slots // 16, :, slots % 16].astype(np.float64)
+    kn = np.linalg.norm(K, axis=-1).max()
+    for h in range(q_heads):
+        z = K[:, h // 4] @ q[0, h].astype(np.float64) * scale
+        p = np.exp(z - z.max())
+        assert p[far].max() / p.sum() * large < 2.0 ** -20 * small
+        p /= p.sum()
+        lost = n * 2.0 ** -40 * 127 * (p * sv[:, h // 4]).max()
+        rel = 2 * (4 * np.sqrt(dim) + 8) * U * scale * np.linalg.norm(q[0, h].astype(float)) * kn + 2.0 ** -19 + (n / 8 + 200) * U
+        assert rel < 1e-2
+        within(y[h], ref[h], spread[h] * rel + np.abs(ref[h]) * H + SUB + lost, ("head", h))

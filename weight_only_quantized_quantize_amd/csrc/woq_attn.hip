@@ -361,7 +361,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
 #pragma unroll
         for (int i = 0; i < E; ++i) acc[i] = f4{0, 0, 0, 0};
         float top = NONE, sum = 0.0f;
-        int power = -90;                      // INT8: scales of values are below 2^power
+        int power = -90;                      // INT8: weights times their values' scales are below 2^power
 
         Mem t;
         bool there[2];
@@ -476,33 +476,47 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
             for (int i = 1; i < 8; ++i) most = fmaxf(most, z[i]);
             most = max_over_rows(most);
             if (__any(most > top)) {
-                const float next = fmaxf(top, most), keep = __builtin_amdgcn_exp2f(top - (next == NONE ? 0.0f : next));
+                // INT8: what the weights lose the power loses too, in whole steps, so that it goes by the
+                // largest product of weight and scale that still counts, not by a scale whose weight is gone
+                // (one row of 131072 51.2 us for 51.3 by the largest scale alone)
+                const float next = fmaxf(top, most), fall = top - (next == NONE ? 0.0f : next);
+                const int lower = INT8 ? max(-90, power + (int)fmaxf(fall, -300.0f)) : power;
+                const float keep = __builtin_amdgcn_exp2f(fall + (float)(power - lower));
                 top = next;
-                sum *= keep;
+                power = lower;
+                sum *= INT8 ? __builtin_amdgcn_exp2f(fall) : keep;
 #pragma unroll
                 for (int i = 0; i < E; ++i) acc[i] *= keep;
             }
-            if constexpr (INT8) {
-                float large = vs[0];
+            const float ref = (top == NONE ? 0.0f : top) - (INT8 ? 0 : TOP);
+            float x[8];                       // weights, times their values' scales
 #pragma unroll
-                for (int i = 1; i < 8; ++i) large = fmaxf(large, vs[i]);
+            for (int i = 0; i < 8; ++i) {
+                x[i] = __builtin_amdgcn_exp2f(z[i] - ref);
+                sum += x[i];
+                if constexpr (INT8) x[i] *= vs[i];
+            }
+            if constexpr (INT8) {
+                float large = x[0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) large = fmaxf(large, x[i]);
                 if (__any(large >= pow2i(power))) {
                     large = max_over_rows(large);
-                    const int next = min(110, (int)(__builtin_amdgcn_readfirstlane(__float_as_uint(large)) >> 23) - 126);
+                    const int next = max(power, min(110, (int)(__float_as_uint(large) >> 23) - 126));
                     const float keep = pow2i(max(-126, power - next));
                     power = next;
 #pragma unroll
                     for (int i = 0; i < E; ++i) acc[i] *= keep;
                 }
+                const float raise = pow2i(TOP - power);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] *= raise;
             }
-            const float ref = (top == NONE ? 0.0f : top) - (INT8 ? 0 : TOP), raise = pow2i(TOP - power);
             h8 weights, rests;                // a weight's fp16 and what that leaves of it
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float e = __builtin_amdgcn_exp2f(z[i] - ref), x = INT8 ? e * (vs[i] * raise) : e;
-                sum += e;
-                weights[i] = (f16)x;
-                rests[i] = (f16)(x - (float)weights[i]);
+                weights[i] = (f16)x[i];
+                rests[i] = (f16)(x[i] - (float)weights[i]);
             }
             // sums: rows of the product are the channels E (lane % 16) + i
 #pragma unroll
