@@ -567,7 +567,8 @@ typedef struct {
  * is WOQ_EINVAL; rot is a multiple of 16, 16 <= rot <= dim.  fp16 rows are
  * 16-byte aligned with leading dimensions that are multiples of 8; rope is
  * 16-byte aligned.  Tokens of the cache that no slot names keep their values.
- * b * (q_heads + 2 heads) < 2^31; b = 0 is a no-op.
+ * b * (q_heads + 2 heads) is at most (2^32 - 256) / 4 for dim <= 64, / 8 for dim <= 128, /
+ * 16 above (the threads of a launch); b = 0 is a no-op.
  */
 int woq_cache_write(const woq_cache* c, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
                     const int32_t* slots, int64_t b, const uint16_t* q, int64_t ldq, int32_t q_heads, uint16_t* q_out,
@@ -580,7 +581,8 @@ int woq_cache_write(const woq_cache* c, const uint16_t* k, int64_t ldk, const ui
  * values (either may be null): the stored fp16, or fp16(fp32(code * scale)) as
  * woq_embed_int8 restores a row.  A slot outside [0, n_pages * page) gives
  * zeros; slots may repeat.  Rows are 16-byte aligned, leading dimensions
- * multiples of 8.  2 n heads < 2^31; n = 0 is a no-op.
+ * multiples of 8.  2 n heads is bounded as the heads of a written batch are; n = 0 is a
+ * no-op.
  */
 int woq_cache_read(const woq_cache* c, const int32_t* slots, int64_t n, uint16_t* k_out, int64_t ldk,
                    uint16_t* v_out, int64_t ldv, void* stream);

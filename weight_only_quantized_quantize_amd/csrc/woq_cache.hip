@@ -252,9 +252,14 @@ __global__ __launch_bounds__(256) void cache_read_kernel(ReadArgs a) {
     gstore_u4(out + 1, hi);
 }
 
+int lanes_of(int dim) { return dim <= 64 ? 4 : dim <= 128 ? 8 : 16; }
+
+// A launch has fewer than 2^32 threads, whole workgroups of 256.
+int64_t max_items(int dim) { return (int64_t)(UINT32_MAX / 256) * (256 / lanes_of(dim)); }
+
 template <class K, class A>
 int launch(K k4, K k8, K k16, int dim, uint32_t items, A& args, void* stream) {
-    const int L = dim <= 64 ? 4 : dim <= 128 ? 8 : 16;
+    const int L = lanes_of(dim);
     const void* f = reinterpret_cast<const void*>(L == 4 ? k4 : L == 8 ? k8 : k16);
     void* argv[] = {&args};
     const uint32_t per = 256 / L;
@@ -312,7 +317,7 @@ int cache_write_check(const woq_cache* c, const uint16_t* k, int64_t ldk, const 
         (rope && (!aligned16(rope) || ((uintptr_t)pos & 3u))))
         return WOQ_EALIGN;
     const int64_t per_row = 2 * (int64_t)c->heads + (q ? q_heads : 0);
-    if ((rope && (rot & 15)) || b > INT32_MAX / per_row) return WOQ_EUNSUPPORTED;
+    if ((rope && (rot & 15)) || b > max_items(c->dim) / per_row) return WOQ_EUNSUPPORTED;
     return WOQ_OK;
 }
 
@@ -364,7 +369,7 @@ extern "C" int woq_cache_read(const woq_cache* c, const int32_t* slots, int64_t 
     if (n == 0) return WOQ_OK;
     if ((k_out && !half_rows_ok(k_out, ldk)) || (v_out && !half_rows_ok(v_out, ldv)) || ((uintptr_t)slots & 3u))
         return WOQ_EALIGN;
-    if (n > INT32_MAX / (2 * (int64_t)c->heads)) return WOQ_EUNSUPPORTED;
+    if (n > max_items(c->dim) / (2 * (int64_t)c->heads)) return WOQ_EUNSUPPORTED;
     ReadArgs a;
     a.c[0] = static_cast<const uint8_t*>(c->k);
     a.c[1] = static_cast<const uint8_t*>(c->v);
