@@ -558,9 +558,8 @@ typedef struct {
  * with cos = rope[pos[r] * rot + i], sin = rope[pos[r] * rot + rot / 2 + i]
  * (fp32 [n_pos][rot] in device memory), a and b the values i and i + rot / 2 of
  * the head, or 2 i and 2 i + 1 where interleaved is 1.  The turned q goes to
- * q_out as fp16, which may be q with the same leading dimension.  q, k and v of
- * a row whose position lies outside [0, n_pos) become NaN where the rotation
- * would read the table.  INT8: scale = fp32(max |v| / 127) over the head's
+ * q_out as fp16, which may be q with the same leading dimension.  The turned
+ * values of q and k of a row whose position lies outside [0, n_pos) become NaN.  INT8: scale = fp32(max |v| / 127) over the head's
  * values, code = clamp(rne(fp32(v / scale)), +-127), bit for bit
  * woq_quantize_int8 of the (turned) values; a head of zeros has scale 0 and
  * codes 0, one with a NaN or an infinity scale NaN and codes 0.  q without rope
@@ -604,14 +603,18 @@ int woq_cache_read(const woq_cache* c, const int32_t* slots, int64_t n, uint16_t
  * aligned, leading dimensions multiples of 8; q_heads is a multiple of heads.
  * Scores, softmax and sums are fp32; the weights of the values (the softmax's
  * numerators, times the token's scale where there is one) meet them as two fp16
- * halves under a power of two that goes by the largest of them.  A visible value of an fp16 cache that is
- * infinite makes its channel infinite (NaN where infinities of both signs meet, or where
- * its weight is below 2^-40 of the largest and counts as none), one that is NaN makes it
- * NaN.  y may be q with the
- * same leading dimension.  workspace: at least woq_attn_decode_workspace bytes of device memory,
- * 16-byte aligned, owned by the caller, its contents on return unspecified;
- * calls that share it must not overlap.  Deterministic for given inputs on one
- * device model.  q_heads <= WOQ_ATTN_MAX_HEADS, b <= WOQ_ATTN_MAX_ROWS,
+ * halves under a power of two that goes by the largest of them, row by row and head
+ * by head.  A visible value of an fp16 cache that is infinite makes its channel
+ * infinite (NaN where infinities of both signs meet, or where its weight is below
+ * 2^-40 of the largest and counts as none), one that is NaN makes it NaN.  y may be q
+ * with the same leading dimension.  workspace: at least woq_attn_decode_workspace
+ * bytes of device memory, 16-byte aligned, owned by the caller, its contents on return
+ * unspecified; calls that share it must not overlap.  Deterministic for given inputs
+ * on one device model; the other rows of a batch and the width of the table decide how
+ * a row's sums are divided, so its last bit may be another beside other rows.  One
+ * launch or two (the second joins) goes by b, the heads and max_pages, not by lens:
+ * where the rows are far shorter than the table, fewer max_pages with the same ldpages
+ * can be faster or slower.  q_heads <= WOQ_ATTN_MAX_HEADS, b <= WOQ_ATTN_MAX_ROWS,
  * max_pages * page <= WOQ_ATTN_MAX_TOKENS, and b * heads * ceil(q_heads / heads / 16)
  * * (max_pages * page / 32 + 1) too; softcap <= WOQ_ATTN_MAX_SOFTCAP, below which no
  * score is too small for fp32 when it is divided by it; 2^24 log2(e) scale, times 2 /
@@ -755,7 +758,8 @@ typedef struct {
  * step runs.  slots, pos, pages and lens are of the batch: every layer's cache is
  * paged alike, and lens count the new tokens.  attn holds an entry for every step.
  * The two calls' limits hold for every such step (the output 16-byte aligned, N a
- * multiple of 8), and everything is checked before the first launch.  workspace:
+ * multiple of 8) and are checked before the first launch; the products check their own
+ * arguments as they are launched, as in woq_stack_run.  workspace:
  * woq_stack_attn_workspace bytes, owned by the caller; runs that share it, or the
  * runner, must not overlap.
  */

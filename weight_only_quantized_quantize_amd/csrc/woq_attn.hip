@@ -4,10 +4,10 @@
 //   y = sum_t e^(z[t] - m) v[t] / sum_t e^(z[t] - m),   m = max_t z[t].
 //
 // Bound by the cache's bytes at many tokens (64 rows of up to 8192, 64 queries over 8
-// heads of 128, INT8: 98 us, 5.7 TB/s of 6.84 that a bare read reaches; 37 rows of a
-// window of 4096 over fp16 heads of 256: 131 us, 5.9 TB/s; one row of 131072: 51 us,
+// heads of 128, INT8: 99 us, 5.6 TB/s of 6.84 that a bare read reaches; 37 rows of a
+// window of 4096 over fp16 heads of 256: 134 us, 5.8 TB/s; one row of 131072: 51 us,
 // 5.5 TB/s) and by dependent round trips at few (lengths, pages, keys; one row of 509:
-// 8.6 us).  One pass over the tokens, a wave 32 of them at a time with the running
+// 9.0 us).  One pass over the tokens, a wave 32 of them at a time with the running
 // maximum and sum of the softmax, every query head of a key head at once: the scores of
 // 16 tokens are one tile of the fp16 matrix cores, tokens as rows, and leave each lane
 // with eight tokens of one head, the operand of the values' product as it stands.
@@ -478,7 +478,8 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 && !(INT8 && FLAT) ? 1 : 2) v
             if (__any(most > top)) {
                 // INT8: what the weights lose the power loses too, in whole steps, so that it goes by the
                 // largest product of weight and scale that still counts, not by a scale whose weight is gone
-                // (one row of 131072 51.2 us for 51.3 by the largest scale alone)
+                // (64 rows of up to 8192 99.2 us for 99.6 by the largest scale alone, over one head of 64, 64 rows of
+                // up to 16000, 46.4 for 45.2)
                 const float next = fmaxf(top, most), fall = top - (next == NONE ? 0.0f : next);
                 const int lower = INT8 ? max(-90, power + (int)fmaxf(fall, -300.0f)) : power;
                 const float keep = __builtin_amdgcn_exp2f(fall + (float)(power - lower));
@@ -752,10 +753,11 @@ int workgroups() { return 2 * woq::compute_units(); }
 // Where the capacity is no more than this and the spans are no more than the
 // workgroups, each takes one whole and there is nothing to join; twice as much where
 // the spans are a quarter to a half of the workgroups.  64 queries over 8 heads of 128,
-// rows of up to 1024: 4 rows 12.8 us against 7.3 + 4.2 and a launch between them, 32
-// rows 14.1 against 15.1 + 4.2, 64 rows 25.6 against 23.0 + 4.2; of up to 2048: 16 rows
-// 21.3 against 14.2 + 4.2, 32 rows 23.0 against 20.7 + 4.2, 64 rows 40.8 against 33.9 +
-// 4.2; 256 rows of up to 512 (2048 spans) 54 against 42 + 4.8.
+// rows of up to 1024: 4 rows 13.8 us against 8.3 + 4.2 and a launch between them, 32
+// rows 14.8 against 15.4 + 3.9, 64 rows 26.6 against 22.3 + 4.8; of up to 2048: 16 rows
+// 22.5 against 14.7 + 4.0, 32 rows 23.4 against 19.8 + 4.2, 64 rows 43 against 34.5 +
+// 4.8; 256 rows of up to 512 (2048 spans) 57 against 43.5 + 4.8.  (From a graph, calls
+// one behind the other: 4 rows 11.9 against 10.5, 32 rows 14.6 against 18.0.)
 constexpr int64_t DIRECT = 1024;
 
 struct Layout {

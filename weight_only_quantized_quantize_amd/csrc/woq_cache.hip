@@ -4,14 +4,14 @@
 //   rotation  (a, b) -> (a cos - b sin, b cos + a sin) for each pair of a head,
 //   INT8      scale = max|v| / 127, byte = rne(v / scale) + 128 per token and head.
 //
-// Bound by memory at many tokens (2047 rows of 16 + 2 x 8 heads of 256 in 17 us, 3.5
-// TB/s; 16381 tokens of 8 heads of 128 read back in 20-24 us, 4.2-5.1 TB/s) and by one
+// Bound by memory at many tokens (2047 rows of 16 + 2 x 8 heads of 256 in 15.5 us, 3.9
+// TB/s; 16381 tokens of 8 heads of 128 read back in 22-25 us, 4.1-4.6 TB/s) and by one
 // launch and two dependent round trips (slot and position with the row, then the
 // angles) at few (one row of 64 + 2 x 8 heads of 128 3.3 us).  A head is held by 4, 8 or
 // 16 lanes, 16 values each, so a wave takes several heads, its maximum is a reduction
 // of two to four steps inside the lanes that hold it, and no value passes through LDS.
 // Four heads to a group of lanes, the angles read once for them, were no faster (17.1
-// us) and slower for few rows (4.9).
+// us where this then took 17) and slower for few rows (4.9).
 #include <hip/hip_runtime.h>
 
 #include "woq_gemv.h"

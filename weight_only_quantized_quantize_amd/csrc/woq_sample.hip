@@ -10,7 +10,7 @@
 //
 // Bound by one compute unit's phases for few rows (one row of 128256 23.6 us: the
 // histogram 8, sums of its bins 2.5, limits 2.8, masses 2.5 to 6, searches 2.9, the
-// place 2.8), by HBM and those in turn for many (256 rows of 256000 56 us, the
+// place 2.8), by HBM and those in turn for many (256 rows of 256000 52 us, the
 // histogram 26 of them at 5.2 TB/s).  A sort would move the row several times, a
 // threshold found in rounds read it several times.
 //
